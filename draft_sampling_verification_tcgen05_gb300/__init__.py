@@ -19,6 +19,8 @@ __all__ = [
     "dspark_verify_greedy", "dspark_verify_logits",
     "dspark_confidence", "dspark_markov_sample_reduced", "dspark_markov_sample_conf", "D2T_INDEX", "D2T_OFFSET", "dspark_draft_logits", "dspark_markov_sample",
     "dspark_verify", "dspark_schedule", "dspark_read_status", "dspark_status_string",
+    "OP_KV_APPEND", "OP_PAGED_ATTENTION", "OP_PROMPT_ATTENTION", "OP_SAMPLE",
+    "dspark_kv_append", "dspark_paged_attention", "dspark_prompt_attention", "dspark_sample",
     "dspark_selftest_wait_timeout", "STATUS_TIMEOUT", "STATUS_NUMERIC", "STATUS_INPUT_RANGE",
     "STATUS_INTERNAL", "STATUS_INDEX",
 ]
@@ -30,7 +32,8 @@ LIB_PATH = os.environ.get("DSPARK_LIBRARY") or os.path.join(os.path.dirname(os.p
 OP_DRAFT_LOGITS, OP_MARKOV_SAMPLE, OP_VERIFY, OP_SCHEDULE, OP_VERIFY_GREEDY, OP_CONFIDENCE = 0, 1, 2, 3, 4, 5
 OP_VERIFY_LOGITS = 6
 OP_VERIFY_GUMBEL = 7
-F32, BF16 = 0, 1
+OP_KV_APPEND, OP_PAGED_ATTENTION, OP_PROMPT_ATTENTION, OP_SAMPLE = 8, 10, 11, 12
+F32, BF16, F16 = 0, 1, 2
 D2T_INDEX, D2T_OFFSET = 0, 1
 OK, ERR_INVALID_ARG, ERR_UNSUPPORTED, ERR_CUDA, ERR_TIMEOUT, ERR_NUMERIC, ERR_INPUT_RANGE = range(7)
 STATUS_TIMEOUT, STATUS_NUMERIC, STATUS_INPUT_RANGE, STATUS_INTERNAL, STATUS_INDEX = 0x1, 0x2, 0x4, 0x8, 0x10
@@ -71,6 +74,14 @@ def lib() -> ctypes.CDLL:
     L.dspark_confidence.argtypes = [vp, i32, vp, i32, vp, vp, vp, vp, ctypes.c_float, vp, i32, i32, i32, i32, i32,
                                     vp, vp, sz, vp]
     L.dspark_schedule.argtypes = [vp, vp, i32, i32, i32, i32, vp, vp, vp, vp, vp, sz, vp]
+    i64, f32 = ctypes.c_longlong, ctypes.c_float
+    L.dspark_kv_append.argtypes = [vp, vp, vp, i32, i64, i64, i64, vp, vp, vp, i32, i32, i32, vp, vp, f32,
+                                   i32, i32, i32, i32, vp, vp, vp, i32, i32, vp, sz, vp]
+    L.dspark_paged_attention.argtypes = [vp, vp, vp, i32, vp, i32, vp, vp, f32, i32, i32, i32, i32, i32, i32, i32, i32,
+                                         vp, vp, vp, sz, vp]
+    L.dspark_prompt_attention.argtypes = [vp, vp, vp, i32, i64, i64, i64, vp, f32, i32, i32, i32, i32, i32, i32,
+                                          vp, vp, vp, sz, vp]
+    L.dspark_sample.argtypes = [vp, i32, vp, vp, vp, vp, vp, i32, i32, vp, vp, vp, sz, vp]
     L.dspark_read_status.argtypes = [vp, u32p, vp]
     L.dspark_status_string.argtypes = [i32]
     L.dspark_status_string.restype = ctypes.c_char_p
@@ -78,6 +89,7 @@ def lib() -> ctypes.CDLL:
     L.dspark_last_error.restype = ctypes.c_char_p
     L.dspark_selftest_wait_timeout.argtypes = [vp, sz, ctypes.c_longlong, vp]
     for f in ("dspark_draft_logits", "dspark_markov_sample", "dspark_verify", "dspark_schedule",
+              "dspark_kv_append", "dspark_paged_attention", "dspark_prompt_attention", "dspark_sample",
               "dspark_read_status", "dspark_selftest_wait_timeout"):
         getattr(L, f).restype = i32
     _lib = L
@@ -418,6 +430,180 @@ def dspark_schedule(cond_accept, sps, K_in: int, survival=None, K_out=None, leng
                                  _ptr(K_out), _ptr(lengths), _ptr(selected), ws.ptr, ws.nbytes,
                                  _stream(stream)), "dspark_schedule")
     return survival, K_out, lengths, selected
+
+
+def _half(t, name):
+    """Library dtype code of a bf16 or fp16 tensor."""
+    torch = _torch()
+    if t.dtype == torch.bfloat16:
+        return BF16
+    if t.dtype == torch.float16:
+        return F16
+    raise TypeError(f"{name} has dtype {t.dtype}, expected torch.bfloat16 or torch.float16")
+
+
+def _rows(t, name, dtype, D):
+    """Checks a [T, H, D] tensor whose heads and values are contiguous; returns its token stride in elements."""
+    torch = _torch()
+    if not isinstance(t, torch.Tensor) or not t.is_cuda:
+        raise TypeError(f"{name} must be a CUDA tensor")
+    if t.dtype != dtype:
+        raise TypeError(f"{name} has dtype {t.dtype}, expected {dtype}")
+    if t.dim() != 3 or t.shape[2] != D:
+        raise ValueError(f"{name} must be [T, H, {D}], got {tuple(t.shape)}")
+    T, H, _ = t.shape
+    token, head, value = t.stride()
+    if (value != 1 and D > 1) or (head != D and H > 1):
+        raise ValueError(f"{name} must have contiguous heads and values (strides {t.stride()})")
+    return token if T > 1 else H * D
+
+
+def dspark_kv_append(q, k, v, positions, slots, cos_sin, k_cache, v_cache, interleaved: bool = False, q_norm=None,
+                     k_norm=None, eps: float = 1e-6, q_out=None, workspace=None, stream=None):
+    """Writes k and v [T, Hkv, D] of new tokens to their slots of a paged cache, the keys (and the queries
+    q [T, Hq, D], or None) normalised (where a weight is given) and rotated; returns q_out [T, Hq, D].
+
+    positions, slots [T] int32 (slot = page * page_size + place; -1: a padding row), cos_sin
+    [max_positions, rot] fp32 (cosines, then sines), k_cache / v_cache [num_pages, Hkv, page_size, D],
+    q_norm / k_norm [D] fp32.  q, k and v may be views of one projection (any token stride).
+    """
+    torch = _torch()
+    if not isinstance(k, torch.Tensor) or k.dim() != 3:
+        raise TypeError("k must be a CUDA tensor [T, Hkv, D]")
+    T, Hkv, D = k.shape
+    dt = _half(k, "k")
+    k_stride, v_stride = _rows(k, "k", k.dtype, D), _rows(v, "v", k.dtype, D)
+    _need(k_cache, "k_cache", (k.dtype,), 4)
+    _need(v_cache, "v_cache", (k.dtype,), 4)
+    _need(positions, "positions", (torch.int32,), 1)
+    _need(slots, "slots", (torch.int32,), 1)
+    _need(cos_sin, "cos_sin", (torch.float32,), 2)
+    num_pages, Hc, page, Dc = k_cache.shape
+    if tuple(v.shape) != (T, Hkv, D) or (Hc, Dc) != (Hkv, D) or v_cache.shape != k_cache.shape \
+            or positions.shape[0] != T or slots.shape[0] != T:
+        raise ValueError("shapes: k / v [T, Hkv, D], caches [num_pages, Hkv, page_size, D], positions / slots [T]")
+    for w, name in ((q_norm, "q_norm"), (k_norm, "k_norm")):
+        if w is not None:
+            _need(w, name, (torch.float32,), 1)
+            if w.shape[0] != D:
+                raise ValueError(f"{name} must be [D]")
+    Hq, q_stride = 0, 0
+    if q is not None:
+        q_stride = _rows(q, "q", k.dtype, D)
+        Hq = q.shape[1]
+        if q.shape[0] != T:
+            raise ValueError("q must be [T, Hq, D] with the tokens of k")
+        if q_out is None:
+            q_out = torch.empty(T, Hq, D, dtype=k.dtype, device=k.device)
+        _need(q_out, "q_out", (k.dtype,), 3)
+        if tuple(q_out.shape) != (T, Hq, D):
+            raise ValueError("q_out must be [T, Hq, D]")
+    ws = _ws(workspace, OP_KV_APPEND, device=k.device)
+    _check(lib().dspark_kv_append(_ptr(q), _ptr(k), _ptr(v), dt, q_stride, k_stride, v_stride, _ptr(positions),
+                                  _ptr(slots), _ptr(cos_sin), cos_sin.shape[0], cos_sin.shape[1], int(interleaved),
+                                  _ptr(q_norm), _ptr(k_norm), eps, T, Hq, Hkv, D, _ptr(q_out), _ptr(k_cache),
+                                  _ptr(v_cache), num_pages, page, ws.ptr, ws.nbytes, _stream(stream)),
+           "dspark_kv_append")
+    return q_out
+
+
+def dspark_paged_attention(q, k_cache, v_cache, block_table, kv_len, scale: float, lengths=None, causal: bool = True,
+                           out=None, lse=None, workspace=None, stream=None):
+    """Attention of a window of N new tokens per request, q [B, N, Hq, D], over a paged cache
+    [num_pages, Hkv, page_size, D] that holds them already; returns out [B, N, Hq, D].
+
+    block_table [B, max_pages], kv_len [B] (cached tokens, the window's among them), lengths [B] (the
+    window's tokens, or None for N) int32.  Pass an fp32 [B, N, Hq] tensor as `lse` to receive the
+    log-sum-exp of each row's scores.
+    """
+    torch = _torch()
+    dt = _half(q, "q")
+    _need(q, "q", (q.dtype,), 4)
+    _need(k_cache, "k_cache", (q.dtype,), 4)
+    _need(v_cache, "v_cache", (q.dtype,), 4)
+    _need(block_table, "block_table", (torch.int32,), 2)
+    _need(kv_len, "kv_len", (torch.int32,), 1)
+    B, N, Hq, D = q.shape
+    num_pages, Hkv, page, Dc = k_cache.shape
+    if Dc != D or v_cache.shape != k_cache.shape or block_table.shape[0] != B or kv_len.shape[0] != B:
+        raise ValueError("shapes: q [B, N, Hq, D], caches [num_pages, Hkv, page_size, D], block_table [B, max_pages], "
+                         "kv_len [B]")
+    if lengths is not None:
+        _need(lengths, "lengths", (torch.int32,), 1)
+        if lengths.shape[0] != B:
+            raise ValueError("lengths must be [B]")
+    if out is None:
+        out = torch.empty_like(q)
+    _need(out, "out", (q.dtype,), 4)
+    if lse is not None:
+        _need(lse, "lse", (torch.float32,), 3)
+    if out.shape != q.shape or (lse is not None and lse.shape != q.shape[:3]):
+        raise ValueError("out must be [B, N, Hq, D] and lse [B, N, Hq]")
+    ws = _ws(workspace, OP_PAGED_ATTENTION, B, N, Hq, D, q.device)
+    _check(lib().dspark_paged_attention(_ptr(q), _ptr(k_cache), _ptr(v_cache), dt, _ptr(block_table),
+                                        block_table.shape[1], _ptr(kv_len), _ptr(lengths), scale, int(causal), B, N,
+                                        Hq, Hkv, D, num_pages, page, _ptr(out), _ptr(lse), ws.ptr, ws.nbytes,
+                                        _stream(stream)), "dspark_paged_attention")
+    return out
+
+
+def dspark_prompt_attention(q, k, v, cu_seqlens, scale: float, causal: bool = True, out=None, lse=None,
+                            workspace=None, stream=None):
+    """Attention within packed prompts: q [T, Hq, D], k / v [T, Hkv, D] (any token stride), sequence b the
+    tokens cu_seqlens[b] to cu_seqlens[b + 1] ([B + 1] int32); returns out [T, Hq, D].
+
+    Pass an fp32 [T, Hq] tensor as `lse` to receive the log-sum-exp of each row's scores.
+    """
+    torch = _torch()
+    if not isinstance(q, torch.Tensor) or q.dim() != 3:
+        raise TypeError("q must be a CUDA tensor [T, Hq, D]")
+    T, Hq, D = q.shape
+    dt = _half(q, "q")
+    q_stride, k_stride, v_stride = _rows(q, "q", q.dtype, D), _rows(k, "k", q.dtype, D), _rows(v, "v", q.dtype, D)
+    _need(cu_seqlens, "cu_seqlens", (torch.int32,), 1)
+    if k.shape != v.shape or k.shape[0] != T:
+        raise ValueError("shapes: q [T, Hq, D], k / v [T, Hkv, D]")
+    if out is None:
+        out = torch.empty(T, Hq, D, dtype=q.dtype, device=q.device)
+    _need(out, "out", (q.dtype,), 3)
+    if lse is not None:
+        _need(lse, "lse", (torch.float32,), 2)
+    if out.shape != q.shape or (lse is not None and lse.shape != q.shape[:2]):
+        raise ValueError("out must be [T, Hq, D] and lse [T, Hq]")
+    B = cu_seqlens.shape[0] - 1
+    ws = _ws(workspace, OP_PROMPT_ATTENTION, B, T, Hq, D, q.device)
+    _check(lib().dspark_prompt_attention(_ptr(q), _ptr(k), _ptr(v), dt, q_stride, k_stride, v_stride, _ptr(cu_seqlens),
+                                         scale, int(causal), B, T, Hq, k.shape[1], D, _ptr(out), _ptr(lse), ws.ptr,
+                                         ws.nbytes, _stream(stream)), "dspark_prompt_attention")
+    return out
+
+
+def dspark_sample(logits, temperature, top_k, top_p, min_p, u, tokens=None, probs=None, workspace=None, stream=None):
+    """Sampling with temperature, top-k, min-p and top-p from the given uniforms u [R]; returns tokens [R] int32.
+
+    logits [R, V] (fp32 or bf16), temperature / top_p / min_p / u [R] fp32, top_k [R] int32 (0: off).  Pass an
+    fp32 [R, V] tensor as `probs` to receive the truncated distributions (dspark_verify's p_target or p_draft).
+    """
+    torch = _torch()
+    _need(logits, "logits", (torch.float32, torch.bfloat16), 2)
+    R, V = logits.shape
+    for t, name in ((temperature, "temperature"), (top_p, "top_p"), (min_p, "min_p"), (u, "u")):
+        _need(t, name, (torch.float32,), 1)
+        if t.shape[0] != R:
+            raise ValueError(f"{name} must be [R]")
+    _need(top_k, "top_k", (torch.int32,), 1)
+    if tokens is None:
+        tokens = torch.empty(R, dtype=torch.int32, device=logits.device)
+    _need(tokens, "tokens", (torch.int32,), 1)
+    if probs is not None:
+        _need(probs, "probs", (torch.float32,), 2)
+    if top_k.shape[0] != R or tokens.shape[0] != R or (probs is not None and probs.shape != logits.shape):
+        raise ValueError("shapes: top_k / tokens [R], probs [R, V]")
+    ws = _ws(workspace, OP_SAMPLE, R, 1, V, 0, logits.device)
+    _check(lib().dspark_sample(_ptr(logits), _dt(logits), _ptr(temperature), _ptr(top_k), _ptr(top_p), _ptr(min_p),
+                               _ptr(u), R, V, _ptr(tokens), _ptr(probs), ws.ptr, ws.nbytes, _stream(stream)),
+           "dspark_sample")
+    return tokens
 
 
 def dspark_read_status(workspace: Workspace, stream=None):

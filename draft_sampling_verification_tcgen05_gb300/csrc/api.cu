@@ -7,6 +7,7 @@
 
 #include <cudaTypedefs.h>
 #include <algorithm>
+#include <cmath>
 #include <mutex>
 #include <stdarg.h>
 #include <stdio.h>
@@ -201,6 +202,12 @@ size_t dspark_workspace_size(int op, int B, int N, int V, int r) {
             return verify_logits_workspace_bytes(B, N, V, r);
         case DSPARK_OP_VERIFY_GUMBEL:
             return verify_gumbel_workspace_bytes(B, N);
+        case DSPARK_OP_KV_APPEND:
+        case DSPARK_OP_PROMPT_ATTENTION:
+        case DSPARK_OP_SAMPLE:
+            return sizeof(WsHeader);
+        case DSPARK_OP_PAGED_ATTENTION:
+            return paged_attention_workspace_bytes(B, N, V, r);
         default:
             return 0;
     }
@@ -433,6 +440,115 @@ dspark_status dspark_schedule(const float* cond_accept, const double* sps, int S
     if (!current_device(&dev)) return DSPARK_ERR_UNSUPPORTED;
     return launch_schedule(cond_accept, sps, S, B, N, K_in, survival, K_out, lengths, selected, workspace,
                            static_cast<cudaStream_t>(stream), dev);
+}
+
+dspark_status dspark_kv_append(const void* q, const void* k, const void* v, dspark_dtype dtype, long long q_stride,
+                               long long k_stride, long long v_stride, const int32_t* positions, const int32_t* slots,
+                               const float* cos_sin, int max_positions, int rot, int interleaved, const float* q_norm,
+                               const float* k_norm, float eps, int T, int Hq, int Hkv, int D, void* q_out,
+                               void* k_cache, void* v_cache, int num_pages, int page, void* workspace, size_t ws_bytes,
+                               void* stream) {
+    g_error[0] = '\0';
+    DSPARK_REQUIRE(k && v && positions && slots && k_cache && v_cache, "kv_append: null pointer");
+    DSPARK_REQUIRE(Hq == 0 || (q && q_out), "kv_append: null q or q_out with Hq = %d", Hq);
+    DSPARK_REQUIRE(rot == 0 || cos_sin, "kv_append: null cos_sin with rot = %d", rot);
+    DSPARK_REQUIRE(dtype == DSPARK_BF16 || dtype == DSPARK_F16, "kv_append: dtype must be bf16 or fp16 (%d)", (int)dtype);
+    DSPARK_REQUIRE(T >= 1 && Hq >= 0 && Hkv >= 1 && Hq <= 65535 && Hkv <= 65535 && D >= 16 && D <= 512 && D % 16 == 0,
+                   "kv_append: bad sizes (T=%d Hq=%d Hkv=%d D=%d)", T, Hq, Hkv, D);
+    DSPARK_REQUIRE(rot >= 0 && rot <= D && rot % 16 == 0 && max_positions >= 1,
+                   "kv_append: rot must be a multiple of 16 in [0, D] (rot=%d D=%d max_positions=%d)", rot, D,
+                   max_positions);
+    DSPARK_REQUIRE(num_pages >= 1 && page >= 1 && static_cast<long long>(num_pages) * page < (1ll << 31),
+                   "kv_append: bad cache (num_pages=%d page=%d)", num_pages, page);
+    DSPARK_REQUIRE(q_stride % 8 == 0 && k_stride % 8 == 0 && v_stride % 8 == 0 &&
+                       (Hq == 0 || q_stride >= static_cast<long long>(Hq) * D) &&
+                       k_stride >= static_cast<long long>(Hkv) * D && v_stride >= static_cast<long long>(Hkv) * D,
+                   "kv_append: token strides must be multiples of 8 and at least a row (%lld %lld %lld)", q_stride,
+                   k_stride, v_stride);
+    DSPARK_REQUIRE(q_out != q || Hq == 0 || q_stride == static_cast<long long>(Hq) * D,
+                   "kv_append: q_out may be q only where q is contiguous");
+    DSPARK_REQUIRE(aligned(q, 16) && aligned(k, 16) && aligned(v, 16) && aligned(q_out, 16) && aligned(k_cache, 16) &&
+                       aligned(v_cache, 16) && aligned(cos_sin, 16),
+                   "kv_append: tensors must be 16-byte aligned");
+    if (bad_ws(workspace, ws_bytes, sizeof(WsHeader))) return DSPARK_ERR_INVALID_ARG;
+    DeviceInfo dev;
+    if (!current_device(&dev)) return DSPARK_ERR_UNSUPPORTED;
+    return launch_kv_append(q, k, v, dtype, q_stride, k_stride, v_stride, positions, slots, cos_sin, max_positions, rot,
+                            interleaved, q_norm, k_norm, eps, T, Hq, Hkv, D, q_out, k_cache, v_cache, num_pages, page,
+                            workspace, static_cast<cudaStream_t>(stream), dev);
+}
+
+dspark_status dspark_paged_attention(const void* q, const void* k_cache, const void* v_cache, dspark_dtype dtype,
+                                     const int32_t* block_table, int max_pages, const int32_t* kv_len,
+                                     const int32_t* lengths, float scale, int causal, int B, int N, int Hq, int Hkv,
+                                     int D, int num_pages, int page, void* out, float* lse, void* workspace,
+                                     size_t ws_bytes, void* stream) {
+    g_error[0] = '\0';
+    DSPARK_REQUIRE(q && k_cache && v_cache && block_table && kv_len && out, "paged_attention: null pointer");
+    DSPARK_REQUIRE(dtype == DSPARK_BF16 || dtype == DSPARK_F16, "paged_attention: dtype must be bf16 or fp16 (%d)",
+                   (int)dtype);
+    DSPARK_REQUIRE(B >= 1 && B <= 65535 && N >= 1 && N <= 65535 && Hkv >= 1 && Hq >= Hkv && Hq % Hkv == 0 &&
+                       Hq / Hkv <= 128 && Hq <= 65535,
+                   "paged_attention: bad sizes (B=%d N=%d Hq=%d Hkv=%d)", B, N, Hq, Hkv);
+    DSPARK_REQUIRE(D == 64 || D == 128, "paged_attention: D must be 64 or 128 (%d)", D);
+    DSPARK_REQUIRE(page >= 8 && page <= 256 && (page & (page - 1)) == 0,
+                   "paged_attention: page must be a power of two from 8 to 256 (%d)", page);
+    DSPARK_REQUIRE(num_pages >= 1 && max_pages >= 1 && static_cast<long long>(max_pages) * page < (1ll << 31) &&
+                       static_cast<long long>(num_pages) * page < (1ll << 31),
+                   "paged_attention: bad cache (num_pages=%d max_pages=%d page=%d)", num_pages, max_pages, page);
+    DSPARK_REQUIRE(std::isfinite(scale), "paged_attention: scale must be finite");
+    DSPARK_REQUIRE(aligned(q, 16) && aligned(k_cache, 16) && aligned(v_cache, 16) && aligned(out, 16),
+                   "paged_attention: q, the caches and out must be 16-byte aligned");
+    if (bad_ws(workspace, ws_bytes, paged_attention_workspace_bytes(B, N, Hq, D))) return DSPARK_ERR_INVALID_ARG;
+    DeviceInfo dev;
+    if (!current_device(&dev)) return DSPARK_ERR_UNSUPPORTED;
+    return launch_paged_attention(q, k_cache, v_cache, dtype, block_table, max_pages, kv_len, lengths, scale, causal, B,
+                                  N, Hq, Hkv, D, num_pages, page, out, lse, workspace,
+                                  static_cast<cudaStream_t>(stream), dev);
+}
+
+dspark_status dspark_prompt_attention(const void* q, const void* k, const void* v, dspark_dtype dtype,
+                                      long long q_stride, long long k_stride, long long v_stride,
+                                      const int32_t* cu_seqlens, float scale, int causal, int B, int T, int Hq,
+                                      int Hkv, int D, void* out, float* lse, void* workspace, size_t ws_bytes,
+                                      void* stream) {
+    g_error[0] = '\0';
+    DSPARK_REQUIRE(q && k && v && cu_seqlens && out, "prompt_attention: null pointer");
+    DSPARK_REQUIRE(dtype == DSPARK_BF16 || dtype == DSPARK_F16, "prompt_attention: dtype must be bf16 or fp16 (%d)",
+                   (int)dtype);
+    DSPARK_REQUIRE(B >= 1 && B <= 65535 && T >= 1 && T <= (1 << 24) && Hkv >= 1 && Hq >= Hkv && Hq % Hkv == 0 &&
+                       Hq / Hkv <= 128 && Hq <= 65535,
+                   "prompt_attention: bad sizes (B=%d T=%d Hq=%d Hkv=%d)", B, T, Hq, Hkv);
+    DSPARK_REQUIRE(D == 64 || D == 128, "prompt_attention: D must be 64 or 128 (%d)", D);
+    DSPARK_REQUIRE(q_stride % 8 == 0 && k_stride % 8 == 0 && v_stride % 8 == 0 &&
+                       q_stride >= static_cast<long long>(Hq) * D && k_stride >= static_cast<long long>(Hkv) * D &&
+                       v_stride >= static_cast<long long>(Hkv) * D && q_stride < (1ll << 31) &&
+                       k_stride < (1ll << 31) && v_stride < (1ll << 31),
+                   "prompt_attention: token strides must be multiples of 8, at least a row and below 2^31 "
+                   "(%lld %lld %lld)", q_stride, k_stride, v_stride);
+    DSPARK_REQUIRE(std::isfinite(scale), "prompt_attention: scale must be finite");
+    DSPARK_REQUIRE(aligned(q, 16) && aligned(k, 16) && aligned(v, 16) && aligned(out, 16),
+                   "prompt_attention: q, k, v and out must be 16-byte aligned");
+    if (bad_ws(workspace, ws_bytes, sizeof(WsHeader))) return DSPARK_ERR_INVALID_ARG;
+    DeviceInfo dev;
+    if (!current_device(&dev)) return DSPARK_ERR_UNSUPPORTED;
+    return launch_prompt_attention(q, k, v, dtype, q_stride, k_stride, v_stride, cu_seqlens, scale, causal, B, T, Hq,
+                                   Hkv, D, out, lse, workspace, static_cast<cudaStream_t>(stream), dev);
+}
+
+dspark_status dspark_sample(const void* logits, dspark_dtype dtype, const float* temperature, const int32_t* top_k,
+                            const float* top_p, const float* min_p, const float* u, int R, int V, int32_t* tokens,
+                            float* probs, void* workspace, size_t ws_bytes, void* stream) {
+    g_error[0] = '\0';
+    DSPARK_REQUIRE(logits && temperature && top_k && top_p && min_p && u && tokens, "sample: null pointer");
+    DSPARK_REQUIRE(dtype == DSPARK_F32 || dtype == DSPARK_BF16, "sample: dtype must be fp32 or bf16 (%d)", (int)dtype);
+    DSPARK_REQUIRE(R >= 1 && V >= 1 && V <= (1 << 21), "sample: bad sizes (R=%d V=%d)", R, V);
+    DSPARK_REQUIRE(aligned(logits, 16) && aligned(probs, 16), "sample: logits and probs must be 16-byte aligned");
+    if (bad_ws(workspace, ws_bytes, sizeof(WsHeader))) return DSPARK_ERR_INVALID_ARG;
+    DeviceInfo dev;
+    if (!current_device(&dev)) return DSPARK_ERR_UNSUPPORTED;
+    return launch_sample(logits, dtype, temperature, top_k, top_p, min_p, u, R, V, tokens, probs, workspace,
+                         static_cast<cudaStream_t>(stream), dev);
 }
 
 dspark_status dspark_read_status(const void* workspace, uint32_t* bits, void* stream) {

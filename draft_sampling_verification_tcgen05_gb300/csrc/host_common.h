@@ -85,6 +85,30 @@ dspark_status launch_schedule(const float* cond_accept, const double* sps, int S
                               int32_t* selected, void* ws, cudaStream_t stream,
                               const DeviceInfo& dev);
 
+dspark_status launch_kv_append(const void* q, const void* k, const void* v, dspark_dtype dtype, long long q_stride,
+                               long long k_stride, long long v_stride, const int32_t* positions, const int32_t* slots,
+                               const float* cos_sin, int max_positions, int rot, int interleaved, const float* q_norm,
+                               const float* k_norm, float eps, int T, int Hq, int Hkv, int D, void* q_out,
+                               void* k_cache, void* v_cache, int num_pages, int page, void* ws, cudaStream_t stream,
+                               const DeviceInfo& dev);
+
+size_t paged_attention_workspace_bytes(int B, int N, int Hq, int D);
+dspark_status launch_paged_attention(const void* q, const void* k_cache, const void* v_cache, dspark_dtype dtype,
+                                     const int32_t* block_table, int max_pages, const int32_t* kv_len,
+                                     const int32_t* lengths, float scale, int causal, int B, int N, int Hq, int Hkv,
+                                     int D, int num_pages, int page, void* out, float* lse, void* ws,
+                                     cudaStream_t stream, const DeviceInfo& dev);
+
+dspark_status launch_prompt_attention(const void* q, const void* k, const void* v, dspark_dtype dtype,
+                                      long long q_stride, long long k_stride, long long v_stride,
+                                      const int32_t* cu_seqlens, float scale, int causal, int B, int T, int Hq,
+                                      int Hkv, int D, void* out, float* lse, void* ws, cudaStream_t stream,
+                                      const DeviceInfo& dev);
+
+dspark_status launch_sample(const void* logits, dspark_dtype dtype, const float* temperature, const int32_t* top_k,
+                            const float* top_p, const float* min_p, const float* u, int R, int V, int32_t* tokens,
+                            float* probs, void* ws, cudaStream_t stream, const DeviceInfo& dev);
+
 dspark_status launch_wait_selftest(void* ws, long long timeout_ns, cudaStream_t stream);
 
 }  // namespace dspark

@@ -63,7 +63,8 @@ typedef enum {
     DSPARK_ERR_INPUT_RANGE = 6    /* a token id, length or probability out of range  */
 } dspark_status;
 
-typedef enum { DSPARK_F32 = 0, DSPARK_BF16 = 1 } dspark_dtype;
+/* DSPARK_F16 is taken by the serving operators only (dspark_kv_append and the attentions). */
+typedef enum { DSPARK_F32 = 0, DSPARK_BF16 = 1, DSPARK_F16 = 2 } dspark_dtype;
 
 typedef enum {
     DSPARK_OP_DRAFT_LOGITS = 0,
@@ -73,7 +74,12 @@ typedef enum {
     DSPARK_OP_VERIFY_GREEDY = 4,
     DSPARK_OP_CONFIDENCE = 5,
     DSPARK_OP_VERIFY_LOGITS = 6,
-    DSPARK_OP_VERIFY_GUMBEL = 7
+    DSPARK_OP_VERIFY_GUMBEL = 7,
+    DSPARK_OP_KV_APPEND = 8,
+    /* 9 is no operation */
+    DSPARK_OP_PAGED_ATTENTION = 10,
+    DSPARK_OP_PROMPT_ATTENTION = 11,
+    DSPARK_OP_SAMPLE = 12
 } dspark_op;
 
 /*
@@ -108,6 +114,11 @@ typedef enum {
  *   DSPARK_OP_CONFIDENCE    256 (the status word)
  *   DSPARK_OP_VERIFY_LOGITS grows with B*V/2048 (normaliser partials); N = gamma
  *   DSPARK_OP_VERIFY_GUMBEL grows with B*(N+1) (row keys); N = gamma
+ *   DSPARK_OP_KV_APPEND     256 (the status word)
+ *   DSPARK_OP_PAGED_ATTENTION  partial results of split requests and their counters;
+ *                           B, N as the call's, V = Hq, r = D
+ *   DSPARK_OP_PROMPT_ATTENTION 256 (the status word)
+ *   DSPARK_OP_SAMPLE        256 (the status word)
  * Returns 0 for an unknown op or negative sizes.
  */
 DSPARK_API size_t dspark_workspace_size(int op, int B, int N, int V, int r);
@@ -501,6 +512,144 @@ DSPARK_API dspark_status dspark_schedule_noalloc(const float* cond_accept, const
                                                  int B, int N, int K_in,
                                                  float* survival, int32_t* K_out, int32_t* lengths,
                                                  int32_t* selected, void* stream);
+
+/*
+ * Appending new tokens to a paged key-value cache, with the position rotation on the way.
+ *
+ * "DSpark implementation and evaluation" §4 (the context-KV precompute: per-head RMS norm of the
+ * keys, rotary embedding, cache writes), for the queries of the same tokens as well:
+ *     x'  = x * rsqrt(mean(x^2) + eps) * weight           (where a weight is given)
+ *     (a, b) -> (a cos - b sin, b cos + a sin)             over the head's first `rot` values
+ *     q_out[t, h]                      = R(positions[t]) q'[t, h]
+ *     k_cache[slot / page, h, slot % page] = R(positions[t]) k'[t, h],   slot = slots[t]
+ *     v_cache[slot / page, h, slot % page] = v[t, h]
+ * The pairs (a, b) are (x[i], x[i + rot/2]), or with `interleaved` (x[2i], x[2i + 1]).
+ * Everything between the loads and the one rounding at the store is fp32.
+ *
+ *   q, k, v      [T, Hq, D], [T, Hkv, D], [T, Hkv, D] dtype (bf16 or fp16), device; tokens are
+ *                q_stride, k_stride, v_stride elements apart (views of a fused projection), heads
+ *                and values contiguous.  q may be NULL with Hq = 0.
+ *   positions    [T] int32 in [0, max_positions), device
+ *   slots        [T] int32 in [0, num_pages * page), or -1: a padding row, whose key and value are
+ *                not written (its q_out row is); slots other than -1 differ from each other, device
+ *   cos_sin      [max_positions, rot] fp32, device: rot/2 cosines, then rot/2 sines
+ *   q_norm, k_norm  [D] fp32, device, or NULL: no norm
+ *   q_out        [T, Hq, D] dtype output, contiguous; may be q itself when q is contiguous
+ *   k_cache, v_cache  [num_pages, Hkv, page, D] dtype, device, updated in place
+ * Requirements: T >= 1, Hq >= 0, Hkv >= 1, D a multiple of 16 up to 512, rot a multiple of 16 in
+ * [0, D], page >= 1, num_pages * page < 2^31; q, k, v, q_out, the caches and cos_sin 16-byte
+ * aligned, strides multiples of 8 and at least a token's row.
+ * Device-side: a position or slot out of range sets INPUT_RANGE; the token's key and value are
+ * not written, and its q_out row is zero where the position is out of range.
+ * workspace: >= dspark_workspace_size(DSPARK_OP_KV_APPEND, ...) bytes.
+ */
+DSPARK_API dspark_status dspark_kv_append(const void* q, const void* k, const void* v, dspark_dtype dtype,
+                               long long q_stride, long long k_stride, long long v_stride,
+                               const int32_t* positions, const int32_t* slots,
+                               const float* cos_sin, int max_positions, int rot, int interleaved,
+                               const float* q_norm, const float* k_norm, float eps,
+                               int T, int Hq, int Hkv, int D,
+                               void* q_out, void* k_cache, void* v_cache, int num_pages, int page,
+                               void* workspace, size_t ws_bytes, void* stream);
+
+/*
+ * Attention of a window of new tokens per request over a paged key-value cache.
+ *
+ * The target's verification pass ("Speculative decoding: from zero to DSpark" §2: the drafted
+ * block scored in one pass), its single-token decode (N = 1) and the draft backbone's block
+ * ("DSpark implementation and evaluation" §4: N query tokens, non-causal over the context KV).
+ * Request b holds kv_len[b] cached tokens, the window's own n = lengths[b] (or N) last among
+ * them; query row i < n sees the first
+ *     limit = kv_len[b] - n + i + 1   (causal)        kv_len[b]   (not causal)
+ * tokens.  With s_j = scale * q_i . k_j over those tokens,
+ *     lse = log sum_j exp(s_j),    out_i = sum_j exp(s_j - lse) v_j.
+ * Query head h reads key head h / (Hq / Hkv).  A row that sees nothing (i >= n, or limit <= 0)
+ * gives out 0 and lse -infinity.  Values in the cache that a row does not see do not reach its
+ * output, infinities and NaN among them.
+ * Scores, statistics and sums are fp32; the weights exp(s_j - max) are rounded to dtype for their
+ * product with v.
+ *
+ *   q            [B, N, Hq, D] dtype (bf16 or fp16), device
+ *   k_cache, v_cache  [num_pages, Hkv, page, D] dtype, device
+ *   block_table  [B, max_pages] int32, device: token j of request b is in page
+ *                block_table[b, j / page]; entries past a request's pages are not read
+ *   kv_len       [B] int32 in [0, max_pages * page], device
+ *   lengths      [B] int32 in [0, N], device, or NULL (= N)
+ *   out          [B, N, Hq, D] dtype output
+ *   lse          [B, N, Hq] fp32 output, or NULL
+ * Requirements: B, N >= 1, B <= 65535, N <= 65535, Hkv >= 1, Hq a multiple of Hkv with
+ * Hq / Hkv <= 128, D 64 or 128, page a power of two from 8 to 256, scale finite; q, k_cache,
+ * v_cache, out 16-byte aligned.
+ * Device-side: a kv_len or length out of range sets INPUT_RANGE and the request's rows are as
+ * rows that see nothing; a page out of [0, num_pages) sets INPUT_RANGE and is read as page 0.
+ * workspace: >= dspark_workspace_size(DSPARK_OP_PAGED_ATTENTION, B, N, Hq, D).
+ */
+DSPARK_API dspark_status dspark_paged_attention(const void* q, const void* k_cache, const void* v_cache,
+                               dspark_dtype dtype, const int32_t* block_table, int max_pages,
+                               const int32_t* kv_len, const int32_t* lengths, float scale, int causal,
+                               int B, int N, int Hq, int Hkv, int D, int num_pages, int page,
+                               void* out, float* lse, void* workspace, size_t ws_bytes, void* stream);
+
+/*
+ * Attention within packed prompts of different lengths.
+ *
+ * The prompt's pass that fills the context KV ("DSpark implementation and evaluation" §4).
+ * Sequence b is the tokens [cu_seqlens[b], cu_seqlens[b + 1]); with `causal` a token sees the
+ * tokens of its sequence up to itself, without it all of them.  out, lse, the heads' grouping,
+ * the precision and the guarantee about values that a row does not see are
+ * dspark_paged_attention's.  Tokens outside every sequence give out 0 and lse -infinity.
+ *
+ *   q, k, v      [T, Hq, D], [T, Hkv, D], [T, Hkv, D] dtype (bf16 or fp16), device; tokens are
+ *                q_stride, k_stride, v_stride elements apart (views of a fused projection), heads
+ *                and values contiguous
+ *   cu_seqlens   [B + 1] int32, device, non-decreasing in [0, T]
+ *   out          [T, Hq, D] dtype output, contiguous
+ *   lse          [T, Hq] fp32 output, or NULL
+ * Requirements: B, T >= 1, B <= 65535, T <= 2^24, Hkv >= 1, Hq a multiple of Hkv with
+ * Hq / Hkv <= 128, D 64 or 128, scale finite; q, k, v, out 16-byte aligned, strides multiples of
+ * 8, at least a token's row and below 2^31.
+ * Device-side: an entry of cu_seqlens out of [0, T] or below one before it sets INPUT_RANGE and is
+ * read as the nearest value that is neither.
+ * workspace: >= dspark_workspace_size(DSPARK_OP_PROMPT_ATTENTION, B, T, Hq, D).
+ */
+DSPARK_API dspark_status dspark_prompt_attention(const void* q, const void* k, const void* v, dspark_dtype dtype,
+                               long long q_stride, long long k_stride, long long v_stride,
+                               const int32_t* cu_seqlens, float scale, int causal,
+                               int B, int T, int Hq, int Hkv, int D,
+                               void* out, float* lse, void* workspace, size_t ws_bytes, void* stream);
+
+/*
+ * Sampling with temperature, top-k, min-p and top-p from given uniforms, and the truncated
+ * distribution itself (what dspark_verify takes as p_target or p_draft when requests bring these
+ * settings: the rejection rule stays lossless for whatever distributions it is given).
+ *
+ * Row r, with m its largest logit and T = temperature[r]:
+ *     w_v = expf((x_v - m) * (1 / T)) in fp32,   q_v = floor(w_v * 2^40)
+ * Entries are ordered by logit, the largest first, equal ones by id.  Kept are the first top_k of
+ * them (all for top_k <= 0) with w_v >= min_p; of those, with Q their mass (the sum of q), the
+ * ones whose mass before them in the order is below floor(Q * P / 2^24), P = floor(top_p * 2^24),
+ * and always the first.  With Q' the mass of what is left and t = floor(Q' * U / 2^24),
+ * U = floor(u * 2^24), the token is the smallest id whose inclusive prefix mass, over ids, exceeds
+ * t.  All sums are integers, so the result depends on no order of summation.  T = 0 is greedy: the
+ * first of the order.
+ *     probs[r, v] = w_v / (Q' * 2^-40) where v is left and q_v > 0, else 0.
+ *
+ *   logits       [R, V] dtype (fp32 or bf16), device
+ *   temperature  [R] fp32 >= 0;  top_k [R] int32;  top_p [R] fp32 in [0, 1];
+ *   min_p        [R] fp32 in [0, 1];  u [R] fp32 in [0, 1), device
+ *   tokens       [R] int32 output
+ *   probs        [R, V] fp32 output, or NULL
+ * Requirements: R >= 1, 1 <= V <= 2^21; logits and probs 16-byte aligned.
+ * Device-side: entries that are -infinity are masked (weight 0); NaN and +infinity are skipped and
+ * set NUMERIC; a row without a finite entry gives token 0, probs 0 and NUMERIC.  A negative or
+ * non-finite temperature sets NUMERIC and is read as 0.  A top_p, min_p or u out of its range sets
+ * INPUT_RANGE and is read as the nearest value in it (NaN: 1, 0 and 0).
+ * workspace: >= dspark_workspace_size(DSPARK_OP_SAMPLE, ...) bytes.
+ */
+DSPARK_API dspark_status dspark_sample(const void* logits, dspark_dtype dtype, const float* temperature,
+                               const int32_t* top_k, const float* top_p, const float* min_p,
+                               const float* u, int R, int V, int32_t* tokens, float* probs,
+                               void* workspace, size_t ws_bytes, void* stream);
 
 /*
  * Synchronises `stream`, reads the status word of `workspace` written by the

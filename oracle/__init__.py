@@ -10,7 +10,8 @@ from the pages that define the method, each function citing its passage:
 
   * "DSpark implementation and evaluation" (ggaaooppeenngg.github.io):
     §2.2 Sequential Markov Sampling, §3 Markov Head structure, §4 draft step,
-    §5 reduced draft vocabulary and verification with the draft's Gumbel noise.
+    §5 reduced draft vocabulary and verification with the draft's Gumbel noise;
+    §4 also for the operators around the backbone's attention.
   * "Speculative decoding: from zero to DSpark" (bittide.aicompass.dev):
     §2 the loop and its lossless property, §6 scheduling by expected
     throughput and the calibrated confidence head, §7 running in a real engine.
@@ -34,6 +35,9 @@ from .greedy import verify_greedy, row_argmax
 from .confidence import confidence
 from .reduced_vocab import map_to_target, markov_sample_reduced
 from .verify_logits import verify_from_logits, draft_distributions, draft_lse, residual_gumbel
+from .attention import attend_row, paged_attention, prompt_attention
+from .kv_append import kv_append, rms_norm, rotate
+from .sample import sample_row, truncated_distribution, weights
 from .verify_gumbel import verify_gumbel, target_gumbel_tokens
 
 __all__ = [
@@ -44,4 +48,6 @@ __all__ = [
     "verify_greedy", "row_argmax", "confidence", "map_to_target", "markov_sample_reduced",
     "verify_from_logits", "draft_distributions", "draft_lse", "residual_gumbel",
     "verify_gumbel", "target_gumbel_tokens",
+    "attend_row", "paged_attention", "prompt_attention", "kv_append", "rms_norm", "rotate",
+    "sample_row", "truncated_distribution", "weights",
 ]
