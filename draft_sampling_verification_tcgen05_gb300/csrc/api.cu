@@ -493,7 +493,7 @@ dspark_status dspark_paged_attention(const void* q, const void* k_cache, const v
     DSPARK_REQUIRE(D == 64 || D == 128, "paged_attention: D must be 64 or 128 (%d)", D);
     DSPARK_REQUIRE(page >= 8 && page <= 256 && (page & (page - 1)) == 0,
                    "paged_attention: page must be a power of two from 8 to 256 (%d)", page);
-    DSPARK_REQUIRE(num_pages >= 1 && max_pages >= 1 && static_cast<long long>(max_pages) * page < (1ll << 31) &&
+    DSPARK_REQUIRE(num_pages >= 1 && max_pages >= 1 && static_cast<long long>(max_pages) * page <= (1ll << 30) &&
                        static_cast<long long>(num_pages) * page < (1ll << 31),
                    "paged_attention: bad cache (num_pages=%d max_pages=%d page=%d)", num_pages, max_pages, page);
     DSPARK_REQUIRE(std::isfinite(scale), "paged_attention: scale must be finite");

@@ -578,8 +578,9 @@ DSPARK_API dspark_status dspark_kv_append(const void* q, const void* k, const vo
  *   out          [B, N, Hq, D] dtype output
  *   lse          [B, N, Hq] fp32 output, or NULL
  * Requirements: B, N >= 1, B <= 65535, N <= 65535, Hkv >= 1, Hq a multiple of Hkv with
- * Hq / Hkv <= 128, D 64 or 128, page a power of two from 8 to 256, scale finite; q, k_cache,
- * v_cache, out 16-byte aligned.
+ * Hq / Hkv <= 128, D 64 or 128, page a power of two from 8 to 256, max_pages * page <= 2^30,
+ * num_pages * page, num_pages * Hkv and B * N below 2^31, scale finite; q, k_cache, v_cache, out
+ * 16-byte aligned.
  * Device-side: a kv_len or length out of range sets INPUT_RANGE and the request's rows are as
  * rows that see nothing; a page out of [0, num_pages) sets INPUT_RANGE and is read as page 0.
  * workspace: >= dspark_workspace_size(DSPARK_OP_PAGED_ATTENTION, B, N, Hq, D).
