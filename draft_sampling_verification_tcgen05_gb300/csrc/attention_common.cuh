@@ -40,6 +40,19 @@ __device__ __forceinline__ uint64_t sw128_token_rows_desc(uint32_t smem_addr, ui
     return d;
 }
 
+// One lane of a converged warp.  The tensor-core warp runs its waits and address arithmetic with all
+// lanes, so that operands stay in uniform registers, and lets one lane issue: issued from a branch that
+// only lane 0 had entered, each instruction cost about 100 cycles of operand moves.
+__device__ __forceinline__ bool elect_one() {
+    uint32_t r;
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "elect.sync _|p, 0xFFFFFFFF;\n\t"
+        "selp.u32 %0, 1, 0, p;\n\t}"
+        : "=r"(r));
+    return r != 0;
+}
+
 // 32 lanes x 32 bits, 32 consecutive columns into r[0..31].
 __device__ __forceinline__ void tmem_ld32(uint32_t taddr, uint32_t* r) {
     asm volatile(
@@ -126,6 +139,17 @@ __device__ __noinline__ void move_infinities(uint8_t* tile, uint32_t block_bytes
     }
 }
 
+// Whether the phase of the given parity is complete, without waiting.
+__device__ __forceinline__ bool mbar_test(uint64_t* bar, uint32_t parity) {
+    uint32_t ok;
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "mbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
+        "selp.u32 %0, 1, 0, p;\n\t}"
+        : "=r"(ok) : "r"(smem_u32(bar)), "r"(parity) : "memory");
+    return ok != 0;
+}
+
 // Named barrier that also tells whether `ok` holds in all its threads.
 __device__ __forceinline__ bool named_bar_and(uint32_t id, uint32_t nthreads, bool ok) {
     uint32_t r;
@@ -137,6 +161,12 @@ __device__ __forceinline__ bool named_bar_and(uint32_t id, uint32_t nthreads, bo
         : "=r"(r) : "r"(id), "r"(nthreads), "r"(static_cast<uint32_t>(ok)) : "memory");
     return r != 0;
 }
+
+// Register shares of a warpgroup (four warps, all of which execute this).
+template <int N>
+__device__ __forceinline__ void registers_give_up() { asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" :: "n"(N)); }
+template <int N>
+__device__ __forceinline__ void registers_take() { asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" :: "n"(N)); }
 
 // Programmatic dependent launch: wait until the preceding kernel of the stream has completed and its
 // writes are visible / allow the next one to be launched (it waits by itself before it reads).

@@ -26,6 +26,10 @@ __device__ __forceinline__ uint32_t pack2(float lo, float hi, __half) {
     return *reinterpret_cast<const uint32_t*>(&p);
 }
 
+template <typename T> __device__ __forceinline__ T round_to(float x);
+template <> __device__ __forceinline__ __nv_bfloat16 round_to(float x) { return __float2bfloat16_rn(x); }
+template <> __device__ __forceinline__ __half round_to(float x) { return __float2half_rn(x); }
+
 template <typename T>
 __device__ __forceinline__ void unpack8(const uint4& w, float* x, T tag) {
     const float2 a = unpack2(w.x, tag), b = unpack2(w.y, tag), c = unpack2(w.z, tag), d = unpack2(w.w, tag);
