@@ -203,9 +203,10 @@ size_t dspark_workspace_size(int op, int B, int N, int V, int r) {
         case DSPARK_OP_VERIFY_GUMBEL:
             return verify_gumbel_workspace_bytes(B, N);
         case DSPARK_OP_KV_APPEND:
-        case DSPARK_OP_PROMPT_ATTENTION:
         case DSPARK_OP_SAMPLE:
             return sizeof(WsHeader);
+        case DSPARK_OP_PROMPT_ATTENTION:
+            return prompt_attention_workspace_bytes(B, N, V);
         case DSPARK_OP_PAGED_ATTENTION:
             return paged_attention_workspace_bytes(B, N, V, r);
         default:
@@ -529,7 +530,7 @@ dspark_status dspark_prompt_attention(const void* q, const void* k, const void* 
     DSPARK_REQUIRE(std::isfinite(scale), "prompt_attention: scale must be finite");
     DSPARK_REQUIRE(aligned(q, 16) && aligned(k, 16) && aligned(v, 16) && aligned(out, 16),
                    "prompt_attention: q, k, v and out must be 16-byte aligned");
-    if (bad_ws(workspace, ws_bytes, sizeof(WsHeader))) return DSPARK_ERR_INVALID_ARG;
+    if (bad_ws(workspace, ws_bytes, prompt_attention_workspace_bytes(B, T, Hq))) return DSPARK_ERR_INVALID_ARG;
     DeviceInfo dev;
     if (!current_device(&dev)) return DSPARK_ERR_UNSUPPORTED;
     return launch_prompt_attention(q, k, v, dtype, q_stride, k_stride, v_stride, cu_seqlens, scale, causal, B, T, Hq,

@@ -88,14 +88,15 @@ __device__ __forceinline__ bool pair_not_finite(uint32_t w, __half) {
 
 // Takes the infinities and NaN out of a value tile (128 token rows of `halves` 128-byte swizzled
 // blocks) before its product, which would spread them to rows that do not see them (0 * infinity is
-// NaN), and adds weight * value of each to the rows that do.  Called by the 128 softmax threads
-// together (named barrier `bar`): thread `line` owns token row `line` of the tile and one output row,
-// which sees this tile's tokens [first, seen).  Scores of the tile are at taddr_s, the output row at
-// taddr_o (complete up to the tile before); `row` and `masks` are scratch in shared memory.
+// NaN), and adds weight * value of each to the rows that do.  Called by 128 softmax threads together
+// (named barrier `bar`): thread `line` owns token row `line` of the tile and one output row, which
+// sees this tile's tokens [first, seen).  The rows' weights are at taddr_p, packed as the product
+// takes them, the output row at taddr_o (complete up to the tile before); `row` and `masks` are
+// scratch in shared memory.
 template <typename T>
 __device__ __noinline__ void move_infinities(uint8_t* tile, uint32_t block_bytes, int halves, int line, int held, int first,
-                                             int seen, uint32_t taddr_s, uint32_t taddr_o, float sl2, float ref,
-                                             float* row, uint32_t* masks, uint32_t bar) {
+                                             int seen, uint32_t taddr_p, uint32_t taddr_o, float* row, uint32_t* masks,
+                                             uint32_t bar) {
     bool bad = false;
     if (line < held) {
         for (int x = 0; x < halves; ++x) {
@@ -124,9 +125,10 @@ __device__ __noinline__ void move_infinities(uint8_t* tile, uint32_t block_bytes
             }
         }
         named_bar_sync(bar, 128);
-        const float s = __uint_as_float(tmem_ld1(taddr_s + static_cast<uint32_t>(t)));
+        const uint32_t pair = tmem_ld1(taddr_p + static_cast<uint32_t>(t >> 1));
         tmem_wait_ld();
-        const float w = exp2_approx(fmaf(s, sl2, -ref));
+        const float2 ws = unpack2(pair, T{});
+        const float w = (t & 1) != 0 ? ws.y : ws.x;
         for (int d = 0; d < 64 * halves; ++d) {
             const float v = row[d];
             if (v == 0.0f) continue;
@@ -168,9 +170,37 @@ __device__ __forceinline__ void registers_give_up() { asm volatile("setmaxnreg.d
 template <int N>
 __device__ __forceinline__ void registers_take() { asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" :: "n"(N)); }
 
+// Quotients of non-negative values: the 32-bit division where it can serve (the 64-bit one is a long
+// dependent chain, and every role starts its work with one).
+__device__ __forceinline__ long long quotient(long long x, long long y) {
+    if (((x | y) >> 32) == 0) return static_cast<uint32_t>(x) / static_cast<uint32_t>(y);
+    return x / y;
+}
+
+// Log-sum-exp from the maximum in log2 units and the sum relative to it.
+__device__ __forceinline__ float lse_of(float m2, float l) {
+    return l == 0.0f ? -INFINITY : ((m2 == -INFINITY ? 0.0f : m2) + log2f(l)) * kLn2;
+}
+
 // Programmatic dependent launch: wait until the preceding kernel of the stream has completed and its
 // writes are visible / allow the next one to be launched (it waits by itself before it reads).
 __device__ __forceinline__ void grid_dependency_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
 __device__ __forceinline__ void grid_dependency_launch() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
+
+// Launch of a kernel that starts while its predecessor ends (it calls grid_dependency_wait itself).
+template <typename K, typename... Args>
+cudaError_t launch_dependent(K kernel, dim3 grid, dim3 block, size_t smem, cudaStream_t stream, Args... args) {
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = grid;
+    cfg.blockDim = block;
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = stream;
+    cudaLaunchAttribute at[1];
+    at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    at[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = at;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, kernel, args...);
+}
 
 }  // namespace dspark

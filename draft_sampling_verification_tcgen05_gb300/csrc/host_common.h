@@ -99,6 +99,7 @@ dspark_status launch_paged_attention(const void* q, const void* k_cache, const v
                                      int D, int num_pages, int page, void* out, float* lse, void* ws,
                                      cudaStream_t stream, const DeviceInfo& dev);
 
+size_t prompt_attention_workspace_bytes(int B, int T, int Hq);
 dspark_status launch_prompt_attention(const void* q, const void* k, const void* v, dspark_dtype dtype,
                                       long long q_stride, long long k_stride, long long v_stride,
                                       const int32_t* cu_seqlens, float scale, int causal, int B, int T, int Hq,

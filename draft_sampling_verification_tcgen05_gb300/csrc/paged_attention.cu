@@ -96,13 +96,6 @@ __device__ __forceinline__ bool request(const PagedArgs& a, int b, int& kv, int&
 __device__ __forceinline__ int tiles_of(int kv) { return (kv + kTile - 1) / kTile; }
 __device__ __forceinline__ int row_tiles_of(const PagedArgs& a, int n) { return (n + a.tile_tokens - 1) / a.tile_tokens; }
 
-// Quotients of non-negative values: the 32-bit division where it can serve (the 64-bit one is a long
-// dependent chain, and every role starts its segments with one).
-__device__ __forceinline__ long long quotient(long long x, long long y) {
-    if (((x | y) >> 32) == 0) return static_cast<uint32_t>(x) / static_cast<uint32_t>(y);
-    return x / y;
-}
-
 // Steps of a unit: kUnitSteps to start and end it, then its tiles.
 constexpr int kUnitSteps = 3;
 __device__ __forceinline__ int steps_of(int tiles) { return tiles + kUnitSteps; }
@@ -255,10 +248,6 @@ __global__ void __launch_bounds__(kPlanThreads) paged_plan_kernel(PagedArgs a, i
         }
         before = end;
     }
-}
-
-__device__ __forceinline__ float lse_of(float m2, float l) {
-    return l == 0.0f ? -INFINITY : ((m2 == -INFINITY ? 0.0f : m2) + log2f(l)) * kLn2;
 }
 
 template <int D, int kParts>
@@ -571,10 +560,8 @@ paged_attention_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_con
 #pragma unroll
                     for (int c = 0; c < kCols; c += 32) tmem_ld32(scol + c, r + c);
                     tmem_wait_ld();
-                    if (pass == 0) {
-                        tc_fence_before();
-                        mbar_arrive(&s.s_free[i & 1]);
-                    }
+                    tc_fence_before();
+                    mbar_arrive(&s.s_free[i & 1]);
                     if (masked) {
 #pragma unroll
                         for (int c = 0; c < kCols; ++c)
@@ -675,11 +662,9 @@ paged_attention_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_con
                         }
                         const int upto = min(seen, kCols) + static_cast<int>(col0);
                         move_infinities<T>(tile, Cfg::kBlockBytes, kHalves, line, g.kv - t * kTile, static_cast<int>(col0),
-                                           upto, tlane + kColS + static_cast<uint32_t>(i & 1) * kTile, tlane + kColO, sl2,
-                                           ref, s.row, s.masks, 2);
+                                           upto, tlane + kColP + static_cast<uint32_t>(i & 1) * 64u, tlane + kColO, s.row,
+                                           s.masks, 2);
                         fence_proxy_async_smem();
-                        tc_fence_before();
-                        mbar_arrive(&s.s_free[i & 1]);
                     }
                     tc_fence_before();
                     mbar_arrive(&s.p_ready[i & 1]);
@@ -970,21 +955,6 @@ __global__ void __launch_bounds__(kJoinRows * D) paged_join_kernel(const __grid_
 // Host side.
 // ---------------------------------------------------------------------------
 int rows_cap_of(int N, int heads) { return static_cast<int>(std::min<long long>(kTile, static_cast<long long>(N) * heads)); }
-
-template <typename K, typename... Args>
-cudaError_t launch_dependent(K kernel, dim3 grid, dim3 block, size_t smem, cudaStream_t stream, Args... args) {
-    cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = grid;
-    cfg.blockDim = block;
-    cfg.dynamicSmemBytes = smem;
-    cfg.stream = stream;
-    cudaLaunchAttribute at[1];
-    at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    at[0].val.programmaticStreamSerializationAllowed = 1;
-    cfg.attrs = at;
-    cfg.numAttrs = 1;
-    return cudaLaunchKernelEx(&cfg, kernel, args...);
-}
 
 template <typename T, int D, int kParts>
 cudaError_t launch_parts(const CUtensorMap& q, const CUtensorMap& k, const CUtensorMap& v, const PagedArgs& a, int grid,

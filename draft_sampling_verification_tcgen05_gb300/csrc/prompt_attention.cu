@@ -1,109 +1,732 @@
 // Attention within packed prompts of different lengths.
 //
-// One warp per (token, query head): the row's query in registers, its sequence's keys one after
-// another, a running maximum and sum (the softmax in one pass), all in fp32.
-#include "device_common.cuh"
-#include "half_common.cuh"
+// An item is 256 rows against one key head of one sequence: two query tiles of 128 rows, each as many
+// tokens as fit with the G query heads that share the key head, so keys and values are loaded once for
+// 256 rows.  A persistent CTA per SM takes items from a queue, the ones with the most keys first, and
+// streams the sequence's keys and values past its two tiles in tiles of 128 tokens.  While one tile's
+// scores go through the softmax, the tensor cores work for the other.
+//
+//   warp 0      takes the items and loads (TMA) queries, keys and values
+//   warp 1      clears the tokens outside every sequence
+//   warps 2, 3  issue S = Q K^T and O += P V of one query tile each on tcgen05 (M = 128, fp32 in
+//               tensor memory; P replaces half of S)
+//   warps 4-7, 8-11  softmax and output of one query tile each: a thread per row, running maximum and
+//               sum in fp32, weights rounded to the inputs' type
+//
+// The running maximum is raised only when a tile exceeds it by 2^8 (O is then rescaled): weights up to
+// 2^8 lose nothing in a floating type, and the rescaling leaves the common path.
+//
+// A row must not see what lies outside its limit, but 0 * infinity is not 0.  Values past the
+// sequence's end are zeroed in shared memory before the product.  A query tile whose result is not
+// finite is done again alone with the infinities and NaN taken out of every value tile and added to
+// the rows that see them; nothing else changes then, so rows that do not see them come out bit for
+// bit as without them.
+#include "attention_common.cuh"
 #include "host_common.h"
+
+#include <algorithm>
 
 namespace dspark {
 namespace {
 
+constexpr int kTile = 128;                 // key tokens per tile, and MMA rows
+constexpr int kThreads = 384;
+constexpr int kRowThreads = 128;           // softmax threads of a query tile
+constexpr float kRaise = 8.0f;             // log2 units
+constexpr int kAhead = 4;                  // items between the loads and the results
+constexpr int kRedo = 2 * kAhead;          // items of which a query tile waits to be done again: at most those under way
+constexpr int kSlots = 2;                  // key tiles, and value tiles, in flight
+constexpr int kOrdered = 256;              // up to so many sequences the items are put in order of their size
+constexpr uint32_t kColS = 0, kColP = 64, kColO = 256, kTmemCols = 512;    // S and O of tile 1: + 128
+constexpr uint32_t kWaitLoad = 0x901, kWaitMma = 0x902, kWaitSoftmax = 0x903;
+
+struct Plan {
+    WsHeader header;
+    int items;                             // without the heads
+    unsigned int next;                     // of the queue, heads innermost
+    int begin, end;                        // the tokens of all sequences
+    int pad[60];
+};
+static_assert(sizeof(Plan) == 512, "the item list behind the plan is aligned");
+
 struct PromptArgs {
-    const void *q, *k, *v;
-    long long q_stride, k_stride, v_stride;
     const int32_t* cu_seqlens;
-    int causal, B, T, Hq, Hkv;
+    int causal, B, T, Hq, Hkv, group;
+    int tile_tokens;                       // tokens of a query tile
     float scale;
     void* out;
     float* lse;
-    WsHeader* ws;
+    Plan* plan;
+    int4* items;                           // sequence begin, end, pair of query tiles, 0
+    long long timeout_ns;
+};
+
+// An item as the roles see it.
+struct Item {
+    int begin, end;                        // the sequence
+    int tok;                               // first token of tile 0, relative to the sequence
+    int h;
+    int n[2];                              // key tiles of each query tile
+    int redo;                              // done again: infinities are moved
+    int id, pair;
+};
+
+// Key tiles that query tile x of an item sees.
+__device__ __forceinline__ int tiles_seen(const PromptArgs& a, int len, int tok, int x) {
+    const int first = tok + x * a.tile_tokens;
+    if (first >= len) return 0;
+    const int last = a.causal ? min(len, first + a.tile_tokens) : len;
+    return (last + kTile - 1) / kTile;
+}
+
+// ---------------------------------------------------------------------------
+// Plan: one block.  Clears the status word and the queue, reads the sequences' bounds as their running
+// maximum within [0, T], and lists the items.
+// ---------------------------------------------------------------------------
+constexpr int kPlanThreads = 1024;
+
+__global__ void __launch_bounds__(kPlanThreads) prompt_plan_kernel(const __grid_constant__ PromptArgs a) {
+    __shared__ int s_warp[kPlanThreads / 32], s_carry;
+    __shared__ int s_end[kPlanThreads + 1];                // bounds of the sequences at hand
+    __shared__ int s_first[kPlanThreads + 1];              // their first items
+    Plan* p = a.plan;
+    const int tid = threadIdx.x;
+    grid_dependency_launch();                              // the attention kernel sets itself up meanwhile
+    if (tid < 64) reinterpret_cast<uint32_t*>(&p->header)[tid] = 0u;
+    // inclusive scan over the block, by maximum or sum, on top of `carry`
+    auto scan = [&](int x, bool sum) {
+        for (int d = 1; d < 32; d <<= 1) {
+            const int y = __shfl_up_sync(0xFFFFFFFFu, x, d);
+            if (lane_id() >= static_cast<uint32_t>(d)) x = sum ? x + y : max(x, y);
+        }
+        __syncthreads();
+        if (lane_id() == 31) s_warp[warp_id()] = x;
+        __syncthreads();
+        int before = 0;
+        for (uint32_t w = 0; w < warp_id(); ++w) before = sum ? before + s_warp[w] : max(before, s_warp[w]);
+        return sum ? x + before : max(x, before);
+    };
+    const int pair = 2 * a.tile_tokens;
+    int bound = min(max(a.cu_seqlens[0], 0), a.T), total = 0;
+    __syncthreads();
+    if (tid == 0) {
+        p->begin = bound;
+        if (a.cu_seqlens[0] != bound) flag_input_index(&p->header);
+    }
+    for (int b0 = 0; b0 < a.B; b0 += kPlanThreads) {
+        const int count = min(kPlanThreads, a.B - b0);
+        const int raw = tid < count ? a.cu_seqlens[b0 + tid + 1] : 0;
+        const int end = max(bound, scan(min(max(raw, 0), a.T), false));
+        if (tid < count && raw != end) flag_input_index(&p->header);
+        s_end[tid + 1] = end;
+        if (tid == 0) s_end[0] = bound;
+        __syncthreads();
+        const int mine = tid < count ? (end - s_end[tid] + pair - 1) / pair : 0;
+        const int last = total + scan(mine, true), first = last - mine;
+        s_first[tid] = first;
+        if (tid == kPlanThreads - 1) s_carry = last;
+        __syncthreads();
+        total = s_carry;
+        bound = s_end[count];
+        if (a.B > kOrdered) {
+            // sequence by sequence, the later tokens first
+            for (int x = 0; x < mine; ++x) a.items[first + x] = make_int4(s_end[tid], end, mine - 1 - x, 0);
+            __syncthreads();
+        }
+    }
+    if (a.B <= kOrdered) {
+        // by the place in the sequence, the last first: that is the order of the work under the causal mask
+        for (int e = tid; e < total; e += kPlanThreads) {
+            int lo = 0, hi = a.B - 1;                      // the sequence of item e
+            while (lo < hi) {
+                const int mid = (lo + hi + 1) / 2;
+                if (s_first[mid] <= e) lo = mid; else hi = mid - 1;
+            }
+            const int x = e - s_first[lo];
+            int at = 0;
+            for (int b = 0; b < a.B; ++b) {
+                const int n = (b + 1 < a.B ? s_first[b + 1] : total) - s_first[b];
+                at += max(0, n - x - 1) + (b < lo && n > x ? 1 : 0);
+            }
+            a.items[at] = make_int4(s_end[lo], s_end[lo + 1], x, 0);
+        }
+    }
+    if (tid == 0) {
+        p->items = total;
+        p->next = 0u;
+        p->end = bound;
+    }
+}
+
+template <int D>
+struct PromptSmem {
+    static constexpr int kHalves = D / 64;                        // 128-byte column blocks
+    static constexpr uint32_t kBlockBytes = kTile * 128;
+    static constexpr uint32_t kTileBytes = kHalves * kBlockBytes;
+    alignas(1024) uint8_t q[2][kTileBytes];
+    alignas(1024) uint8_t k[kSlots][kTileBytes];
+    alignas(1024) uint8_t v[kSlots][kTileBytes];
+    alignas(1024) float4 stage[2][kTile * 8];                     // 32 columns of a query tile's rows
+    Item item[kAhead];
+    float row[2][D];
+    uint32_t masks[2][4];
+    int redo[2][kRedo];                                           // items to be done again, by query tile
+    unsigned int redo_count[2];                                   // entries written so far
+    uint64_t item_full[kAhead], item_empty[kAhead];
+    uint64_t q_full[2], q_empty[2];
+    uint64_t k_full[kSlots], k_empty[kSlots], v_full[kSlots], v_empty[kSlots];
+    uint64_t s_full[2], p_high[2], p_low[2], pv_done[2], o_empty[2], drain[2];
+    uint32_t tmem_base;
 };
 
 template <typename T, int D>
-__global__ void __launch_bounds__(128) prompt_attention_kernel(PromptArgs a) {
-    constexpr int kPer = D / 32;                      // values of a row per lane (2 or 4)
-    const long long row = static_cast<long long>(blockIdx.x) * 4 + warp_id();
-    if (row >= static_cast<long long>(a.T) * a.Hq) return;
-    const int h = static_cast<int>(row % a.Hq), t = static_cast<int>(row / a.Hq);
-    const int lane = lane_id(), hk = h / (a.Hq / a.Hkv);
-    // the token's sequence, from the bounds as their running maximum clipped to [0, T]
-    int begin = 0, end = 0, lo = 0;
-    bool bad = false;
-    for (int b = 0; b <= a.B; ++b) {
-        const int c = a.cu_seqlens[b], hi = max(lo, min(max(c, 0), a.T));
-        bad = bad || c != hi;
-        if (b > 0 && lo <= t && t < hi) {
-            begin = lo;
-            end = a.causal ? t + 1 : hi;
-        }
-        lo = hi;
-    }
-    if (bad && lane == 0) flag_input_index(a.ws);
+__global__ void __launch_bounds__(kThreads, 1)
+prompt_attention_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmK,
+                        const __grid_constant__ CUtensorMap tmV, const __grid_constant__ PromptArgs a) {
+    using Smem = PromptSmem<D>;
+    constexpr int kHalves = Smem::kHalves;
+    constexpr uint32_t kBlockBytes = Smem::kBlockBytes, kTileBytes = Smem::kTileBytes;
+    extern __shared__ __align__(1024) uint8_t smem_raw[];
+    Smem& s = *reinterpret_cast<Smem*>(smem_raw);
+    const uint32_t warp = warp_id(), lane = lane_id();
+    WsHeader* ws = &a.plan->header;
 
-    float q[kPer], o[kPer] = {};
-    auto load = [&](const void* base, long long at, float* x) {
-        const T* p = static_cast<const T*>(base) + at + lane * kPer;
-#pragma unroll
-        for (int e = 0; e < kPer; e += 2) {
-            const float2 v = unpack2(*reinterpret_cast<const uint32_t*>(p + e), T{});
-            x[e] = v.x;
-            x[e + 1] = v.y;
+    if (threadIdx.x == 0) {
+        for (int i = 0; i < kAhead; ++i) {
+            mbar_init(&s.item_full[i], 1);
+            mbar_init(&s.item_empty[i], 2 * kRowThreads + 2);
         }
-    };
-    load(a.q, t * a.q_stride + static_cast<long long>(h) * D, q);
-    float m = -INFINITY, l = 0.0f;
-    for (int j = begin; j < end; ++j) {
-        float k[kPer], v[kPer];
-        load(a.k, j * a.k_stride + static_cast<long long>(hk) * D, k);
-        load(a.v, j * a.v_stride + static_cast<long long>(hk) * D, v);
-        float s = 0.0f;
-#pragma unroll
-        for (int e = 0; e < kPer; ++e) s = fmaf(q[e], k[e], s);
-        for (int d = 16; d > 0; d >>= 1) s += __shfl_xor_sync(0xFFFFFFFFu, s, d);
-        s *= a.scale;
-        const float mn = fmaxf(m, s), ref = mn == -INFINITY ? 0.0f : mn;
-        const float c = expf((m == -INFINITY ? ref : m) - ref), w = expf(s - ref);
-        l = l * c + w;
-#pragma unroll
-        for (int e = 0; e < kPer; ++e) o[e] = o[e] * c + w * v[e];
-        m = mn;
+        for (int i = 0; i < 2; ++i) {
+            mbar_init(&s.q_full[i], 1);
+            mbar_init(&s.q_empty[i], 1);
+            mbar_init(&s.s_full[i], 1);
+            mbar_init(&s.p_high[i], kRowThreads);
+            mbar_init(&s.p_low[i], kRowThreads);
+            mbar_init(&s.pv_done[i], 1);
+            mbar_init(&s.o_empty[i], kRowThreads);
+            mbar_init(&s.drain[i], 1);
+        }
+        for (int i = 0; i < kSlots; ++i) {
+            mbar_init(&s.k_full[i], 1);
+            mbar_init(&s.k_empty[i], 2);
+            mbar_init(&s.v_full[i], 1);
+            mbar_init(&s.v_empty[i], 2);
+        }
+        s.redo_count[0] = s.redo_count[1] = 0u;
+        fence_mbarrier_init();
+        prefetch_tensormap(&tmQ);
+        prefetch_tensormap(&tmK);
+        prefetch_tensormap(&tmV);
     }
-    const float inv = l != 0.0f ? 1.0f / l : 0.0f;
-    T* out = static_cast<T*>(a.out) + row * D + lane * kPer;
+    if (warp == 2) {
+        tmem_alloc(&s.tmem_base, kTmemCols);
+        tmem_relinquish();
+    }
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tmem = s.tmem_base;
+    grid_dependency_wait();
+
+    bool ok = true;
+    auto all = [&](bool x) { return __all_sync(0xFFFFFFFFu, x); };
+    auto wait = [&](uint64_t& bar, int use, uint32_t where) {            // use: how often it completed before
+        return mbar_wait(&bar, static_cast<uint32_t>(use) & 1u, ws, a.timeout_ns, where);
+    };
+
+    if (warp == 0) {
+        // ---------------- items and loads ----------------
+        if (lane == 0) {
+            const uint64_t keep = l2_policy_evict_last();
+            const int total = a.plan->items * a.Hkv;
+            int kt = 0, qt[2] = {0, 0}, count = 0;        // key tiles, query tiles, items so far
+            unsigned int redone[2] = {0, 0};
+            // a query tile to be done again (item * 2 + tile), or -1
+            auto pending = [&] {
+                for (int x = 0; x < 2; ++x) {
+                    if (redone[x] == *reinterpret_cast<volatile unsigned int*>(&s.redo_count[x])) continue;
+                    __threadfence_block();
+                    return s.redo[x][redone[x]++ % kRedo] * 2 + x;
+                }
+                return -1;
+            };
+            while (true) {
+                Item it{};
+                int again = pending();                    // else the queue's next item
+                int id = again >= 0 ? again >> 1 : static_cast<int>(atomicAdd(&a.plan->next, 1u));
+                if (again < 0 && id >= total) {
+                    // the queue is empty: what is under way may still ask for a tile to be done again
+                    for (int x = std::max(0, count - kAhead); ok && x < count; ++x)
+                        ok = wait(s.item_empty[x % kAhead], x / kAhead, kWaitLoad);
+                    if (ok) again = pending();
+                    if (again < 0) break;
+                    id = again >> 1;
+                }
+                const int entry = id / a.Hkv;
+                const int4 e = a.items[entry];
+                it.begin = e.x;
+                it.end = e.y;
+                it.h = id - entry * a.Hkv;
+                it.tok = e.z * 2 * a.tile_tokens;
+                it.id = id;
+                it.redo = again >= 0 ? 1 : 0;
+                for (int x = 0; x < 2; ++x)
+                    it.n[x] = again >= 0 && (again & 1) != x ? 0 : tiles_seen(a, it.end - it.begin, it.tok, x);
+                ok = wait(s.item_empty[count % kAhead], count / kAhead + 1, kWaitLoad);
+                if (!ok) break;
+                s.item[count % kAhead] = it;
+                mbar_arrive(&s.item_full[count % kAhead]);
+                ++count;
+                for (int x = 0; ok && x < 2; ++x) {
+                    if (it.n[x] == 0) continue;
+                    ok = wait(s.q_empty[x], qt[x] + 1, kWaitLoad);
+                    if (!ok) break;
+                    mbar_arrive_expect_tx(&s.q_full[x], static_cast<uint32_t>(a.tile_tokens * a.group) * 128u * kHalves);
+                    for (int y = 0; y < kHalves; ++y)
+                        tma_load_3d(s.q[x] + y * kBlockBytes, &tmQ, y * 64, it.h * a.group,
+                                    it.begin + it.tok + x * a.tile_tokens, &s.q_full[x], keep);
+                    ++qt[x];
+                }
+                const int n = std::max(it.n[0], it.n[1]);
+                for (int t = 0; ok && t < n; ++t, ++kt) {
+                    const int slot = kt % kSlots;
+                    ok = wait(s.k_empty[slot], kt / kSlots + 1, kWaitLoad);
+                    if (!ok) break;
+                    mbar_arrive_expect_tx(&s.k_full[slot], kTileBytes);
+                    for (int y = 0; y < kHalves; ++y)
+                        tma_load_3d(s.k[slot] + y * kBlockBytes, &tmK, y * 64, it.h, it.begin + t * kTile, &s.k_full[slot], keep);
+                    ok = wait(s.v_empty[slot], kt / kSlots + 1, kWaitLoad);
+                    if (!ok) break;
+                    mbar_arrive_expect_tx(&s.v_full[slot], kTileBytes);
+                    for (int y = 0; y < kHalves; ++y)
+                        tma_load_3d(s.v[slot] + y * kBlockBytes, &tmV, y * 64, it.h, it.begin + t * kTile, &s.v_full[slot], keep);
+                }
+                if (!ok) break;
+            }
+            if (ok) {
+                // the end: an item without a head
+                ok = wait(s.item_empty[count % kAhead], count / kAhead + 1, kWaitLoad);
+                if (ok) {
+                    s.item[count % kAhead].h = -1;
+                    mbar_arrive(&s.item_full[count % kAhead]);
+                }
+            }
+            if (!ok) {
+                // give copies in flight time to land before the block exits
+                const long long t0 = global_ns();
+                while (global_ns() - t0 < a.timeout_ns) {
+                }
+            }
+        }
+    } else if (warp == 1) {
+        // ---------------- tokens outside every sequence ----------------
+        const int begin = a.plan->begin, end = a.plan->end;
+        const int outside = begin + (a.T - end);
+        for (int x = blockIdx.x; x < outside; x += gridDim.x) {
+            const long long t = x < begin ? x : end + (x - begin);
+            uint4* dst = reinterpret_cast<uint4*>(static_cast<T*>(a.out) + t * a.Hq * D);
+            for (int y = static_cast<int>(lane); y < a.Hq * (D / 8); y += 32) dst[y] = make_uint4(0u, 0u, 0u, 0u);
+            if (a.lse)
+                for (int y = static_cast<int>(lane); y < a.Hq; y += 32) a.lse[t * a.Hq + y] = -INFINITY;
+        }
+    } else if (warp < 4) {
+        // ---------------- products of query tile w: the whole warp waits, one lane issues ----------------
+        const int w = static_cast<int>(warp) - 2;
+        constexpr uint32_t kIdescS = attn_idesc<T, false>(kTile, kTile);
+        constexpr uint32_t kIdescO = attn_idesc<T, true>(kTile, D);
+        constexpr uint32_t kStep = kTileBytes >> 4;               // a tile, in descriptor units
+        const uint64_t q_desc = sw128_kmajor_desc(smem_u32(s.q[w]));
+        const uint64_t k_desc = sw128_kmajor_desc(smem_u32(s.k[0]));
+        const uint64_t v_desc = sw128_token_rows_desc(smem_u32(s.v[0]), kBlockBytes);
+        const uint32_t tS = tmem + kColS + w * 128u, tP = tmem + kColP + w * 128u, tO = tmem + kColO + w * 128u;
+        int kt = 0, i = 0, used = 0;                              // key tiles, own key tiles, own query tiles
+        for (int count = 0; ok; ++count) {
+            ok = all(wait(s.item_full[count % kAhead], count / kAhead, kWaitMma));
+            if (!ok) break;
+            const Item& it = s.item[count % kAhead];
+            const int h = __shfl_sync(0xFFFFFFFFu, it.h, 0);
+            if (h < 0) break;
+            const int n = __shfl_sync(0xFFFFFFFFu, it.n[w], 0), other = __shfl_sync(0xFFFFFFFFu, it.n[1 - w], 0);
+            const int len = __shfl_sync(0xFFFFFFFFu, it.end - it.begin, 0);
+            const int redo = __shfl_sync(0xFFFFFFFFu, it.redo, 0);
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&s.item_empty[count % kAhead]);
+            if (n > 0) ok = all(wait(s.q_full[w], used, kWaitMma));
+            // One tile's scores, then the product of its weights: the tensor cores run them in this order,
+            // so S may be written as soon as the product that read P (in S) has been issued.
+            const int most = max(n, other);
+            for (int t = 0; ok && t < most; ++t, ++kt) {
+                const int slot = kt % kSlots;
+                ok = all(wait(s.k_full[slot], kt / kSlots, kWaitMma));
+                if (!ok) break;
+                if (t < n) {
+                    tc_fence_after();
+                    const uint64_t k = k_desc + static_cast<uint32_t>(slot) * kStep;
+                    if (elect_one()) {
 #pragma unroll
-    for (int e = 0; e < kPer; e += 2)
-        *reinterpret_cast<uint32_t*>(out + e) = pack2(o[e] * inv, o[e + 1] * inv, T{});
-    if (a.lse && lane == 0) a.lse[row] = l != 0.0f ? (m == -INFINITY ? 0.0f : m) + logf(l) : -INFINITY;
+                        for (int d = 0; d < D / 16; ++d) {
+                            const uint64_t off = (static_cast<uint32_t>(d / 4) * kBlockBytes + (d % 4) * 32) >> 4;
+                            mma_issue<false>(tS, q_desc + off, k + off, kIdescS, d != 0 ? 1u : 0u);
+                        }
+                        mma_commit(&s.s_full[w]);
+                        mma_commit(&s.k_empty[slot]);
+                        if (t + 1 == n) mma_commit(&s.q_empty[w]);
+                    }
+                    __syncwarp();
+                } else if (elect_one()) {
+                    mbar_arrive(&s.k_empty[slot]);
+                }
+                ok = all(wait(s.v_full[slot], kt / kSlots, kWaitMma));
+                if (!ok) break;
+                if (t < n) {
+                    const int held = len - t * kTile;
+                    if (held < kTile) {                           // behind the sequence's end nothing may count
+                        const int pieces = (kTile - held) * 8;    // of 16 bytes, per block
+                        for (int y = 0; y < kHalves; ++y)
+                            for (int x = static_cast<int>(lane); x < pieces; x += 32)
+                                *reinterpret_cast<uint4*>(s.v[slot] + y * kBlockBytes + held * 128 + x * 16) =
+                                    make_uint4(0u, 0u, 0u, 0u);
+                        fence_proxy_async_smem();
+                        __syncwarp();
+                    }
+                    ok = all(wait(s.p_high[w], i, kWaitMma) && (t > 0 || used == 0 || wait(s.o_empty[w], used - 1, kWaitMma)));
+                    if (!ok) break;
+                    tc_fence_after();
+                    const uint64_t v = v_desc + static_cast<uint32_t>(slot) * kStep;
+                    const uint32_t onto = t == 0 && redo == 0 ? 0u : 1u;   // done again, O starts from what is there
+                    // tokens 64..127 first: their weights are ready first
+                    if (elect_one()) {
+#pragma unroll
+                        for (int x = 4; x < 8; ++x) mma_issue_ta(tO, tP + x * 8, v + x * 128, kIdescO, x == 4 ? onto : 1u);
+                    }
+                    __syncwarp();
+                    ok = all(wait(s.p_low[w], i, kWaitMma));
+                    if (!ok) break;
+                    tc_fence_after();
+                    if (elect_one()) {
+#pragma unroll
+                        for (int x = 0; x < 4; ++x) mma_issue_ta(tO, tP + x * 8, v + x * 128, kIdescO, 1u);
+                        mma_commit(&s.pv_done[w]);
+                        mma_commit(&s.v_empty[slot]);
+                    }
+                    __syncwarp();
+                    ++i;
+                } else if (elect_one()) {
+                    mbar_arrive(&s.v_empty[slot]);
+                }
+                __syncwarp();
+            }
+            if (n > 0) ++used;
+        }
+        if (elect_one()) mma_commit(&s.drain[w]);
+        __syncwarp();
+        const long long t0 = global_ns();
+        while (!mbar_try_wait(&s.drain[w], 0) && global_ns() - t0 < a.timeout_ns) {
+        }
+        __syncwarp();
+    } else {
+        // ---------------- softmax and output of query tile w ----------------
+        const int w = static_cast<int>(warp >= 8 ? 1 : 0);
+        const uint32_t bar = 1u + static_cast<uint32_t>(w);
+        const uint32_t quad = warp & 3u;
+        const uint32_t lanes = (quad * 32u) << 16;
+        const uint32_t tS = tmem + lanes + kColS + w * 128u, tP = tmem + lanes + kColP + w * 128u, tO = tmem + lanes + kColO + w * 128u;
+        const int row = static_cast<int>(quad * 32u + lane);
+        const int row_tok = row / a.group, row_head = row - row_tok * a.group;
+        const bool row_used = row < a.tile_tokens * a.group;
+        const float sl2 = a.scale * kLog2e;
+        const bool falling = sl2 < 0.0f;                          // the largest score is the smallest product
+        const float none = falling ? INFINITY : -INFINITY;
+        int i = 0;                                                // own key tiles
+        int kt = 0;                                               // key tiles
+        int used = 0;                                             // own query tiles
+        for (int count = 0;; ++count) {
+            ok = named_bar_and(bar, kRowThreads, wait(s.item_full[count % kAhead], count / kAhead, kWaitSoftmax));
+            if (!ok) break;
+            const Item it = s.item[count % kAhead];
+            if (it.h < 0) break;
+            const int n = it.n[w], len = it.end - it.begin;
+            if (n == 0) {
+                kt += it.n[1 - w];
+                mbar_arrive(&s.item_empty[count % kAhead]);
+                continue;
+            }
+            const int tok = it.tok + w * a.tile_tokens + row_tok;         // of this row, in its sequence
+            const bool valid = row_used && tok < len;
+            const int limit = valid && a.causal ? tok + 1 : len;
+            float m2 = -INFINITY, l = 0.0f;
+            for (int t = 0; t < n; ++t, ++i) {
+                bool go = wait(s.s_full[w], i, kWaitSoftmax);
+                if (it.redo) go = named_bar_and(bar, kRowThreads, go);    // these meet in barriers below
+                ok = all(go);
+                if (!ok) break;
+                tc_fence_after();
+                const int seen = limit - t * kTile;
+                const bool masked = __any_sync(0xFFFFFFFFu, seen < kTile);
+                // 64 scores at a time in registers: the first half for the maximum only
+                uint32_t r[64];
+                auto load = [&](int c0) {
+                    tmem_ld32(tS + c0, r);
+                    tmem_ld32(tS + c0 + 32, r + 32);
+                    tmem_wait_ld();
+                    if (masked) {
+#pragma unroll
+                        for (int c = 0; c < 64; ++c)
+                            if (c0 + c >= seen) r[c] = __float_as_uint(none);
+                    }
+                };
+                float best[4] = {none, none, none, none};
+                auto most = [&] {
+                    if (!falling) {
+#pragma unroll
+                        for (int c = 0; c < 64; c += 8)
+#pragma unroll
+                            for (int x = 0; x < 4; ++x)
+                                best[x] = fmaxf(fmaxf(best[x], __uint_as_float(r[c + x])), __uint_as_float(r[c + 4 + x]));
+                    } else {
+#pragma unroll
+                        for (int c = 0; c < 64; ++c) best[c & 3] = fminf(best[c & 3], __uint_as_float(r[c]));
+                    }
+                };
+                load(0);
+                most();
+                load(64);
+                most();
+                const float top = falling ? fminf(fminf(best[0], best[1]), fminf(best[2], best[3]))
+                                          : fmaxf(fmaxf(best[0], best[1]), fmaxf(best[2], best[3]));
+                const float mt = top == none ? -INFINITY : top * sl2;
+                if (t == 0) {
+                    m2 = mt;
+                } else {
+                    const bool raise = valid && mt > m2 + kRaise;
+                    if (__any_sync(0xFFFFFFFFu, raise)) {
+                        ok = all(wait(s.pv_done[w], i - 1, kWaitSoftmax));
+                        if (!ok && !it.redo) break;                       // else at the vote below
+                        tc_fence_after();
+                        const float f = raise ? exp2_approx(m2 - mt) : 1.0f;
+                        if (raise) {
+                            l *= f;
+                            m2 = mt;
+                        }
+#pragma unroll 1
+                        for (uint32_t c = 0; c < D; c += 16) {
+                            uint32_t o[16];
+                            tmem_ld16(tO + c, o);
+                            tmem_wait_ld();
+#pragma unroll
+                            for (int x = 0; x < 16; ++x) o[x] = __float_as_uint(__uint_as_float(o[x]) * f);
+                            tmem_st16(tO + c, o);
+                        }
+                        tmem_wait_st();
+                    }
+                }
+                const float ref = m2 == -INFINITY ? 0.0f : m2;
+                float sum[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+                auto weigh = [&](int c0) {                                // 64 weights, to P
+#pragma unroll
+                    for (int c = 0; c < 64; ++c)
+                        r[c] = __float_as_uint(exp2_approx(fmaf(__uint_as_float(r[c]), sl2, -ref)));
+                    if (masked) {
+#pragma unroll
+                        for (int c = 0; c < 64; ++c)
+                            if (c0 + c >= seen) r[c] = 0u;
+                    }
+#pragma unroll
+                    for (int c = 0; c < 64; c += 32) {
+                        uint32_t p[16];
+#pragma unroll
+                        for (int x = 0; x < 16; ++x)
+                            p[x] = pack2(__uint_as_float(r[c + 2 * x]), __uint_as_float(r[c + 2 * x + 1]), T{});
+                        tmem_st16(tP + (c0 + c) / 2, p);
+                    }
+#pragma unroll
+                    for (int c = 0; c < 64; ++c) sum[c & 3] += __uint_as_float(r[c]);
+                };
+                weigh(64);                                                // P takes the place of scores 64..127
+                tmem_wait_st();
+                if (!it.redo) {
+                    tc_fence_before();
+                    mbar_arrive(&s.p_high[w]);
+                }
+                load(0);
+                weigh(0);
+                l += (sum[0] + sum[1]) + (sum[2] + sum[3]);
+                tmem_wait_st();
+                if (it.redo) {
+                    const int slot = (kt + t) % kSlots;
+                    bool there = ok && wait(s.v_full[slot], (kt + t) / kSlots, kWaitSoftmax);
+                    // O is about to be changed here: the products before must be complete
+                    if (there && t > 0) there = wait(s.pv_done[w], i - 1, kWaitSoftmax);
+                    ok = named_bar_and(bar, kRowThreads, there);
+                    if (!ok) break;
+                    tc_fence_after();
+                    if (t == 0) {
+                        uint32_t zero[16];
+#pragma unroll
+                        for (int c = 0; c < 16; ++c) zero[c] = 0u;
+                        for (uint32_t c = 0; c < D; c += 16) tmem_st16(tO + c, zero);
+                        tmem_wait_st();
+                    }
+                    move_infinities<T>(s.v[slot], kBlockBytes, kHalves, row, len - t * kTile, 0, min(seen, kTile), tP, tO,
+                                       s.row[w], s.masks[w], bar);
+                    fence_proxy_async_smem();
+                    tc_fence_before();
+                    mbar_arrive(&s.p_high[w]);
+                }
+                tc_fence_before();
+                mbar_arrive(&s.p_low[w]);
+            }
+            kt += max(n, it.n[1 - w]);
+
+            // ---------------- the query tile's rows ----------------
+            if (ok) ok = all(wait(s.pv_done[w], i - 1, kWaitSoftmax));
+            ok = named_bar_and(bar, kRowThreads, ok);                     // the warps meet again: give up together
+            if (!ok) break;
+            {
+                tc_fence_after();
+                const float f = l != 0.0f ? 1.0f / l : 0.0f;
+                float check[4] = {l * 0.0f, 0.0f, 0.0f, 0.0f};            // 0, or NaN
+                // 32 columns at a time through shared memory, so that four lanes write a row's piece together
+                float4* stage = s.stage[w] + quad * 256;
+                const int piece = static_cast<int>(lane) & 3;             // eight columns
+                const int first = it.tok + w * a.tile_tokens;
+                const int rows = min(a.tile_tokens, len - first) * a.group;
+                const long long row0 = static_cast<long long>(it.begin + first) * a.Hq + it.h * a.group;
+                long long to[4];                                          // this lane's four rows (-1: none)
+#pragma unroll
+                for (int y = 0; y < 4; ++y) {
+                    const int rr = static_cast<int>(quad) * 32 + y * 8 + (static_cast<int>(lane) >> 2);
+                    const int rt = rr / a.group;
+                    to[y] = rr >= rows ? -1 : (row0 + static_cast<long long>(rt) * a.Hq + (rr - rt * a.group)) * D + piece * 8;
+                }
+#pragma unroll 1
+                for (int c = 0; c < D; c += 32) {
+                    float o[32];
+                    tmem_ld32(tO + c, reinterpret_cast<uint32_t*>(o));
+                    tmem_wait_ld();
+                    if (c + 32 == D) {
+                        tc_fence_before();
+                        mbar_arrive(&s.o_empty[w]);
+                    }
+                    __syncwarp();                                         // the columns before have been read
+#pragma unroll
+                    for (int x = 0; x < 8; ++x) {
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) check[e] = fmaf(o[4 * x + e], 0.0f, check[e]);
+                        stage[lane * 8 + (x ^ (lane & 7))] =
+                            make_float4(o[4 * x] * f, o[4 * x + 1] * f, o[4 * x + 2] * f, o[4 * x + 3] * f);
+                    }
+                    __syncwarp();
+#pragma unroll
+                    for (int y = 0; y < 4; ++y) {
+                        if (to[y] < 0) continue;
+                        const int from = y * 8 + (static_cast<int>(lane) >> 2);
+                        const float4 p = stage[from * 8 + ((2 * piece) ^ (from & 7))];
+                        const float4 q = stage[from * 8 + ((2 * piece + 1) ^ (from & 7))];
+                        const float v[8] = {p.x, p.y, p.z, p.w, q.x, q.y, q.z, q.w};
+                        *reinterpret_cast<uint4*>(static_cast<T*>(a.out) + to[y] + c) = pack8(v, T{});
+                    }
+                }
+                if (valid && a.lse)
+                    a.lse[static_cast<long long>(it.begin + tok) * a.Hq + it.h * a.group + row_head] = lse_of(m2, l);
+                // a row that is not finite: the tile is done again (before the item is given up, so that the
+                // loading warp learns of it in time)
+                if (!it.redo) {
+                    const bool fine = !valid || check[0] + check[1] + check[2] + check[3] == 0.0f;
+                    if (!named_bar_and(bar, kRowThreads, fine) && row == 0) {
+                        const unsigned int at = s.redo_count[w];
+                        s.redo[w][at % kRedo] = it.id;
+                        __threadfence_block();
+                        *reinterpret_cast<volatile unsigned int*>(&s.redo_count[w]) = at + 1;
+                    }
+                }
+                ++used;
+                mbar_arrive(&s.item_empty[count % kAhead]);
+            }
+        }
+    }
+
+    tc_fence_before();
+    __syncthreads();
+    if (warp == 2) {
+        __syncwarp();
+        tc_fence_after();
+        tmem_dealloc(tmem, kTmemCols);
+    }
+}
+
+// ---------------------------------------------------------------------------
+// Host side.
+// ---------------------------------------------------------------------------
+template <typename T, int D>
+dspark_status launch_typed(const void* q, const void* k, const void* v, long long q_stride, long long k_stride,
+                           long long v_stride, const PromptArgs& a, int grid, cudaStream_t stream) {
+    const uint64_t e = sizeof(T);
+    CUtensorMap mq, mk, mv;
+    const uint64_t qd[3] = {static_cast<uint64_t>(D), static_cast<uint64_t>(a.Hq), static_cast<uint64_t>(a.T)};
+    const uint64_t kd[3] = {static_cast<uint64_t>(D), static_cast<uint64_t>(a.Hkv), static_cast<uint64_t>(a.T)};
+    const uint64_t qs[2] = {D * e, q_stride * e}, ks[2] = {D * e, k_stride * e}, vs[2] = {D * e, v_stride * e};
+    const uint32_t qb[3] = {64, static_cast<uint32_t>(a.group), static_cast<uint32_t>(a.tile_tokens)};
+    const uint32_t kb[3] = {64, 1, kTile};
+    if (!make_tensor_map(&mq, HalfType<T>::kMapType, 3, q, qd, qs, qb, CU_TENSOR_MAP_SWIZZLE_128B) ||
+        !make_tensor_map(&mk, HalfType<T>::kMapType, 3, k, kd, ks, kb, CU_TENSOR_MAP_SWIZZLE_128B) ||
+        !make_tensor_map(&mv, HalfType<T>::kMapType, 3, v, kd, vs, kb, CU_TENSOR_MAP_SWIZZLE_128B))
+        return DSPARK_ERR_CUDA;
+    prompt_plan_kernel<<<1, kPlanThreads, 0, stream>>>(a);
+    cudaError_t err = cudaGetLastError();
+    if (err != cudaSuccess) return cuda_error(err, "launch(prompt_attention plan)");
+    constexpr size_t kSmem = sizeof(PromptSmem<D>);
+    static_assert(kSmem <= 227 * 1024, "shared memory of one SM");
+    err = cudaFuncSetAttribute(prompt_attention_kernel<T, D>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                               static_cast<int>(kSmem));
+    if (err == cudaSuccess)
+        err = launch_dependent(prompt_attention_kernel<T, D>, dim3(grid), dim3(kThreads), kSmem, stream, mq, mk, mv, a);
+    if (err != cudaSuccess) return cuda_error(err, "launch(prompt_attention)");
+    return DSPARK_OK;
+}
+
+// Items, without the heads, of T tokens in B sequences with at most `heads` query heads to a key head.
+long long items_bound(int B, int T, int heads) {
+    const int tokens = 2 * (kTile / std::min(heads, kTile));
+    return static_cast<long long>(B) + T / tokens;
 }
 
 }  // namespace
+
+size_t prompt_attention_workspace_bytes(int B, int T, int Hq) {
+    if (B < 1 || T < 1 || Hq < 1) return 0;
+    return sizeof(Plan) + static_cast<size_t>(items_bound(B, T, Hq)) * sizeof(int4);
+}
 
 dspark_status launch_prompt_attention(const void* q, const void* k, const void* v, dspark_dtype dtype,
                                       long long q_stride, long long k_stride, long long v_stride,
                                       const int32_t* cu_seqlens, float scale, int causal, int B, int T, int Hq,
                                       int Hkv, int D, void* out, float* lse, void* ws, cudaStream_t stream,
-                                      const DeviceInfo&) {
-    dspark_status st = clear_workspace(ws, sizeof(WsHeader), stream);
-    if (st != DSPARK_OK) return st;
-    PromptArgs a{q, k, v, q_stride, k_stride, v_stride, cu_seqlens, causal, B, T, Hq, Hkv, scale, out, lse,
-                 static_cast<WsHeader*>(ws)};
-    const long long blocks = (static_cast<long long>(T) * Hq + 3) / 4;
-    if (blocks >= (1ll << 31)) {
-        set_error("prompt_attention: too many rows (T=%d Hq=%d)", T, Hq);
+                                      const DeviceInfo& dev) {
+    PromptArgs a{};
+    a.cu_seqlens = cu_seqlens;
+    a.causal = causal;
+    a.B = B;
+    a.T = T;
+    a.Hq = Hq;
+    a.Hkv = Hkv;
+    a.group = Hq / Hkv;
+    a.tile_tokens = kTile / a.group;
+    a.scale = scale;
+    a.out = out;
+    a.lse = lse;
+    a.plan = static_cast<Plan*>(ws);
+    a.items = reinterpret_cast<int4*>(static_cast<uint8_t*>(ws) + sizeof(Plan));
+    a.timeout_ns = kDefaultTimeoutNs;
+    if (items_bound(B, T, a.group) * Hkv >= (1ll << 30)) {
+        set_error("prompt_attention: too much work for one call (B=%d T=%d Hq=%d Hkv=%d)", B, T, Hq, Hkv);
         return DSPARK_ERR_UNSUPPORTED;
     }
-    const unsigned grid = static_cast<unsigned>(blocks);
-    if (dtype == DSPARK_BF16) {
-        if (D == 64) prompt_attention_kernel<__nv_bfloat16, 64><<<grid, 128, 0, stream>>>(a);
-        else prompt_attention_kernel<__nv_bfloat16, 128><<<grid, 128, 0, stream>>>(a);
-    } else {
-        if (D == 64) prompt_attention_kernel<__half, 64><<<grid, 128, 0, stream>>>(a);
-        else prompt_attention_kernel<__half, 128><<<grid, 128, 0, stream>>>(a);
-    }
-    const cudaError_t e = cudaGetLastError();
-    if (e != cudaSuccess) return cuda_error(e, "launch(prompt_attention)");
-    return DSPARK_OK;
+    if (dtype == DSPARK_BF16)
+        return D == 64 ? launch_typed<__nv_bfloat16, 64>(q, k, v, q_stride, k_stride, v_stride, a, dev.sm_count, stream)
+                       : launch_typed<__nv_bfloat16, 128>(q, k, v, q_stride, k_stride, v_stride, a, dev.sm_count, stream);
+    return D == 64 ? launch_typed<__half, 64>(q, k, v, q_stride, k_stride, v_stride, a, dev.sm_count, stream)
+                   : launch_typed<__half, 128>(q, k, v, q_stride, k_stride, v_stride, a, dev.sm_count, stream);
 }
 
 }  // namespace dspark

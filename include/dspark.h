@@ -117,7 +117,7 @@ typedef enum {
  *   DSPARK_OP_KV_APPEND     256 (the status word)
  *   DSPARK_OP_PAGED_ATTENTION  partial results of split requests and their counters;
  *                           B, N as the call's, V = Hq, r = D
- *   DSPARK_OP_PROMPT_ATTENTION 256 (the status word)
+ *   DSPARK_OP_PROMPT_ATTENTION  the list of its work items; B as the call's, N = T, V = Hq
  *   DSPARK_OP_SAMPLE        256 (the status word)
  * Returns 0 for an unknown op or negative sizes.
  */
@@ -611,7 +611,7 @@ DSPARK_API dspark_status dspark_paged_attention(const void* q, const void* k_cac
  * 8, at least a token's row and below 2^31.
  * Device-side: an entry of cu_seqlens out of [0, T] or below one before it sets INPUT_RANGE and is
  * read as the nearest value that is neither.
- * workspace: >= dspark_workspace_size(DSPARK_OP_PROMPT_ATTENTION, B, T, Hq, D).
+ * workspace: >= dspark_workspace_size(DSPARK_OP_PROMPT_ATTENTION, B, T, Hq, 0).
  */
 DSPARK_API dspark_status dspark_prompt_attention(const void* q, const void* k, const void* v, dspark_dtype dtype,
                                long long q_stride, long long k_stride, long long v_stride,

@@ -24,8 +24,10 @@ def _refused(fn, good, changes):
 
 
 def test_workspace_sizes(L):
-    for op in (8, 11, 12):
+    for op in (8, 12):
         assert L.dspark_workspace_size(op, 4, 4, 1000, 64) == 256
+    assert L.dspark_workspace_size(11, 4, 1000, 16, 0) >= 256 + 16 * (4 + 1000 // 64)
+    assert L.dspark_workspace_size(11, 4, 0, 16, 0) == 0
     assert L.dspark_workspace_size(10, 4, 4, 32, 128) >= 256
     assert L.dspark_workspace_size(10, 0, 4, 32, 128) == 0
 
@@ -49,7 +51,8 @@ def test_paged_attention(L):
 
 
 def test_prompt_attention(L):
-    good = [FAKE, FAKE, FAKE, 2, 1024, 256, 256, FAKE, 0.1, 1, 2, 50, 16, 4, 64, FAKE, NULL, FAKE, 256, NULL]
+    need = L.dspark_workspace_size(11, 2, 50, 16, 0)
+    good = [FAKE, FAKE, FAKE, 2, 1024, 256, 256, FAKE, 0.1, 1, 2, 50, 16, 4, 64, FAKE, NULL, FAKE, need, NULL]
     _refused(L.dspark_prompt_attention, good, [
         (0, NULL), (1, NULL), (2, ODD), (3, 0), (4, 1020), (5, 128), (6, 1 << 31), (7, NULL), (8, math.nan), (10, 0),
         (11, 0), (11, (1 << 24) + 1), (12, 15), (13, 0), (14, 80), (15, NULL), (18, 16)])
