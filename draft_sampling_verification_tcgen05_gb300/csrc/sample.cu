@@ -4,21 +4,28 @@
 // is described by its last entry, the cut, and every sum is of integers (a weight's mass is
 // floor(w * 2^40)), so the cut, the total and the token depend on no order of summation.
 //
-// A cluster of 1 to 16 blocks holds one row in shared memory, read once from memory; the passes below
-// run on that copy, partial sums and counts travel through distributed shared memory.  What a row
-// needs, and no more, is done:
-//   1. load the row, its largest logit m, and each thread's largest (their smallest bounds a range)
-//   2. with top-k (k up to the number of threads): a histogram of the threads' largest logits gives a
-//      bound that at least k entries reach; those entries, usually a few more than k, go to a list
-//      that one block sorts, and min-p and top-p are settled on the list
+// With as many rows as SMs a row is a block's, which passes over it in memory (the rows under way
+// fit the L2 cache, so later passes find them there); with fewer rows a cluster of 2 to 16 blocks
+// shares a row, each with a copy of its part in shared memory.  Sums, counts and lists then travel as
+// asynchronous stores into the receiving block's shared memory that complete on an mbarrier there (a
+// cluster's barrier waits for all earlier stores: 2000 cycles and more each time, an exchange takes a
+// third of that).  A warp passes over a run of neighbouring entries, so sums by id come with any pass.
+// What a row needs, and no more, is done:
+//   1. the largest entry, and the largest of each thread; a greedy row is settled by that
+//   2. with a small top-k: a histogram of the largest logits of groups of entries (at least 2 k groups)
+//      gives a bound that at least k entries reach; those entries, usually a few more than k, go to a
+//      list, and one block settles min-p, top-p and the token on it: a histogram of counts and masses
+//      over 1024 parts of the range, then over the part that holds the cut, until that is one entry
 //   3. else the total mass of the entries that min-p leaves; entries of mass at most (Q - need) / count
-//      cannot be needed for top-p, and if the others fit, they go to the list in the same way
-//   4. else (a wide nucleus, a very large k) the cut is closed in on: a histogram of counts over 2048
-//      parts of the range, bounds of each part's mass from its edges, the parts that can hold the cut
-//      are the next range, and the mass above it is summed exactly; once the range's entries fit the
-//      list, it is sorted; a range of one repeated logit is settled by id
-//   5. one pass sums the kept masses of contiguous runs and writes the probabilities; the run that
-//      holds the drawn mass is gone through again for the token
+//      cannot be needed for top-p
+//   4. the cut is closed in on among the others: a histogram of counts over 2048 parts of their range,
+//      bounds of each part's mass from its edges, the parts that can hold the cut are the next range,
+//      and the mass above it is summed exactly; once the range's entries fit the list, they are settled
+//      there; a range of one repeated logit is settled by id
+//   5. the token, where the list did not give it: kept masses of the runs, then the run that holds the
+//      drawn mass again.  Probabilities: zeros and the list's entries, or a pass over the row
+// A row that needs 3 and 4 is bound by its instructions (an exponential and an exact mass per entry and
+// pass), the others by memory.
 #include "device_common.cuh"
 #include "half_common.cuh"
 #include "host_common.h"
@@ -28,12 +35,15 @@
 namespace dspark {
 namespace {
 
-constexpr int kThreads = 512;
+constexpr int kThreads = 1024;
 constexpr int kWarps = kThreads / 32;
 constexpr int kMaxCluster = 16;
 constexpr int kList = 2048;                // entries of the list
 constexpr int kBins = 2048;
 constexpr int kPerThread = kBins / kThreads;
+constexpr int kParts = kThreads;           // of the list's range, a thread each
+constexpr int kBatch = 4;                  // 16-byte pieces that a thread has under way
+constexpr uint32_t kWaitPeer = 0xA01;
 
 struct SampleArgs {
     const void* logits;
@@ -41,8 +51,8 @@ struct SampleArgs {
     const int32_t* top_k;
     const float *top_p, *min_p, *u;
     int R, V;
-    int cluster, slice;                    // blocks of a row, entries of a block (a multiple of 8)
-    int resident;                          // the slice is held in shared memory
+    int cluster, slice;                    // blocks of a row, entries of a block
+    int resident;                          // a block's part is held in shared memory
     int32_t* tokens;
     float* probs;
     WsHeader* ws;
@@ -56,31 +66,24 @@ __device__ __forceinline__ uint32_t cluster_rank() {
     return r;
 }
 
-__device__ __forceinline__ void cluster_sync() {
-    asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
-}
-
-// Address of the same shared variable in block `rank` of the cluster, and accesses through it.
+// Address of the same shared variable in block `rank` of the cluster.
 __device__ __forceinline__ uint32_t remote(const void* p, uint32_t rank) {
     uint32_t r;
     asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(r) : "r"(smem_u32(p)), "r"(rank));
     return r;
 }
-__device__ __forceinline__ void remote_store(uint32_t at, u64 v) {
-    asm volatile("st.shared::cluster.u64 [%0], %1;" :: "r"(at), "l"(v) : "memory");
+// Asynchronous stores and an addition there, counted in bytes on an mbarrier of the same block.
+__device__ __forceinline__ void send(uint32_t at, u64 v, uint32_t bar) {
+    asm volatile("st.async.weak.shared::cluster.mbarrier::complete_tx::bytes.b64 [%0], %1, [%2];"
+                 :: "r"(at), "l"(v), "r"(bar) : "memory");
 }
-__device__ __forceinline__ void remote_add(uint32_t at, uint32_t v) {
-    asm volatile("red.shared::cluster.add.u32 [%0], %1;" :: "r"(at), "r"(v) : "memory");
+__device__ __forceinline__ void send32(uint32_t at, uint32_t v, uint32_t bar) {
+    asm volatile("st.async.weak.shared::cluster.mbarrier::complete_tx::bytes.b32 [%0], %1, [%2];"
+                 :: "r"(at), "r"(v), "r"(bar) : "memory");
 }
-__device__ __forceinline__ uint32_t remote_take(uint32_t at, uint32_t v) {
-    uint32_t old;
-    asm volatile("atom.shared::cluster.add.u32 %0, [%1], %2;" : "=r"(old) : "r"(at), "r"(v) : "memory");
-    return old;
-}
-__device__ __forceinline__ uint32_t remote_load(uint32_t at) {
-    uint32_t v;
-    asm volatile("ld.shared::cluster.u32 %0, [%1];" : "=r"(v) : "r"(at) : "memory");
-    return v;
+__device__ __forceinline__ void send_add(uint32_t at, uint32_t v, uint32_t bar) {
+    asm volatile("red.async.relaxed.cluster.shared::cluster.mbarrier::complete_tx::bytes.add.u32 [%0], %1, [%2];"
+                 :: "r"(at), "r"(v), "r"(bar) : "memory");
 }
 
 __device__ __forceinline__ float to_float(float x) { return x; }
@@ -91,34 +94,69 @@ __device__ __forceinline__ u64 share_of(u64 total, uint32_t frac) {
     return (total >> 24) * frac + (((total & 0xFFFFFFull) * frac) >> 24);
 }
 
-// floor(w * 2^40) in two halves of at most 20 bits (w <= 1): both scalings by 2^20 are exact, and
-// 32-bit conversions and additions are cheaper than 64-bit ones.
+// floor(w * 2^40) in two halves of 20 bits, w <= 1.  Scalings by 2^20 are exact; adding 2^23 rounded toward
+// zero leaves the floor of a value below 2^23 in the low bits (a conversion instruction runs at an
+// eighth of an addition's rate).  The halves come with 2^23's bits, kHalfBias, on top.
+constexpr uint32_t kHalfBias = 0x4B000000u;
+__device__ __forceinline__ void mass_halves_biased(float w, uint32_t& hi, uint32_t& lo) {
+    const float s = __fmul_rn(w, 0x1p20f), t = __fadd_rz(s, 0x1p23f);
+    hi = __float_as_uint(t);
+    lo = __float_as_uint(__fadd_rz(__fmul_rn(__fsub_rn(s, __fsub_rn(t, 0x1p23f)), 0x1p20f), 0x1p23f));
+}
 __device__ __forceinline__ void mass_halves(float w, uint32_t& hi, uint32_t& lo) {
-    const float s = __fmul_rn(w, 0x1p20f);
-    hi = static_cast<uint32_t>(s);
-    lo = static_cast<uint32_t>(__fmul_rn(__fsub_rn(s, static_cast<float>(hi)), 0x1p20f));
+    mass_halves_biased(w, hi, lo);
+    hi -= kHalfBias;
+    lo -= kHalfBias;
 }
 __device__ __forceinline__ u64 mass_of(float w) {
     uint32_t hi, lo;
     mass_halves(w, hi, lo);
     return (static_cast<u64>(hi) << 20) + lo;
 }
+// A sum of masses, of fewer than 4096 entries.
+struct MassSum {
+    uint32_t hi = 0, lo = 0, n = 0;
+    __device__ __forceinline__ void add(float w) {
+        uint32_t h, l;
+        mass_halves_biased(w, h, l);
+        hi += h;
+        lo += l;
+        ++n;
+    }
+    __device__ __forceinline__ u64 value() const {
+        return (static_cast<u64>(hi - n * kHalfBias) << 20) + (lo - n * kHalfBias);
+    }
+};
+// floor(y) for 0 <= y < 2^23, likewise.
+__device__ __forceinline__ int floor_of(float y) {
+    return static_cast<int>(__float_as_uint(__fadd_rz(y, 0x1p23f)) - kHalfBias);
+}
 
 struct alignas(16) Shared {
     u64 red[2][kMaxCluster][4];            // values exchanged by the blocks, two exchanges in turn
-    u64 list[kList];                       // of the first block: argmax keys
-    uint32_t hist[kBins];                  // counts, all blocks' in the first one
-    uint32_t list_count, pad;
-    u64 found;                             // the entry that locate() was asked for
+    union {
+        u64 list[kList];                   // argmax keys: of this block, then in the first block of all
+        struct {                           // while there is no list:
+            uint32_t share[kBins];         // all blocks' counts of the bins that this block adds up
+            uint32_t bins[kBins];          // in the first block: all blocks' counts
+        };
+    };
+    uint32_t hist[3 * kParts];             // counts (kBins), or on the list counts and masses' halves of kParts parts
     u64 segment[kMaxCluster * kWarps];     // of the first block: mass or count of each warp's run
     u64 warp_sum[4][kWarps];
     u64 out[4];                            // what the first block tells the others
+    u64 run[kWarps];                       // mass of the list's entries in each run of this block
+    u64 found;                             // the entry that locate() was asked for
+    uint32_t list_count, pad;
+    u64 bar_red[2], bar_out, bar_hist, bar_list, bar_segment, bar_found, bar_share, bar_bins;
 };
+
+static_assert(3 * kParts >= kBins, "one array for both histograms");
 
 struct Reduced { u64 a, b, c, d; };
 
 template <typename T>
-__global__ void __launch_bounds__(kThreads) sample_kernel(const __grid_constant__ SampleArgs p) {
+__global__ void __launch_bounds__(kThreads, 1) sample_kernel(const __grid_constant__ SampleArgs p) {
     extern __shared__ __align__(16) uint8_t smem_raw[];
     Shared& s = *reinterpret_cast<Shared*>(smem_raw);
     T* const held = reinterpret_cast<T*>(smem_raw + sizeof(Shared));
@@ -129,7 +167,26 @@ __global__ void __launch_bounds__(kThreads) sample_kernel(const __grid_constant_
     const long long r = blockIdx.x / C;
     const T* const global = static_cast<const T*>(p.logits) + r * V;
     const int v0 = min(V, static_cast<int>(rank) * p.slice), v1 = min(V, v0 + p.slice), n = v1 - v0;
-    auto sync = [&] { if (C > 1) cluster_sync(); else __syncthreads(); };
+
+    for (int i = tid; i < kBins; i += kThreads) s.hist[i] = 0u;
+    if (tid == 0) s.list_count = 0u;
+    if (C > 1) {
+        if (tid == 0) {
+            for (u64* b = s.bar_red; b <= &s.bar_bins; ++b) mbar_init(reinterpret_cast<uint64_t*>(b), 1);
+            fence_mbarrier_init();
+        }
+        __syncthreads();
+        // the others may write here from now on; waited for ahead of the first exchange
+        asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
+    }
+    // Waits for `bytes` that other blocks send to `bar` here; `uses` counts its phases.
+    auto receive = [&](u64& bar, int& uses, uint32_t bytes) {
+        uint64_t* b = reinterpret_cast<uint64_t*>(&bar);
+        if (tid == 0) mbar_arrive_expect_tx(b, bytes);
+        mbar_wait(b, static_cast<uint32_t>(uses++) & 1u, p.ws, kDefaultTimeoutNs, kWaitPeer);
+    };
+    int used_red[2] = {0, 0}, used_out = 0, used_hist = 0, used_list = 0, used_segment = 0, used_found = 0, used_share = 0,
+        used_bins = 0;
 
     // ---- parameters, each read as the nearest valid value ----
     uint32_t flags = 0;
@@ -146,23 +203,26 @@ __global__ void __launch_bounds__(kThreads) sample_kernel(const __grid_constant_
 
     // Ordered bits of an entry; 0 for one that takes no part (NaN, infinities).
     auto bits = [](float x) { return x < INFINITY && x > -INFINITY ? float_order_bits(x) : 0u; };
+    auto key_of = [](float x, int v) { return argmax_key(x, static_cast<uint32_t>(v)); };
+    auto key_logit = [](u64 key) { return float_from_order_bits(static_cast<uint32_t>(key >> 32)); };
 
     // ---- exchanges ----
     int turn = 0;
     // Every block's four values, added up (a, b) or by maximum (c, d); the arguments count in thread 0 only.
+    // Afterwards s.red[turn ^ 1][i] holds block i's.
     auto exchange = [&](u64 a, u64 b, u64 c, u64 d) {
-        Reduced x{a, b, c, d};
         if (tid == 0) {
             u64* mine = s.red[turn][rank];
             mine[0] = a; mine[1] = b; mine[2] = c; mine[3] = d;
         }
+        __syncthreads();
         if (C > 1) {
-            __syncthreads();
-            if (tid < C * 4 && static_cast<uint32_t>(tid >> 2) != rank)
-                remote_store(remote(&s.red[turn][rank][tid & 3], static_cast<uint32_t>(tid >> 2)), s.red[turn][rank][tid & 3]);
+            const uint32_t to = static_cast<uint32_t>(tid >> 2);
+            if (tid < C * 4 && to != rank)
+                send(remote(&s.red[turn][rank][tid & 3], to), s.red[turn][rank][tid & 3], remote(&s.bar_red[turn], to));
+            receive(s.bar_red[turn], used_red[turn], static_cast<uint32_t>(C - 1) * 32u);
         }
-        sync();
-        x = Reduced{0, 0, 0, 0};
+        Reduced x{0, 0, 0, 0};
         for (int i = 0; i < C; ++i) {
             const u64* y = s.red[turn][i];
             x.a += y[0];
@@ -173,12 +233,13 @@ __global__ void __launch_bounds__(kThreads) sample_kernel(const __grid_constant_
         turn ^= 1;
         return x;
     };
-    // Sums (a, b) and maxima (c, d) over the block's threads, in thread 0, then exchanged.
-    auto reduce = [&](u64 a, u64 b, u64 c, u64 d) {
+    // Sums (a, b) and maxima (c, d) over the block's threads, in its first warp.
+    auto block = [&](u64& a, u64& b, u64& c, u64& d) {
         a = warp_sum_u64(a);
         b = warp_sum_u64(b);
         c = warp_max_u64(c);
         d = warp_max_u64(d);
+        __syncthreads();
         if (lane == 0) {
             s.warp_sum[0][warp] = a;
             s.warp_sum[1][warp] = b;
@@ -187,250 +248,460 @@ __global__ void __launch_bounds__(kThreads) sample_kernel(const __grid_constant_
         }
         __syncthreads();
         if (warp == 0) {
-            const bool in = lane < kWarps;
-            a = warp_sum_u64(in ? s.warp_sum[0][lane] : 0);
-            b = warp_sum_u64(in ? s.warp_sum[1][lane] : 0);
-            c = warp_max_u64(in ? s.warp_sum[2][lane] : 0);
-            d = warp_max_u64(in ? s.warp_sum[3][lane] : 0);
+            a = warp_sum_u64(s.warp_sum[0][lane]);
+            b = warp_sum_u64(s.warp_sum[1][lane]);
+            c = warp_max_u64(s.warp_sum[2][lane]);
+            d = warp_max_u64(s.warp_sum[3][lane]);
         }
+    };
+    static_assert(kWarps == 32, "a warp adds up the warps");
+    auto reduce = [&](u64 a, u64 b, u64 c, u64 d) {
+        block(a, b, c, d);
         return exchange(a, b, c, d);
+    };
+    // Inclusive sums over the block's threads, on top of a0 and b0.
+    auto scan = [&](u64& a, u64& b, u64 a0, u64 b0) {
+        for (int d = 1; d < 32; d <<= 1) {
+            const u64 y = __shfl_up_sync(0xFFFFFFFFu, a, d), z = __shfl_up_sync(0xFFFFFFFFu, b, d);
+            if (lane >= static_cast<uint32_t>(d)) {
+                a += y;
+                b += z;
+            }
+        }
+        if (lane == 31) {
+            s.warp_sum[0][warp] = a;
+            s.warp_sum[1][warp] = b;
+        }
+        __syncthreads();
+        // the warps' sums ahead of this one
+        u64 y = lane < warp ? s.warp_sum[0][lane] : 0, z = lane < warp ? s.warp_sum[1][lane] : 0;
+        a += a0 + warp_sum_u64(y);
+        b += b0 + warp_sum_u64(z);
     };
     // What the first block has put into s.out, in every block.
     auto hear = [&] {
-        __syncthreads();
-        if (C > 1 && rank == 0 && tid < C * 4 && (tid >> 2) != 0)
-            remote_store(remote(&s.out[tid & 3], static_cast<uint32_t>(tid >> 2)), s.out[tid & 3]);
-        sync();
+        if (rank == 0) {
+            __syncthreads();
+            const uint32_t to = static_cast<uint32_t>(tid >> 2);
+            if (tid < C * 4 && to != 0) send(remote(&s.out[tid & 3], to), s.out[tid & 3], remote(&s.bar_out, to));
+        } else {
+            receive(s.bar_out, used_out, 32u);
+        }
     };
 
-    // ---- 1. the row ----
-    // Entry v is held at v - v0 + pad, so that 16-byte pieces of the row stay pieces in shared memory.
+    // ---- the row, in 16-byte pieces: entry e of piece i is place0 + i * kPiece + e ----
+    // The first and last piece may reach into the rows beside this one; in shared memory they stay pieces.
     constexpr int kPiece = 16 / sizeof(T);
-    const int pad = p.resident ? static_cast<int>((reinterpret_cast<uintptr_t>(global + v0) & 15u) / sizeof(T)) : 0;
-    const T* const row = p.resident ? held + pad - v0 : global;              // row[v], v in [v0, v1)
-    uint32_t top = 0, odd = 0;
-    auto look = [&](float x) {
-        if (!(x < INFINITY)) odd = 1;                                         // NaN and +infinity; not -infinity
-        top = max(top, bits(x));
+    const int pad = static_cast<int>((reinterpret_cast<uintptr_t>(global + v0) & 15u) / sizeof(T));
+    const int pieces = n > 0 ? (pad + n + kPiece - 1) / kPiece : 0, place0 = v0 - pad;
+    const uint4* const row16 = reinterpret_cast<const uint4*>(global + place0);
+    const int per_run = (pieces + kWarps - 1) / kWarps;
+    const int run0 = min(pieces, static_cast<int>(warp) * per_run), run1 = min(pieces, run0 + per_run);   // this warp's
+    auto whole = [&](int i) { return place0 + i * kPiece >= v0 && place0 + (i + 1) * kPiece <= v1; };
+    auto fetch = [&](int i, bool from_memory) {                               // piece i; 0 outside the row
+        if (!from_memory) return reinterpret_cast<const uint4*>(held)[i];
+        if (whole(i)) return __ldg(row16 + i);
+        T y[kPiece];
+        for (int e = 0; e < kPiece; ++e) {
+            const int v = place0 + i * kPiece + e;
+            y[e] = v >= v0 && v < v1 ? global[v] : T(0.0f);
+        }
+        return *reinterpret_cast<const uint4*>(y);
     };
-    if (p.resident) {
-        const int pieces = (pad + n + kPiece - 1) / kPiece;
-        const T* const base = global + v0 - pad;
-#pragma unroll 4
-        for (int i = tid; i < pieces; i += kThreads) {
-            T x[kPiece];
-            const int first = i * kPiece - pad;                               // of the piece, in the slice
-            if (first >= 0 && first + kPiece <= n) {
-                *reinterpret_cast<uint4*>(x) = *reinterpret_cast<const uint4*>(base + i * kPiece);
+    auto unpack = [&](const uint4& w, int i, float (&x)[kPiece]) {            // as fp32; NaN outside the row
+        T y[kPiece];
+        *reinterpret_cast<uint4*>(y) = w;
 #pragma unroll
-                for (int e = 0; e < kPiece; ++e) look(to_float(x[e]));
-                *reinterpret_cast<uint4*>(held + i * kPiece) = *reinterpret_cast<const uint4*>(x);
-            } else {
-                for (int e = 0; e < kPiece; ++e) {
-                    if (first + e < 0 || first + e >= n) continue;
-                    const T y = base[i * kPiece + e];
-                    look(to_float(y));
-                    held[i * kPiece + e] = y;
-                }
+        for (int e = 0; e < kPiece; ++e) x[e] = to_float(y[e]);
+        if (!whole(i)) {
+#pragma unroll
+            for (int e = 0; e < kPiece; ++e) {
+                const int v = place0 + i * kPiece + e;
+                if (v < v0 || v >= v1) x[e] = NAN;
             }
         }
-    } else {
-        for (int v = v0 + tid; v < v1; v += kThreads) look(to_float(row[v]));
+    };
+    // Calls f(piece, its entries) for this warp's run, by whole warps; entries outside the row, and pieces past
+    // the run's end, come as NaN.
+    const int whole0 = pad > 0 ? 1 : 0, whole1 = min(run1, (pad + n) / kPiece);   // pieces wholly inside, of this run
+    auto pass = [&](bool from_memory, auto f) {
+        int i0 = run0;
+        for (; i0 < run1; ) {
+            const bool full = i0 >= whole0 && i0 + 32 * kBatch <= whole1;
+            if (full) {
+                uint4 w[kBatch];
+#pragma unroll
+                for (int j = 0; j < kBatch; ++j) {
+                    const int i = i0 + j * 32 + static_cast<int>(lane);
+                    w[j] = from_memory ? __ldg(row16 + i) : reinterpret_cast<const uint4*>(held)[i];
+                }
+#pragma unroll
+                for (int j = 0; j < kBatch; ++j) {
+                    T y[kPiece];
+                    *reinterpret_cast<uint4*>(y) = w[j];
+                    float x[kPiece];
+#pragma unroll
+                    for (int e = 0; e < kPiece; ++e) x[e] = to_float(y[e]);
+                    f(i0 + j * 32 + static_cast<int>(lane), x, w[j], j);
+                }
+                i0 += 32 * kBatch;
+            } else {
+                const int i = i0 + static_cast<int>(lane);
+                const uint4 w = i < run1 ? fetch(i, from_memory) : make_uint4(0u, 0u, 0u, 0u);
+                float x[kPiece];
+                unpack(w, i, x);
+                if (i >= run1) {
+#pragma unroll
+                    for (int e = 0; e < kPiece; ++e) x[e] = NAN;
+                }
+                f(i, x, w, 0);
+                i0 += 32;
+            }
+        }
+    };
+    const bool streamed = p.resident == 0;
+
+    // ---- 1. the largest entries ----
+    float tops[kBatch];                                                       // of this thread's pieces, in turn
+    int at[kBatch];
+#pragma unroll
+    for (int j = 0; j < kBatch; ++j) {
+        tops[j] = -INFINITY;
+        at[j] = 0;
     }
-    const uint32_t mine = top;                                                // this thread's largest
-    if (tid == 0) s.list_count = 0u;
-    for (int i = tid; i < kBins; i += kThreads) s.hist[i] = 0u;
-    // c: the largest; d: the smallest of the threads' largest, as its complement
-    Reduced x = reduce(odd, mine != 0 ? 1 : 0, mine, mine != 0 ? 0xFFFFFFFFu - mine : 0u);
+    uint32_t odd = 0;
+    pass(true, [&](int i, float (&x)[kPiece], const uint4& w, int j) {
+        if (!streamed && i < run1) reinterpret_cast<uint4*>(held)[i] = w;
+        float top = x[0], sum = x[0];
+#pragma unroll
+        for (int e = 1; e < kPiece; ++e) {
+            top = fmaxf(top, x[e]);
+            sum += x[e];
+        }
+        if (top == INFINITY || !(sum == sum)) {                               // rare: something that is skipped
+            top = -INFINITY;
+#pragma unroll
+            for (int e = 0; e < kPiece; ++e) {
+                const int v = place0 + i * kPiece + e;
+                if (!(x[e] < INFINITY)) odd |= i < run1 && v >= v0 && v < v1 ? 1u : 0u;    // not what lies outside
+                else top = fmaxf(top, x[e]);
+            }
+        }
+        if (top > tops[j]) {
+            tops[j] = top;
+            at[j] = i;
+        }
+    });
+    __syncwarp();
+    // this thread's largest entry: the first of them within the first piece that has it
+    u64 best = 0;
+    {
+        float top = tops[0];
+        int i = at[0];
+#pragma unroll
+        for (int j = 1; j < kBatch; ++j)
+            if (tops[j] > top || (tops[j] == top && at[j] < i)) {
+                top = tops[j];
+                i = at[j];
+            }
+        if (top > -INFINITY) {
+            float x[kPiece];
+            unpack(fetch(i, streamed), i, x);
+#pragma unroll
+            for (int e = kPiece - 1; e >= 0; --e)
+                if (x[e] == top) best = key_of(top, place0 + i * kPiece + e);
+        }
+    }
+    if (C > 1) asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
+    // For a small top-k: groups of entries, at least 2 k of them if there can be, and their largest: 1 to 32
+    // threads' entries, or a thread's every kBatch-th piece.
+    int span = 32;
+    while (span > 1 && (C * kThreads) / span < 2 * k) span >>= 2;             // 32, 8, 2, 0: single threads
+    span = max(span, 1);
+    const bool fine = C * kThreads < 2 * k;
+    uint32_t group = static_cast<uint32_t>(best >> 32);
+    for (int d = 1; d < span; d <<= 1) group = max(group, __shfl_xor_sync(0xFFFFFFFFu, group, d));
+    uint32_t leads = group != 0 && (lane & (span - 1)) == 0 ? 1u : 0u, least_group = group;
+    if (fine) {
+        leads = 0;
+        least_group = 0xFFFFFFFFu;
+#pragma unroll
+        for (int j = 0; j < kBatch; ++j) {
+            const uint32_t b = bits(tops[j]);
+            if (b == 0) continue;
+            ++leads;
+            least_group = min(least_group, b);
+        }
+        if (leads == 0) least_group = 0;
+    }
+    // c: the largest entry; d: the smallest of the groups' largest, as its complement
+    const Reduced x = reduce(odd, leads, best, least_group != 0 ? 0xFFFFFFFFu - least_group : 0u);
     if (x.a != 0) flags |= DSPARK_STATUS_NUMERIC;
-    const uint32_t top_bits = static_cast<uint32_t>(x.c);
+    const uint32_t top_bits = static_cast<uint32_t>(x.c >> 32);
     if (top_bits == 0) flags |= DSPARK_STATUS_NUMERIC;
     if (rank == 0 && tid == 0 && flags) set_status(p.ws, flags);
     const float m = float_from_order_bits(top_bits);
-    const int groups = static_cast<int>(x.b);                                 // threads with an entry
+    const int groups = static_cast<int>(x.b);                                 // groups with an entry
     const float bottom = float_from_order_bits(0xFFFFFFFFu - static_cast<uint32_t>(x.d));
 
     auto weight = [&](float l) { return expf(__fmul_rn(__fsub_rn(l, m), inv)); };
 
-    u64 cut = 0, total = 0;                                                   // the kept set: argmax_key >= cut; its mass
+    u64 cut = 0, total = 0;                                                   // the kept set: key >= cut; its mass
     u64 limit = 0;                                                            // likewise after top-k, while top-p is sought
-    // Entries that min-p and `limit` leave.  Calls f(bits, id, logit).
-    auto each = [&](auto f) {
-        for (int v = v0 + tid; v < v1; v += kThreads) {
-            const float l = to_float(row[v]);
-            const uint32_t b = bits(l);
-            if (b != 0 && argmax_key(l, static_cast<uint32_t>(v)) >= limit) f(b, v, l);
-        }
+    int token = -1;                                                           // once it is known
+    bool in_list = false;                                                     // the blocks' lists hold the kept set
+    // Calls f(logit, id, whether it takes part so far) for the entries of at least `least`, where few are: by
+    // whole warps, a warp being there as long as one of its entries is.
+    auto each = [&](float least, auto f) {
+        pass(streamed, [&](int i, const float (&x)[kPiece], const uint4&, int) {
+            float top = x[0];
+#pragma unroll
+            for (int e = 1; e < kPiece; ++e) top = fmaxf(top, x[e]);
+            if (!__any_sync(0xFFFFFFFFu, top >= least)) return;
+#pragma unroll
+            for (int e = 0; e < kPiece; ++e) {
+                bool in = x[e] >= least && x[e] < INFINITY;
+                if (!__any_sync(0xFFFFFFFFu, in)) continue;
+                const int v = place0 + i * kPiece + e;
+                if (limit != 0) in = in && key_of(x[e], v) >= limit;
+                f(x[e], v, in);
+            }
+        });
     };
-    // Entries for which in(bits, id, logit) holds go to the list; returns how many there are (the list
-    // holds them if they are no more than kList).
-    auto append = [&](bool yes, float l, int v) {                             // warp-converged
+    // The same, by threads, where many are: only for those that take part.
+    auto every = [&](float least, auto f) {
+        pass(streamed, [&](int i, const float (&x)[kPiece], const uint4&, int) {
+#pragma unroll
+            for (int e = 0; e < kPiece; ++e) {
+                if (!(x[e] >= least && x[e] < INFINITY)) continue;
+                const int v = place0 + i * kPiece + e;
+                if (limit != 0 && key_of(x[e], v) < limit) continue;
+                f(x[e], v);
+            }
+        });
+    };
+    // Entries for which `yes` go to this block's list, as long as they fit.
+    auto append = [&](bool yes, float l, int v) {
         const uint32_t vote = __ballot_sync(0xFFFFFFFFu, yes);
         if (vote == 0) return;
         uint32_t at = 0;
-        const uint32_t count_at = C > 1 ? remote(&s.list_count, 0) : 0;
-        if (lane == 0) at = C > 1 ? remote_take(count_at, __popc(vote)) : atomicAdd(&s.list_count, __popc(vote));
+        if (lane == 0) at = atomicAdd(&s.list_count, __popc(vote));
         at = __shfl_sync(0xFFFFFFFFu, at, 0) + __popc(vote & ((1u << lane) - 1u));
-        if (yes && at < kList) {
-            const u64 key = argmax_key(l, static_cast<uint32_t>(v));
-            if (C > 1) remote_store(remote(&s.list[at], 0), key);
-            else s.list[at] = key;
-        }
+        if (yes && at < kList) s.list[at] = key_of(l, v);
     };
-    auto each_converged = [&](auto f) {                                       // f is called by whole warps: in, id, logit
-        const int end = v0 + (n + 31) / 32 * 32;
-        for (int v = v0 + tid; v < end; v += kThreads) {
-            const float l = v < v1 ? to_float(row[v]) : -INFINITY;
-            f(bits(l) != 0 && argmax_key(l, static_cast<uint32_t>(v)) >= limit, v, l);
-        }
-    };
-
-    // Bitonic sort of list[0 .. size), size a power of two, the largest first, by the calling block.
-    auto sort = [&](int size) {
-        for (int span = 2; span <= size; span <<= 1)
-            for (int step = span >> 1; step > 0; step >>= 1) {
-                __syncthreads();
-                for (int i = tid; i < size / 2; i += kThreads) {
-                    const int a = 2 * i - (i & (step - 1)), b = a + step;
-                    const u64 ka = s.list[a], kb = s.list[b];
-                    if (((a & span) == 0) == (ka < kb)) {
-                        s.list[a] = kb;
-                        s.list[b] = ka;
-                    }
-                }
-            }
+    // The blocks' lists, one behind the other, in the first block, unless they are more than kList together;
+    // tells their number.  Every block's own entries stay the first s.list_count of its list.
+    auto gather = [&] {
         __syncthreads();
+        const uint32_t mine = s.list_count;
+        const Reduced all = exchange(mine, 0, 0, 0);
+        if (all.a <= kList && C > 1) {
+            if (rank != 0) {
+                uint32_t before = 0;
+                for (int i = 0; i < static_cast<int>(rank); ++i) before += static_cast<uint32_t>(s.red[turn ^ 1][i][0]);
+                for (uint32_t i = tid; i < mine; i += kThreads)
+                    send(remote(&s.list[before + i], 0), s.list[i], remote(&s.bar_list, 0));
+            } else {
+                receive(s.bar_list, used_list, 8u * static_cast<uint32_t>(all.a - mine));
+            }
+        }
+        __syncthreads();
+        if (tid == 0) s.list_count = all.a <= kList ? mine : 0u;
+        __syncthreads();
+        return static_cast<int>(min(all.a, static_cast<u64>(kList) + 1));
     };
-    auto key_logit = [&](u64 key) { return float_from_order_bits(static_cast<uint32_t>(key >> 32)); };
 
     // First block: settles the cut on the list of `count` entries, behind `above` entries of mass `over`: at
     // most kk entries in all, and of those as many as reach the mass `need` (~0: top-p's share of them).
-    // Leaves {cut, mass} in s.out.
+    // Leaves {cut, mass, token + 1 if nothing is above the list, else 0} in s.out.
     auto settle = [&](int count, u64 above, u64 over, u64 kk, u64 need) {
-        int size = 2;
-        while (size < count) size <<= 1;
-        for (int i = count + tid; i < size; i += kThreads) s.list[i] = 0;
-        sort(size);
-        // per thread kPerThread neighbours: masses, their prefix
+        // this thread's entries that take part, and their masses' halves
         constexpr int kPer = kList / kThreads;
-        u64 q[kPer], sum = 0;
+        u64 key[kPer];
+        uint32_t qh[kPer], ql[kPer];
+        u64 sum = 0, number = 0, low = 0, high = 0;
 #pragma unroll
         for (int e = 0; e < kPer; ++e) {
-            const int i = tid * kPer + e;
-            q[e] = 0;
-            if (i < count && above + static_cast<u64>(i) < kk) {
-                const float w = weight(key_logit(s.list[i]));
-                if (w >= min_p) q[e] = mass_of(w) + (1ull << 62);             // bit 62: it takes part
+            const int i = e * kThreads + tid;
+            key[e] = i < count ? s.list[i] : 0;
+            qh[e] = ql[e] = 0;
+            if (key[e] == 0) continue;
+            const float w = weight(key_logit(key[e]));
+            if (w < min_p) {
+                key[e] = 0;
+                continue;
             }
+            mass_halves(w, qh[e], ql[e]);
+            sum += (static_cast<u64>(qh[e]) << 20) + ql[e];
+            ++number;
+            low = max(low, ~key[e]);
+            high = max(high, key[e]);
         }
-        // the entries that take part are a prefix of the list: their masses' sum
-#pragma unroll
-        for (int e = 0; e < kPer; ++e) sum += q[e] & ~(1ull << 62);
-        u64 incl = sum;
-        for (int d = 1; d < 32; d <<= 1) {
-            const u64 y = __shfl_up_sync(0xFFFFFFFFu, incl, d);
-            if (lane >= static_cast<uint32_t>(d)) incl += y;
+        block(sum, number, low, high);
+        if (tid == 0) {
+            s.out[0] = sum;
+            s.out[1] = number;
+            s.out[2] = ~low;
+            s.out[3] = high;
         }
-        if (lane == 31) s.warp_sum[0][warp] = incl;
         __syncthreads();
-        u64 before = over + incl - sum, all = over;
-        for (uint32_t w = 0; w < kWarps; ++w) {
-            if (w < warp) before += s.warp_sum[0][w];
-            all += s.warp_sum[0][w];
-        }
-        if (need == ~0ull) need = share_of(all, P);
-        // kept: what takes part while the mass before it is short of what is needed (the first of all is kept
-        // anyway); the last of them is the cut
-        uint32_t last = 0;                                                    // its place + 1
-        u64 upto = 0;
+        sum = s.out[0];
+        number = s.out[1];
+        const u64 bottom_key = s.out[2], top_key = s.out[3];
+        // Of the entries with keys in [lo, hi], the largest key first, behind c_before entries of mass m_before:
+        // the first with which the count reaches want_count, or the mass want_mass (the other is ~0); it is
+        // there.  Returns its key, and the mass up to it.
+        auto descend = [&](const u64 (&key)[kPer], u64 lo, u64 hi, u64 c_before, u64 m_before, u64 want_count, u64 want_mass,
+                           u64& upto) {
+            for (int level = 0; level < 8; ++level) {                         // 10 bits each time
+                int shift = 0;
+                while (((hi - lo) >> shift) >= kParts) ++shift;
+                __syncthreads();
 #pragma unroll
-        for (int e = 0; e < kPer; ++e) {
-            const int i = tid * kPer + e;
-            const bool keep = (q[e] >> 62) != 0 && (before < need || (above == 0 && i == 0));
-            before += q[e] & ~(1ull << 62);
-            if (keep) {
-                last = static_cast<uint32_t>(i) + 1u;
-                upto = before;
+                for (int y = 0; y < 3; ++y) s.hist[y * kParts + tid] = 0u;
+                __syncthreads();
+#pragma unroll
+                for (int e = 0; e < kPer; ++e) {
+                    if (key[e] < lo || key[e] > hi) continue;
+                    const int part = static_cast<int>((hi - key[e]) >> shift);
+                    atomicAdd(&s.hist[part], 1u);
+                    atomicAdd(&s.hist[kParts + part], qh[e]);
+                    atomicAdd(&s.hist[2 * kParts + part], ql[e]);
+                }
+                __syncthreads();
+                const u64 c = s.hist[tid], q = (static_cast<u64>(s.hist[kParts + tid]) << 20) + s.hist[2 * kParts + tid];
+                u64 ci = c, qi = q;
+                scan(ci, qi, c_before, m_before);
+                const bool crosses = want_count != ~0ull ? ci - c < want_count && ci >= want_count
+                                                         : qi - q < want_mass && qi >= want_mass;
+                if (crosses) {
+                    s.out[0] = static_cast<u64>(tid);
+                    s.out[1] = c;
+                    s.out[2] = ci - c;
+                    s.out[3] = qi - q;
+                }
+                __syncthreads();
+                const u64 part = s.out[0], in_part = s.out[1];
+                c_before = s.out[2];
+                m_before = s.out[3];
+                const u64 first = hi - (part << shift), length = (1ull << shift) - 1;
+                lo = first - lo > length ? first - length : lo;
+                hi = first;
+                if (in_part == 1) break;
             }
-        }
-        const uint32_t best = __reduce_max_sync(0xFFFFFFFFu, last);
-        if (best != 0 ? last == best : lane == 0) {
-            s.warp_sum[2][warp] = best;
-            s.warp_sum[3][warp] = upto;
+            // the one entry left
+            __syncthreads();
+#pragma unroll
+            for (int e = 0; e < kPer; ++e)
+                if (key[e] >= lo && key[e] <= hi) {
+                    s.out[0] = key[e];
+                    s.out[1] = m_before + (static_cast<u64>(qh[e]) << 20) + ql[e];
+                }
+            __syncthreads();
+            upto = s.out[1];
+            return s.out[0];
+        };
+        u64 last = bottom_key, upto = over + sum;
+        if (above + number > kk) last = descend(key, bottom_key, top_key, above, over, kk, ~0ull, upto);
+        if (need == ~0ull) need = max(1ull, share_of(upto, P));
+        if (need < upto) last = descend(key, last, top_key, above, over, ~0ull, need, upto);
+        u64 drawn = 0;
+        if (above == 0) {
+            // by id: the first with which the mass exceeds the drawn share
+            u64 id_key[kPer];
+#pragma unroll
+            for (int e = 0; e < kPer; ++e) id_key[e] = key[e] >= last ? (key[e] & 0xFFFFFFFFull) + 1 : 0;
+            u64 unused;
+            const u64 found = descend(id_key, 1, 1ull << 32, 0, 0, ~0ull, share_of(upto, U) + 1, unused);
+            drawn = static_cast<u64>(key_index(found - 1)) + 1;
         }
         __syncthreads();
         if (tid == 0) {
-            uint32_t w = 0;
-            for (uint32_t y = 1; y < kWarps; ++y)
-                if (s.warp_sum[2][y] != 0) w = y;
-            s.out[0] = s.list[max(1ull, s.warp_sum[2][w]) - 1];
-            s.out[1] = s.warp_sum[3][w];
+            s.out[0] = last;
+            s.out[1] = upto;
+            s.out[2] = drawn;
         }
         __syncthreads();
     };
+    auto settled_on_list = [&] {
+        hear();
+        cut = s.out[0];
+        total = s.out[1];
+        token = static_cast<int>(s.out[2]) - 1;
+        in_list = token >= 0;
+    };
 
-    bool settled = top_bits == 0;                                             // nothing to keep: cut 0, total 0
-    if (settled) cut = ~0ull;
+    bool settled = top_bits == 0 || k == 1;                                   // nothing to keep, or one entry
+    if (settled) {
+        cut = top_bits == 0 ? ~0ull : x.c;
+        total = top_bits == 0 ? 0 : 1ull << 40;
+        token = top_bits == 0 ? 0 : static_cast<int>(key_index(x.c));
+        in_list = true;
+        if (top_bits != 0 && token >= v0 && token < v1 && tid == 0) {
+            s.list[0] = cut;
+            s.list_count = 1u;
+        }
+        __syncthreads();
+    }
 
     // ---- 2. a small top-k ----
     // A range that can be parted evenly (not of one value, and finite).
     auto even = [&](float lowest) { return m - lowest > 1e-30f && m - lowest < 1e38f; };
     if (!settled && k <= groups && k <= kList / 2 && even(bottom)) {
         const float scale = (kBins - 1) / (m - bottom);
-        if (mine != 0) {
-            const int bin = min(kBins - 1, static_cast<int>((m - float_from_order_bits(mine)) * scale));
-            if (C > 1) remote_add(remote(&s.hist[bin], 0), 1u);
+        auto enter = [&](uint32_t b) {
+            const int bin = min(kBins - 1, static_cast<int>((m - float_from_order_bits(b)) * scale));
+            if (rank != 0) send_add(remote(&s.hist[bin], 0), 1u, remote(&s.bar_hist, 0));
             else atomicAdd(&s.hist[bin], 1u);
+        };
+        if (!fine) {
+            if (leads != 0) enter(group);
+        } else {
+#pragma unroll
+            for (int j = 0; j < kBatch; ++j)
+                if (bits(tops[j]) != 0) enter(bits(tops[j]));
         }
-        sync();
         if (rank == 0) {
+            if (C > 1) receive(s.bar_hist, used_hist, 4u * static_cast<uint32_t>(x.b - s.red[turn ^ 1][0][1]));
+            __syncthreads();
             // the first bin up to which there are k
-            uint32_t c[kPerThread], sum = 0;
+            u64 c[kPerThread], sum = 0, none = 0;
 #pragma unroll
             for (int e = 0; e < kPerThread; ++e) sum += c[e] = s.hist[tid * kPerThread + e];
-            uint32_t incl = sum;
-            for (int d = 1; d < 32; d <<= 1) {
-                const uint32_t y = __shfl_up_sync(0xFFFFFFFFu, incl, d);
-                if (lane >= static_cast<uint32_t>(d)) incl += y;
-            }
-            if (lane == 31) s.warp_sum[0][warp] = incl;
-            __syncthreads();
-            uint32_t before = incl - sum;
-            for (uint32_t w = 0; w < warp; ++w) before += static_cast<uint32_t>(s.warp_sum[0][w]);
+            u64 incl = sum;
+            scan(incl, none, 0, 0);
+            u64 before = incl - sum;
+#pragma unroll
             for (int e = 0; e < kPerThread; ++e) {
-                if (before < static_cast<uint32_t>(k) && before + c[e] >= static_cast<uint32_t>(k))
+                if (before < static_cast<u64>(k) && before + c[e] >= static_cast<u64>(k))
                     s.out[0] = static_cast<u64>(tid * kPerThread + e);
                 before += c[e];
             }
         }
         hear();
         const float reach = static_cast<float>(s.out[0] + 1);
-        each_converged([&](bool in, int v, float l) { append(in && (m - l) * scale < reach, l, v); });
-        sync();
-        const uint32_t count = C > 1 ? remote_load(remote(&s.list_count, 0)) : s.list_count;
+        // a logit that no entry of those parts is below
+        const float least = m - reach / scale * (1.0f + 1e-5f) - fabsf(m) * 2.5e-7f;
+        each(least, [&](float l, int v, bool in) { append(in && (m - l) * scale < reach, l, v); });
+        const int count = gather();
         if (count <= kList) {
-            if (rank == 0) settle(static_cast<int>(count), 0, 0, static_cast<u64>(k), ~0ull);
-            hear();
-            cut = s.out[0];
-            total = s.out[1];
+            if (rank == 0) settle(count, 0, 0, static_cast<u64>(k), ~0ull);
+            settled_on_list();
             settled = true;
-        } else {
-            sync();                                                           // all have read the count
-            if (tid == 0) s.list_count = 0u;
         }
     }
 
-    // This warp's run of neighbouring entries.
-    const int per_run = ((n + kWarps - 1) / kWarps + 31) / 32 * 32;
-    const int run0 = min(v1, v0 + static_cast<int>(warp) * per_run), run1 = min(v1, run0 + per_run);
     // With every run's sum in the first block's s.segment: the first id at which the sum of value(logit, id)
     // over all ids up to it exceeds t, known to one warp of the cluster, which calls found(id) in all lanes.
     auto locate = [&](u64 t, auto value, auto found) {
-        sync();
+        if (rank == 0) {
+            if (C > 1) receive(s.bar_segment, used_segment, static_cast<uint32_t>(C - 1) * kWarps * 8u);
+            __syncthreads();
+        }
         if (rank == 0 && warp == 0) {
             u64 before = 0;
             for (int i0 = 0; i0 < C * kWarps; i0 += 32) {
-                const u64 mass = i0 + static_cast<int>(lane) < C * kWarps ? s.segment[i0 + lane] : 0;
+                const u64 mass = s.segment[i0 + lane];
                 u64 incl = mass;
                 for (int d = 1; d < 32; d <<= 1) {
                     const u64 y = __shfl_up_sync(0xFFFFFFFFu, incl, d);
@@ -446,64 +717,126 @@ __global__ void __launch_bounds__(kThreads) sample_kernel(const __grid_constant_
         }
         hear();
         if (s.out[0] == rank * kWarps + warp) {
+            // a lane sums neighbouring pieces of the run; then the lanes share the pieces of the one it is in
             u64 left = s.out[1];
-            for (int b = run0; b < run1; b += 32) {
-                const int v = b + static_cast<int>(lane);
-                u64 incl = v < run1 ? value(to_float(row[v]), v) : 0;
+            const int per_lane = ((run1 - run0 + 31) / 32) | 1;               // odd: the lanes meet no bank twice
+            int a0 = min(run1, run0 + static_cast<int>(lane) * per_lane), a1 = min(run1, a0 + per_lane);
+            auto add = [&](int i) {
+                float y[kPiece];
+                unpack(fetch(i, streamed), i, y);
+                u64 sum = 0;
+#pragma unroll
+                for (int e = 0; e < kPiece; ++e) sum += value(y[e], place0 + i * kPiece + e);
+                return sum;
+            };
+            auto pick = [&](u64 own, int& at) {                               // the lane whose sum passes `left`
+                u64 incl = own;
                 for (int d = 1; d < 32; d <<= 1) {
                     const u64 y = __shfl_up_sync(0xFFFFFFFFu, incl, d);
                     if (lane >= static_cast<uint32_t>(d)) incl += y;
                 }
                 const uint32_t vote = __ballot_sync(0xFFFFFFFFu, incl > left);
-                if (vote != 0) {
-                    found(b + __ffs(static_cast<int>(vote)) - 1);
+                at = vote != 0 ? __ffs(static_cast<int>(vote)) - 1 : 31;
+                const u64 y = __shfl_sync(0xFFFFFFFFu, vote != 0 ? incl - own : incl, at);
+                left -= y;
+                return vote != 0;
+            };
+            u64 sum = 0;
+            for (int i = a0; i < a1; ++i) sum += add(i);
+            int at;
+            if (pick(sum, at)) {
+                a0 = __shfl_sync(0xFFFFFFFFu, a0, at);
+                a1 = __shfl_sync(0xFFFFFFFFu, a1, at);
+                for (int i = a0; i < a1; i += 32) {
+                    const int mine = i + static_cast<int>(lane);
+                    if (!pick(mine < a1 ? add(mine) : 0, at)) continue;
+                    float y[kPiece];
+                    unpack(fetch(i + at, streamed), i + at, y);
+                    int v = place0 + (i + at) * kPiece;
+#pragma unroll
+                    for (int e = 0; e < kPiece; ++e) {
+                        const u64 q = value(y[e], v);
+                        if (q > left) break;
+                        left -= q;
+                        ++v;
+                    }
+                    found(v);
                     break;
                 }
-                left -= __shfl_sync(0xFFFFFFFFu, incl, 31);
             }
         }
     };
     auto report_run = [&](u64 sum) {                                          // lane 0's: this run's sum
         if (lane != 0) return;
-        if (C > 1) remote_store(remote(&s.segment[rank * kWarps + warp], 0), sum);
+        if (rank != 0) send(remote(&s.segment[rank * kWarps + warp], 0), sum, remote(&s.bar_segment, 0));
         else s.segment[warp] = sum;
+    };
+    auto set_token = [&](int v) {
+        if (lane == 0) p.tokens[r] = v;
     };
 
     // ---- 3. and 4. ----
+    bool runs_known = false;                                                  // the runs' kept masses are reported
     if (!settled) {
         // Closes in on the cut: the first entry of the order with which the count reaches `want_count`, or the
         // mass `want_mass` (the other is ~0).  `lowest`: no entry below this logit can be the cut.
+        // Where the cut comes from a list, `run_mass` receives the mass that this warp's run has above the list.
+        u64 run_mass = 0;
         auto close_in = [&](u64 want_count, u64 want_mass, float lowest) {
             u64 above = 0, over = 0;                                          // count and mass above the range
+            run_mass = 0;
+            runs_known = false;
             bool linear = even(lowest);                                       // parts of equal width, or of equal bits
             uint32_t hi = top_bits, lo = float_order_bits(lowest);
-            while (true) {
+            for (int i = tid; i < kBins; i += kThreads) s.share[i] = 0u;
+            exchange(0, 0, 0, 0);                                             // all blocks' shares are clear
+            for (int level = 0; level < 8; ++level) {                         // four settle any range; bounded all the same
                 const float scale = linear ? kBins / (m - lowest) : 0.0f;
                 int shift = 0;
                 while (((hi - lo) >> shift) >= kBins) ++shift;
-                auto bin_of = [&](uint32_t b, float l) {
-                    return linear ? min(kBins - 1, static_cast<int>((m - l) * scale)) : static_cast<int>((hi - b) >> shift);
+                const float from = float_from_order_bits(lo);
+                // an entry's part, or kBins
+                auto part_of = [&](float l, bool in) {
+                    const uint32_t b = float_order_bits(l);
+                    if (!in || b > hi || (min_p != 0.0f && weight(l) < min_p)) return kBins;
+                    return linear ? min(kBins - 1, floor_of((m - l) * scale)) : static_cast<int>((hi - b) >> shift);
                 };
-                sync();
+                __syncthreads();
                 if (tid == 0) s.list_count = 0u;
                 for (int i = tid; i < kBins; i += kThreads) s.hist[i] = 0u;
                 __syncthreads();
-                each([&](uint32_t b, int, float l) {
-                    if (b >= lo && b <= hi && weight(l) >= min_p) atomicAdd(&s.hist[bin_of(b, l)], 1u);
+                every(from, [&](float l, int) {
+                    const int part = part_of(l, true);
+                    if (part < kBins) atomicAdd(&s.hist[part], 1u);
                 });
-                sync();
-                if (rank != 0)
-                    for (int i = tid; i < kBins; i += kThreads)
-                        if (s.hist[i] != 0) remote_add(remote(&s.hist[i], 0), s.hist[i]);
-                sync();
+                __syncthreads();
+                if (C > 1) {
+                    // each block adds up its share of the bins over all blocks, for the first one
+                    const int share = kBins / C, bin0 = static_cast<int>(rank) * share;
+                    for (int i = tid; i < kBins; i += kThreads) {
+                        const uint32_t to = static_cast<uint32_t>(i / share);
+                        if (to != rank) send_add(remote(&s.share[i], to), s.hist[i], remote(&s.bar_share, to));
+                        else atomicAdd(&s.share[i], s.hist[i]);
+                    }
+                    receive(s.bar_share, used_share, static_cast<uint32_t>((C - 1) * share) * 4u);
+                    __syncthreads();
+                    for (int i = bin0 + tid; i < bin0 + share; i += kThreads) {
+                        if (rank != 0) send32(remote(&s.bins[i], 0), s.share[i], remote(&s.bar_bins, 0));
+                        else s.bins[i] = s.share[i];
+                        s.share[i] = 0u;                                      // the next level comes after an exchange
+                    }
+                    if (rank == 0) receive(s.bar_bins, used_bins, static_cast<uint32_t>(kBins - share) * 4u);
+                } else {
+                    for (int i = tid; i < kBins; i += kThreads) s.bins[i] = s.hist[i];
+                }
+                __syncthreads();
                 if (rank == 0) {
                     // bounds of each part's mass from its edges, with room for the rounding of edges and expf
-                    uint32_t c[kPerThread];
-                    u64 least[kPerThread], most[kPerThread], sum_least = 0, sum_most = 0;
+                    u64 c[kPerThread], least[kPerThread], most[kPerThread], in_least = 0, in_most = 0;
 #pragma unroll
                     for (int e = 0; e < kPerThread; ++e) {
                         const int i = tid * kPerThread + e;
-                        c[e] = s.hist[i];
+                        c[e] = s.bins[i];
                         least[e] = most[e] = c[e];
                         if (want_count == ~0ull) {
                             float hi_edge, lo_edge;
@@ -518,32 +851,16 @@ __global__ void __launch_bounds__(kThreads) sample_kernel(const __grid_constant_
                                 lo_edge = float_from_order_bits(last);
                             }
                             most[e] = c[e] * (mass_of(fminf(1.0f, weight(hi_edge) * (1.0f + 1e-4f))) + 1);
-                            least[e] = c[e] * mass_of(fmaxf(0.0f, weight(lo_edge) * (1.0f - 1e-4f)));
+                            least[e] = c[e] * mass_of(fminf(1.0f, fmaxf(0.0f, weight(lo_edge) * (1.0f - 1e-4f))));
                         }
-                        sum_least += least[e];
-                        sum_most += most[e];
+                        in_least += least[e];
+                        in_most += most[e];
                     }
-                    u64 in_least = sum_least, in_most = sum_most;
-                    for (int d = 1; d < 32; d <<= 1) {
-                        const u64 y = __shfl_up_sync(0xFFFFFFFFu, in_least, d), z = __shfl_up_sync(0xFFFFFFFFu, in_most, d);
-                        if (lane >= static_cast<uint32_t>(d)) {
-                            in_least += y;
-                            in_most += z;
-                        }
-                    }
-                    if (lane == 31) {
-                        s.warp_sum[0][warp] = in_least;
-                        s.warp_sum[1][warp] = in_most;
-                    }
-                    if (tid == 0) {
-                        s.out[0] = s.out[1] = kBins - 1;                      // first and last part that can hold the cut
-                    }
-                    __syncthreads();
-                    u64 least_before = in_least - sum_least, most_before = in_most - sum_most;
-                    for (uint32_t w = 0; w < warp; ++w) {
-                        least_before += s.warp_sum[0][w];
-                        most_before += s.warp_sum[1][w];
-                    }
+                    u64 least_before = in_least, most_before = in_most;
+                    if (tid == 0) s.out[0] = s.out[1] = kBins - 1;            // first and last part that can hold the cut
+                    scan(least_before, most_before, 0, 0);
+                    least_before -= in_least;
+                    most_before -= in_most;
                     const u64 want = want_count != ~0ull ? want_count - above : want_mass - over;
 #pragma unroll
                     for (int e = 0; e < kPerThread; ++e) {
@@ -553,46 +870,62 @@ __global__ void __launch_bounds__(kThreads) sample_kernel(const __grid_constant_
                         least_before += least[e];
                         most_before += most[e];
                     }
+                    __syncthreads();
+                    // the entries in those parts
+                    u64 inside = 0, none = 0, zero = 0, nil = 0;
+#pragma unroll
+                    for (int e = 0; e < kPerThread; ++e) {
+                        const u64 i = static_cast<u64>(tid * kPerThread + e);
+                        if (i >= s.out[0] && i <= s.out[1]) inside += c[e];
+                    }
+                    block(inside, none, zero, nil);
+                    if (tid == 0) s.out[2] = inside;
                 }
                 hear();
                 const int first = static_cast<int>(s.out[0]), last = static_cast<int>(s.out[1]);
-                // above those parts: summed; in them: counted, bounded and, if they fit, listed
+                const bool fits = s.out[2] <= kList;
+                __syncthreads();                                              // the bins' place may become the list's
+                // above those parts: summed; in them: listed if they fit, else bounded
                 u64 more = 0, high = 0, low = 0;
-                uint32_t mass_hi = 0, mass_lo = 0, inside = 0;
-                each_converged([&](bool in, int v, float l) {
-                    const uint32_t b = bits(l);
-                    in = in && b >= lo && b <= hi;
-                    float w = 0.0f;
-                    int bin = kBins;
-                    if (in) {
-                        bin = bin_of(b, l);
-                        w = weight(l);
-                        in = w >= min_p;
-                    }
-                    if (in && bin < first) {
-                        uint32_t qh, ql;
-                        mass_halves(w, qh, ql);
-                        mass_hi += qh;
-                        mass_lo += ql;
+                MassSum mass;
+                every(from, [&](float l, int v) {
+                    const int part = part_of(l, true);
+                    if (part < first) {
+                        mass.add(weight(l));
                         ++more;
+                    } else if (part <= last) {
+                        if (fits) {
+                            s.list[atomicAdd(&s.list_count, 1u)] = key_of(l, v);
+                        } else {
+                            high = max(high, static_cast<u64>(float_order_bits(l)));
+                            low = max(low, static_cast<u64>(0xFFFFFFFFu - float_order_bits(l)));
+                        }
                     }
-                    const bool here = in && bin >= first && bin <= last;
-                    if (here) {
-                        ++inside;
-                        high = max(high, static_cast<u64>(b));
-                        low = max(low, static_cast<u64>(0xFFFFFFFFu - b));
-                    }
-                    append(here, l, v);
                 });
-                const Reduced y = reduce((static_cast<u64>(mass_hi) << 20) + mass_lo, more + (static_cast<u64>(inside) << 32), high, low);
+                const u64 own = mass.value();
+                run_mass += warp_sum_u64(own);
+                const Reduced y = reduce(own, more, high, low);
                 over += y.a;
-                above += y.b & 0xFFFFFFFFull;
-                const u64 count = y.b >> 32;
-                if (count <= kList) {
-                    if (rank == 0) settle(static_cast<int>(count), above, over, want_count, want_mass);
-                    hear();
-                    cut = s.out[0];
-                    total = s.out[1];
+                above += y.b;
+                if (fits) {
+                    const int count = gather();
+                    if (rank == 0) settle(count, above, over, want_count, want_mass);
+                    settled_on_list();
+                    if (token < 0) {
+                        // the runs' sums: the list's kept entries join those above it
+                        __syncthreads();
+                        if (tid < kWarps) s.run[tid] = 0;
+                        __syncthreads();
+                        for (uint32_t i = tid; i < s.list_count; i += kThreads) {
+                            const u64 key = s.list[i];
+                            if (key < cut) continue;
+                            const int place = (static_cast<int>(key_index(key)) - place0) / kPiece;
+                            atomicAdd(&s.run[place / per_run], mass_of(weight(key_logit(key))));
+                        }
+                        __syncthreads();
+                        run_mass += s.run[warp];
+                        runs_known = true;
+                    }
                     return;
                 }
                 linear = false;
@@ -604,24 +937,21 @@ __global__ void __launch_bounds__(kThreads) sample_kernel(const __grid_constant_
                     const u64 take = want_count != ~0ull ? want_count - above
                                      : q == 0          ? 1
                                                        : max(1ull, (want_mass - over + q - 1) / q);
+                    auto tie = [&](float l, int v) -> u64 { return bits(l) == hi && key_of(l, v) >= limit ? 1 : 0; };
                     u64 ties = 0;
-                    for (int v = run0 + static_cast<int>(lane); v < run1; v += 32) {
-                        const float l = to_float(row[v]);
-                        if (bits(l) == hi && argmax_key(l, static_cast<uint32_t>(v)) >= limit) ++ties;
-                    }
+                    pass(streamed, [&](int i, const float (&y)[kPiece], const uint4&, int) {
+#pragma unroll
+                        for (int e = 0; e < kPiece; ++e) ties += tie(y[e], place0 + i * kPiece + e);
+                    });
                     report_run(warp_sum_u64(ties));
-                    locate(take - 1,
-                           [&](float l, int v) -> u64 {
-                               return bits(l) == hi && argmax_key(l, static_cast<uint32_t>(v)) >= limit ? 1 : 0;
-                           },
-                           [&](int v) {
-                               if (lane < static_cast<uint32_t>(C)) {
-                                   const u64 key = argmax_key(float_from_order_bits(hi), static_cast<uint32_t>(v));
-                                   if (C > 1) remote_store(remote(&s.found, lane), key);
-                                   else s.found = key;
-                               }
-                           });
-                    sync();
+                    locate(take - 1, tie, [&](int v) {
+                        const u64 key = key_of(float_from_order_bits(hi), v);
+                        if (C == 1) s.found = key;
+                        else if (lane < static_cast<uint32_t>(C))
+                            send(remote(&s.found, lane), key, remote(&s.bar_found, lane));
+                    });
+                    if (C > 1) receive(s.bar_found, used_found, 8u);
+                    else __syncthreads();
                     cut = s.found;
                     total = over + take * q;
                     return;
@@ -630,84 +960,100 @@ __global__ void __launch_bounds__(kThreads) sample_kernel(const __grid_constant_
         };
 
         // what min-p leaves
-        uint32_t mass_hi = 0, mass_lo = 0, count = 0, low = 0;
-        each([&](uint32_t b, int, float l) {
-            const float w = weight(l);
-            if (w < min_p) return;
-            uint32_t qh, ql;
-            mass_halves(w, qh, ql);
-            mass_hi += qh;
-            mass_lo += ql;
-            ++count;
-            low = max(low, 0xFFFFFFFFu - b);
+        MassSum mass;
+        uint32_t count = 0;
+        float smallest = INFINITY;
+        pass(streamed, [&](int, const float (&x)[kPiece], const uint4&, int) {
+#pragma unroll
+            for (int e = 0; e < kPiece; ++e) {
+                const bool finite = fabsf(x[e]) < INFINITY;
+                float w = finite ? weight(x[e]) : 0.0f;
+                const bool in = finite && w >= min_p;
+                if (!in) w = 0.0f;
+                mass.add(w);
+                count += in ? 1u : 0u;
+                if (in) smallest = fminf(smallest, x[e]);
+            }
         });
-        const Reduced all = reduce((static_cast<u64>(mass_hi) << 20) + mass_lo, count, 0, low);
+        const u64 own = mass.value();
+        const Reduced all = reduce(own, count, 0, count != 0 ? 0xFFFFFFFFu - float_order_bits(smallest) : 0u);
         const float lowest = float_from_order_bits(0xFFFFFFFFu - static_cast<uint32_t>(all.d));
         u64 entries = all.b;
         total = all.a;
+        run_mass = warp_sum_u64(own);
+        runs_known = true;                                                    // if everything is kept
         if (static_cast<u64>(k) < entries) {
             close_in(static_cast<u64>(k), ~0ull - 1, lowest);
             limit = cut;
             entries = static_cast<u64>(k);
         }
-        const u64 need = max(1ull, share_of(total, P));       // the first entry (mass 2^40) is kept anyway
+        const u64 need = max(1ull, share_of(total, P));                       // the first entry (mass 2^40) is kept anyway
         if (need < total) {
             // Entries of mass at most z weigh no more than total - need together: the cut is not among them.
             const u64 z = (total - need) / entries;
             float least = lowest;
             if (z > 0) least = fmaxf(lowest, m + (logf(__ull2float_rn(z) * 0x1p-40f) * (1.0f + 1e-5f) - 1e-5f) / inv);
-            sync();
-            if (tid == 0) s.list_count = 0u;
-            sync();
-            each_converged([&](bool in, int v, float l) { append(in && l >= least && weight(l) >= min_p, l, v); });
-            sync();
-            const uint32_t listed = C > 1 ? remote_load(remote(&s.list_count, 0)) : s.list_count;
-            if (listed <= kList) {
-                if (rank == 0) settle(static_cast<int>(listed), 0, 0, ~0ull, need);
-                hear();
-                cut = s.out[0];
-                total = s.out[1];
-            } else {
-                close_in(~0ull, need, least);
-            }
+            token = -1;                                                       // what top-k's list said is not the last word
+            in_list = false;
+            close_in(~0ull, need, least);
         }
+        if (token < 0 && runs_known) report_run(run_mass);
     }
 
-    // ---- 5. the kept entries' runs, and the probabilities ----
-    const float cut_logit = cut == 0 ? -INFINITY : float_from_order_bits(static_cast<uint32_t>(cut >> 32));
+    // ---- 5. the token, and the probabilities ----
+    const float cut_logit = cut == 0 ? -INFINITY : key_logit(cut);
     auto kept = [&](float l, int v) {                                         // weight of a kept entry, else 0
-        if (!(l >= cut_logit) || bits(l) == 0 || argmax_key(l, static_cast<uint32_t>(v)) < cut) return 0.0f;
+        if (!(l >= cut_logit) || bits(l) == 0 || key_of(l, v) < cut) return 0.0f;
         const float w = weight(l);
         return w < min_p ? 0.0f : w;
     };
-    const bool some = top_bits != 0;
-    if (some || p.probs != nullptr) {
-        const float norm = __fmul_rn(__ull2float_rn(total), 0x1p-40f);
-        float* const probs = p.probs != nullptr ? p.probs + r * V : nullptr;
-        uint32_t mass_hi = 0, mass_lo = 0;
-#pragma unroll 4
-        for (int v = run0 + static_cast<int>(lane); v < run1; v += 32) {
-            const float w = some ? kept(to_float(row[v]), v) : 0.0f;
-            float y = 0.0f;
-            if (w > 0.0f) {
-                uint32_t qh, ql;
-                mass_halves(w, qh, ql);
-                mass_hi += qh;
-                mass_lo += ql;
-                if (probs != nullptr && (qh | ql) != 0) y = __fdiv_rn(w, norm);
-            }
-            if (probs != nullptr) probs[v] = y;
+    if (token < 0) {
+        if (!runs_known) {
+            MassSum mass;
+            pass(streamed, [&](int i, const float (&y)[kPiece], const uint4&, int) {
+#pragma unroll
+                for (int e = 0; e < kPiece; ++e)
+                    if (y[e] >= cut_logit) mass.add(kept(y[e], place0 + i * kPiece + e));
+            });
+            report_run(warp_sum_u64(mass.value()));
         }
-        if (some) report_run(warp_sum_u64((static_cast<u64>(mass_hi) << 20) + mass_lo));
+        locate(share_of(total, U), [&](float l, int v) { return mass_of(kept(l, v)); }, set_token);
+    } else if (rank == 0 && warp == 0) {
+        set_token(token);
     }
-    if (some) {
-        locate(share_of(total, U), [&](float l, int v) { return mass_of(kept(l, v)); },
-               [&](int v) {
-                   if (lane == 0) p.tokens[r] = v;
-               });
-        sync();                                                               // shared memory lives as long as it is read
-    } else if (rank == 0 && tid == 0) {
-        p.tokens[r] = 0;
+    if (p.probs == nullptr) return;
+    const float norm = __fmul_rn(__ull2float_rn(total), 0x1p-40f);
+    float* const probs = p.probs + r * V;
+    auto share = [&](float w) { return w >= 0x1p-40f ? __fdiv_rn(w, norm) : 0.0f; };      // 0 where the mass is
+    if (in_list) {
+        // zeros, then this block's part of the list
+        const int head = min(n, static_cast<int>((16u - (reinterpret_cast<uintptr_t>(probs + v0) & 15u)) & 15u) / 4);
+        const int quads = (n - head) / 4;
+        for (int i = tid; i < head; i += kThreads) probs[v0 + i] = 0.0f;
+        for (int i = tid; i < quads; i += kThreads)
+            __stcs(reinterpret_cast<float4*>(probs + v0 + head) + i, make_float4(0.0f, 0.0f, 0.0f, 0.0f));
+        for (int i = head + 4 * quads + tid; i < n; i += kThreads) probs[v0 + i] = 0.0f;
+        __syncthreads();
+        for (uint32_t i = tid; i < s.list_count; i += kThreads) {
+            const u64 key = s.list[i];
+            if (key >= cut) probs[key_index(key)] = share(weight(key_logit(key)));
+        }
+    } else {
+        // 16-byte stores where the two rows are aligned alike (fp32 logits)
+        pass(streamed, [&](int i, const float (&x)[kPiece], const uint4&, int) {
+            if (i >= run1) return;
+            float y[kPiece];
+            const int v = place0 + i * kPiece;
+#pragma unroll
+            for (int e = 0; e < kPiece; ++e) y[e] = x[e] >= cut_logit ? share(kept(x[e], v + e)) : 0.0f;
+            if (kPiece == 4 && whole(i)) {
+                __stcs(reinterpret_cast<float4*>(probs + v), *reinterpret_cast<const float4*>(y));
+            } else {
+#pragma unroll
+                for (int e = 0; e < kPiece; ++e)
+                    if (v + e >= v0 && v + e < v1) probs[v + e] = y[e];
+            }
+        });
     }
 }
 
@@ -716,18 +1062,14 @@ __global__ void __launch_bounds__(kThreads) sample_kernel(const __grid_constant_
 // ---------------------------------------------------------------------------
 template <typename T>
 cudaError_t launch_typed(SampleArgs p, cudaStream_t stream, const DeviceInfo& dev) {
-    const size_t room = dev.smem_optin - sizeof(Shared) - 64;
-    // Blocks per row: enough that two blocks' copies fit an SM; with few rows, more, as long as a block keeps
-    // kMinSlice entries, so that all SMs share the row's passes.
+    // Blocks per row: as many as give every SM one, while a block keeps kMinSlice entries.
     constexpr int kMinSlice = 4096;
-    constexpr size_t kCopy = 80 * 1024;
-    int c = 1;
     auto slice_of = [&](int blocks) { return ((p.V + blocks - 1) / blocks + 7) / 8 * 8; };
-    while (c < kMaxCluster && slice_of(c) * sizeof(T) > kCopy) c *= 2;
-    while (c < kMaxCluster && static_cast<long long>(p.R) * c < 2ll * dev.sm_count && slice_of(2 * c) >= kMinSlice) c *= 2;
+    int c = 1;
+    while (c < kMaxCluster && static_cast<long long>(p.R) * c < dev.sm_count && slice_of(2 * c) >= kMinSlice) c *= 2;
     p.cluster = c;
     p.slice = slice_of(c);
-    p.resident = static_cast<size_t>(p.slice) * sizeof(T) <= room ? 1 : 0;
+    p.resident = sizeof(Shared) + static_cast<size_t>(p.slice) * sizeof(T) + 32 <= dev.smem_optin ? 1 : 0;
     const size_t smem = sizeof(Shared) + (p.resident ? static_cast<size_t>(p.slice) * sizeof(T) + 32 : 0);
     cudaError_t e = cudaFuncSetAttribute(sample_kernel<T>, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem));
     if (e == cudaSuccess) e = cudaFuncSetAttribute(sample_kernel<T>, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
