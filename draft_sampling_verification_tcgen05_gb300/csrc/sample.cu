@@ -42,6 +42,8 @@ constexpr int kList = 2048;                // entries of the list
 constexpr int kBins = 2048;
 constexpr int kPerThread = kBins / kThreads;
 constexpr int kParts = kThreads;           // of the list's range, a thread each
+constexpr int kHist = 3 * kParts > kBins ? 3 * kParts : kBins;
+constexpr int kFew = 256;                  // entries that are settled by comparing each with all
 constexpr int kBatch = 4;                  // 16-byte pieces that a thread has under way
 constexpr uint32_t kWaitPeer = 0xA01;
 
@@ -53,6 +55,7 @@ struct SampleArgs {
     int R, V;
     int cluster, slice;                    // blocks of a row, entries of a block
     int resident;                          // a block's part is held in shared memory
+    int heavy_first;                       // blocks choose their rows by what they take
     int32_t* tokens;
     float* probs;
     WsHeader* ws;
@@ -141,7 +144,7 @@ struct alignas(16) Shared {
             uint32_t bins[kBins];          // in the first block: all blocks' counts
         };
     };
-    uint32_t hist[3 * kParts];             // counts (kBins), or on the list counts and masses' halves of kParts parts
+    uint32_t hist[kHist];                  // counts (kBins), or on the list counts and masses' halves of kParts parts
     u64 segment[kMaxCluster * kWarps];     // of the first block: mass or count of each warp's run
     u64 warp_sum[4][kWarps];
     u64 out[4];                            // what the first block tells the others
@@ -150,8 +153,6 @@ struct alignas(16) Shared {
     uint32_t list_count, pad;
     u64 bar_red[2], bar_out, bar_hist, bar_list, bar_segment, bar_found, bar_share, bar_bins;
 };
-
-static_assert(3 * kParts >= kBins, "one array for both histograms");
 
 struct Reduced { u64 a, b, c, d; };
 
@@ -164,7 +165,36 @@ __global__ void __launch_bounds__(kThreads, 1) sample_kernel(const __grid_consta
     const uint32_t warp = warp_id(), lane = lane_id();
     const int C = p.cluster;
     const uint32_t rank = C > 1 ? cluster_rank() : 0u;
-    const long long r = blockIdx.x / C;
+    // Rows that take the most passes first (with a block per row, more rows than SMs): without top-k, with
+    // top-p.  Every block finds its own row in that order.
+    long long r = blockIdx.x / C;
+    if (p.heavy_first) {
+        auto heavy = [&](int i) {
+            const int k = p.top_k[i];
+            return p.temperature[i] > 0.0f && (k <= 0 || k > kList / 2) && p.top_p[i] < 1.0f;
+        };
+        const int place = static_cast<int>(blockIdx.x);
+        int all = 0, seen = 0;
+        for (int i0 = 0; i0 < p.R; i0 += kThreads) all += __syncthreads_count(i0 + tid < p.R && heavy(i0 + tid));
+        const bool first = place < all;
+        const int want = first ? place : place - all;
+        for (int i0 = 0; i0 < p.R; i0 += kThreads) {
+            const bool mine = i0 + tid < p.R && heavy(i0 + tid) == first;
+            const int here = __syncthreads_count(mine);
+            if (want < seen + here) {
+                const uint32_t vote = __ballot_sync(0xFFFFFFFFu, mine);
+                if (lane == 0) s.run[warp] = __popc(vote);
+                __syncthreads();
+                int before = seen + __popc(vote & ((1u << lane) - 1u));
+                for (uint32_t w = 0; w < warp; ++w) before += static_cast<int>(s.run[w]);
+                if (mine && before == want) s.found = static_cast<u64>(i0 + tid);
+                __syncthreads();
+                break;
+            }
+            seen += here;
+        }
+        r = static_cast<long long>(s.found);
+    }
     const T* const global = static_cast<const T*>(p.logits) + r * V;
     const int v0 = min(V, static_cast<int>(rank) * p.slice), v1 = min(V, v0 + p.slice), n = v1 - v0;
 
@@ -248,13 +278,14 @@ __global__ void __launch_bounds__(kThreads, 1) sample_kernel(const __grid_consta
         }
         __syncthreads();
         if (warp == 0) {
-            a = warp_sum_u64(s.warp_sum[0][lane]);
-            b = warp_sum_u64(s.warp_sum[1][lane]);
-            c = warp_max_u64(s.warp_sum[2][lane]);
-            d = warp_max_u64(s.warp_sum[3][lane]);
+            const bool in = lane < kWarps;
+            a = warp_sum_u64(in ? s.warp_sum[0][lane] : 0);
+            b = warp_sum_u64(in ? s.warp_sum[1][lane] : 0);
+            c = warp_max_u64(in ? s.warp_sum[2][lane] : 0);
+            d = warp_max_u64(in ? s.warp_sum[3][lane] : 0);
         }
     };
-    static_assert(kWarps == 32, "a warp adds up the warps");
+    static_assert(kWarps <= 32, "a warp adds up the warps");
     auto reduce = [&](u64 a, u64 b, u64 c, u64 d) {
         block(a, b, c, d);
         return exchange(a, b, c, d);
@@ -515,6 +546,55 @@ __global__ void __launch_bounds__(kThreads, 1) sample_kernel(const __grid_consta
     // most kk entries in all, and of those as many as reach the mass `need` (~0: top-p's share of them).
     // Leaves {cut, mass, token + 1 if nothing is above the list, else 0} in s.out.
     auto settle = [&](int count, u64 above, u64 over, u64 kk, u64 need) {
+        if (count <= kFew) {
+            // a thread per entry: its rank and the mass before it, by comparison with all entries
+            u64* const masses = reinterpret_cast<u64*>(s.hist);
+            u64 key = 0, mass = 0;
+            if (tid < count) {
+                key = s.list[tid];
+                const float w = weight(key_logit(key));
+                mass = w < min_p ? ~0ull : mass_of(w);                        // ~0: it takes no part
+                masses[tid] = mass;
+            }
+            const bool part = tid < count && mass != ~0ull;
+            __syncthreads();
+            u64 rank_of = above, before = over;
+            if (part)
+                for (int i = 0; i < count; ++i) {
+                    const u64 other = s.list[i], q = masses[i];
+                    if (other > key && q != ~0ull) {
+                        ++rank_of;
+                        before += q;
+                    }
+                }
+            const bool counted = part && rank_of < kk;
+            u64 sum = counted ? mass : 0, none = 0, zero = 0, nil = 0;
+            block(sum, none, zero, nil);
+            if (tid == 0) s.out[0] = over + sum;
+            __syncthreads();
+            const u64 upto_k = s.out[0];
+            if (need == ~0ull) need = max(1ull, share_of(upto_k, P));
+            const bool keep = counted && (before < need || rank_of == 0);
+            const int number = __syncthreads_count(keep);
+            if (keep && rank_of + 1 == above + static_cast<u64>(number)) {    // the last of them
+                s.out[0] = key;
+                s.out[1] = before + mass;
+            }
+            if (tid < count) masses[tid] = keep ? mass : 0;
+            if (tid == 0) s.out[2] = 0;
+            __syncthreads();
+            if (above == 0 && keep) {
+                // by id: the one in which the drawn mass falls
+                const u64 t = share_of(s.out[1], U);
+                const uint32_t id = key_index(key);
+                u64 ahead = 0;
+                for (int i = 0; i < count; ++i)
+                    if (key_index(s.list[i]) < id) ahead += masses[i];
+                if (ahead <= t && t < ahead + mass) s.out[2] = static_cast<u64>(id) + 1;
+            }
+            __syncthreads();
+            return;
+        }
         // this thread's entries that take part, and their masses' halves
         constexpr int kPer = kList / kThreads;
         u64 key[kPer];
@@ -701,7 +781,7 @@ __global__ void __launch_bounds__(kThreads, 1) sample_kernel(const __grid_consta
         if (rank == 0 && warp == 0) {
             u64 before = 0;
             for (int i0 = 0; i0 < C * kWarps; i0 += 32) {
-                const u64 mass = s.segment[i0 + lane];
+                const u64 mass = i0 + static_cast<int>(lane) < C * kWarps ? s.segment[i0 + lane] : 0;
                 u64 incl = mass;
                 for (int d = 1; d < 32; d <<= 1) {
                     const u64 y = __shfl_up_sync(0xFFFFFFFFu, incl, d);
@@ -805,10 +885,21 @@ __global__ void __launch_bounds__(kThreads, 1) sample_kernel(const __grid_consta
                 if (tid == 0) s.list_count = 0u;
                 for (int i = tid; i < kBins; i += kThreads) s.hist[i] = 0u;
                 __syncthreads();
-                every(from, [&](float l, int) {
-                    const int part = part_of(l, true);
-                    if (part < kBins) atomicAdd(&s.hist[part], 1u);
-                });
+                const bool plain = linear && limit == 0 && min_p == 0.0f;    // no more than the range to look at
+                if (plain) {
+                    pass(streamed, [&](int, const float (&x)[kPiece], const uint4&, int) {
+#pragma unroll
+                        for (int e = 0; e < kPiece; ++e) {
+                            const int part = min(kBins - 1, floor_of((m - x[e]) * scale));
+                            if (x[e] >= from && x[e] <= m) atomicAdd(&s.hist[part], 1u);
+                        }
+                    });
+                } else {
+                    every(from, [&](float l, int) {
+                        const int part = part_of(l, true);
+                        if (part < kBins) atomicAdd(&s.hist[part], 1u);
+                    });
+                }
                 __syncthreads();
                 if (C > 1) {
                     // each block adds up its share of the bins over all blocks, for the first one
@@ -888,20 +979,38 @@ __global__ void __launch_bounds__(kThreads, 1) sample_kernel(const __grid_consta
                 // above those parts: summed; in them: listed if they fit, else bounded
                 u64 more = 0, high = 0, low = 0;
                 MassSum mass;
-                every(from, [&](float l, int v) {
-                    const int part = part_of(l, true);
-                    if (part < first) {
-                        mass.add(weight(l));
-                        ++more;
-                    } else if (part <= last) {
-                        if (fits) {
-                            s.list[atomicAdd(&s.list_count, 1u)] = key_of(l, v);
-                        } else {
-                            high = max(high, static_cast<u64>(float_order_bits(l)));
-                            low = max(low, static_cast<u64>(0xFFFFFFFFu - float_order_bits(l)));
-                        }
+                auto inside = [&](float l, int v) {
+                    if (fits) {
+                        s.list[atomicAdd(&s.list_count, 1u)] = key_of(l, v);
+                    } else {
+                        high = max(high, static_cast<u64>(float_order_bits(l)));
+                        low = max(low, static_cast<u64>(0xFFFFFFFFu - float_order_bits(l)));
                     }
-                });
+                };
+                if (plain) {
+                    uint32_t entries_above = 0;
+                    pass(streamed, [&](int i, const float (&x)[kPiece], const uint4&, int) {
+#pragma unroll
+                        for (int e = 0; e < kPiece; ++e) {
+                            const bool in = x[e] >= from && x[e] <= m;
+                            const int part = in ? min(kBins - 1, floor_of((m - x[e]) * scale)) : kBins;
+                            mass.add(part < first ? weight(x[e]) : 0.0f);
+                            entries_above += part < first ? 1u : 0u;
+                            if (part >= first && part <= last) inside(x[e], place0 + i * kPiece + e);
+                        }
+                    });
+                    more = entries_above;
+                } else {
+                    every(from, [&](float l, int v) {
+                        const int part = part_of(l, true);
+                        if (part < first) {
+                            mass.add(weight(l));
+                            ++more;
+                        } else if (part <= last) {
+                            inside(l, v);
+                        }
+                    });
+                }
                 const u64 own = mass.value();
                 run_mass += warp_sum_u64(own);
                 const Reduced y = reduce(own, more, high, low);
@@ -1022,9 +1131,9 @@ __global__ void __launch_bounds__(kThreads, 1) sample_kernel(const __grid_consta
         set_token(token);
     }
     if (p.probs == nullptr) return;
-    const float norm = __fmul_rn(__ull2float_rn(total), 0x1p-40f);
+    const float norm = 0x1p40f / __ull2float_rn(total);
     float* const probs = p.probs + r * V;
-    auto share = [&](float w) { return w >= 0x1p-40f ? __fdiv_rn(w, norm) : 0.0f; };      // 0 where the mass is
+    auto share = [&](float w) { return w >= 0x1p-40f ? w * norm : 0.0f; };    // 0 where the mass is
     if (in_list) {
         // zeros, then this block's part of the list
         const int head = min(n, static_cast<int>((16u - (reinterpret_cast<uintptr_t>(probs + v0) & 15u)) & 15u) / 4);
@@ -1068,6 +1177,7 @@ cudaError_t launch_typed(SampleArgs p, cudaStream_t stream, const DeviceInfo& de
     int c = 1;
     while (c < kMaxCluster && static_cast<long long>(p.R) * c < dev.sm_count && slice_of(2 * c) >= kMinSlice) c *= 2;
     p.cluster = c;
+    p.heavy_first = c == 1 && p.R > dev.sm_count ? 1 : 0;
     p.slice = slice_of(c);
     p.resident = sizeof(Shared) + static_cast<size_t>(p.slice) * sizeof(T) + 32 <= dev.smem_optin ? 1 : 0;
     const size_t smem = sizeof(Shared) + (p.resident ? static_cast<size_t>(p.slice) * sizeof(T) + 32 : 0);
@@ -1100,7 +1210,7 @@ dspark_status launch_sample(const void* logits, dspark_dtype dtype, const float*
     }
     dspark_status st = clear_workspace(ws, sizeof(WsHeader), stream);
     if (st != DSPARK_OK) return st;
-    SampleArgs p{logits, temperature, top_k, top_p, min_p, u, R, V, 1, 0, 0, tokens, probs, static_cast<WsHeader*>(ws)};
+    SampleArgs p{logits, temperature, top_k, top_p, min_p, u, R, V, 1, 0, 0, 0, tokens, probs, static_cast<WsHeader*>(ws)};
     const cudaError_t e = dtype == DSPARK_F32 ? launch_typed<float>(p, stream, dev)
                                               : launch_typed<__nv_bfloat16>(p, stream, dev);
     if (e != cudaSuccess) return cuda_error(e, "launch(sample)");
