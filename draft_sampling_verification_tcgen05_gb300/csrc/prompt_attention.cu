@@ -8,8 +8,8 @@
 //
 //   warp 0      takes the items and loads (TMA) queries, keys and values
 //   warp 1      clears the tokens outside every sequence
-//   warps 2, 3  issue S = Q K^T and O += P V of one query tile each on tcgen05 (M = 128, fp32 in
-//               tensor memory; P replaces half of S)
+//   warp 2      issues S = Q K^T and O += P V on tcgen05 (M = 128, fp32 in tensor memory; P replaces
+//               half of S)
 //   warps 4-7, 8-11  softmax and output of one query tile each: a thread per row, running maximum and
 //               sum in fp32, weights rounded to the inputs' type
 //
@@ -175,7 +175,7 @@ struct PromptSmem {
     uint64_t item_full[kAhead], item_empty[kAhead];
     uint64_t q_full[2], q_empty[2];
     uint64_t k_full[kSlots], k_empty[kSlots], v_full[kSlots], v_empty[kSlots];
-    uint64_t s_full[2], p_high[2], p_low[2], pv_done[2], o_empty[2], drain[2];
+    uint64_t s_full[2], p_high[2], p_low[2], pv_done[2], o_empty[2], drain;
     uint32_t tmem_base;
 };
 
@@ -194,7 +194,7 @@ prompt_attention_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_co
     if (threadIdx.x == 0) {
         for (int i = 0; i < kAhead; ++i) {
             mbar_init(&s.item_full[i], 1);
-            mbar_init(&s.item_empty[i], 2 * kRowThreads + 2);
+            mbar_init(&s.item_empty[i], 2 * kRowThreads + 1);
         }
         for (int i = 0; i < 2; ++i) {
             mbar_init(&s.q_full[i], 1);
@@ -204,14 +204,14 @@ prompt_attention_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_co
             mbar_init(&s.p_low[i], kRowThreads);
             mbar_init(&s.pv_done[i], 1);
             mbar_init(&s.o_empty[i], kRowThreads);
-            mbar_init(&s.drain[i], 1);
         }
         for (int i = 0; i < kSlots; ++i) {
             mbar_init(&s.k_full[i], 1);
-            mbar_init(&s.k_empty[i], 2);
+            mbar_init(&s.k_empty[i], 1);
             mbar_init(&s.v_full[i], 1);
-            mbar_init(&s.v_empty[i], 2);
+            mbar_init(&s.v_empty[i], 1);
         }
+        mbar_init(&s.drain, 1);
         s.redo_count[0] = s.redo_count[1] = 0u;
         fence_mbarrier_init();
         prefetch_tensormap(&tmQ);
@@ -329,102 +329,120 @@ prompt_attention_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_co
             if (a.lse)
                 for (int y = static_cast<int>(lane); y < a.Hq; y += 32) a.lse[t * a.Hq + y] = -INFINITY;
         }
-    } else if (warp < 4) {
-        // ---------------- products of query tile w: the whole warp waits, one lane issues ----------------
-        const int w = static_cast<int>(warp) - 2;
+    } else if (warp == 2) {
+        // ---------------- products: the whole warp waits, one lane issues ----------------
+        // The order is PV of tile 0, its next S, PV of tile 1, its next S, ...: the tensor cores run them in
+        // this order, so S may be written as soon as the product that read P (in S) has been issued, and one
+        // query tile's products run while the other is in its softmax.
         constexpr uint32_t kIdescS = attn_idesc<T, false>(kTile, kTile);
         constexpr uint32_t kIdescO = attn_idesc<T, true>(kTile, D);
         constexpr uint32_t kStep = kTileBytes >> 4;               // a tile, in descriptor units
-        const uint64_t q_desc = sw128_kmajor_desc(smem_u32(s.q[w]));
+        const uint64_t q_desc = sw128_kmajor_desc(smem_u32(s.q[0]));
         const uint64_t k_desc = sw128_kmajor_desc(smem_u32(s.k[0]));
         const uint64_t v_desc = sw128_token_rows_desc(smem_u32(s.v[0]), kBlockBytes);
-        const uint32_t tS = tmem + kColS + w * 128u, tP = tmem + kColP + w * 128u, tO = tmem + kColO + w * 128u;
-        int kt = 0, i = 0, used = 0;                              // key tiles, own key tiles, own query tiles
+        int kt = 0, i[2] = {0, 0}, used[2] = {0, 0};              // key tiles, own key tiles, own query tiles
         for (int count = 0; ok; ++count) {
             ok = all(wait(s.item_full[count % kAhead], count / kAhead, kWaitMma));
             if (!ok) break;
             const Item& it = s.item[count % kAhead];
             const int h = __shfl_sync(0xFFFFFFFFu, it.h, 0);
             if (h < 0) break;
-            const int n = __shfl_sync(0xFFFFFFFFu, it.n[w], 0), other = __shfl_sync(0xFFFFFFFFu, it.n[1 - w], 0);
+            const int n[2] = {__shfl_sync(0xFFFFFFFFu, it.n[0], 0), __shfl_sync(0xFFFFFFFFu, it.n[1], 0)};
             const int len = __shfl_sync(0xFFFFFFFFu, it.end - it.begin, 0);
             const int redo = __shfl_sync(0xFFFFFFFFu, it.redo, 0);
             __syncwarp();
             if (lane == 0) mbar_arrive(&s.item_empty[count % kAhead]);
-            if (n > 0) ok = all(wait(s.q_full[w], used, kWaitMma));
-            // One tile's scores, then the product of its weights: the tensor cores run them in this order,
-            // so S may be written as soon as the product that read P (in S) has been issued.
-            const int most = max(n, other);
-            for (int t = 0; ok && t < most; ++t, ++kt) {
-                const int slot = kt % kSlots;
-                ok = all(wait(s.k_full[slot], kt / kSlots, kWaitMma));
-                if (!ok) break;
-                if (t < n) {
-                    tc_fence_after();
-                    const uint64_t k = k_desc + static_cast<uint32_t>(slot) * kStep;
-                    if (elect_one()) {
+            const int most = max(n[0], n[1]);
+            // S of query tile x and key tile t
+            auto scores = [&](int x, int t) {
+                if (t == 0 && !all(wait(s.q_full[x], used[x], kWaitMma))) return false;
+                tc_fence_after();
+                if (elect_one()) {
+                    const uint64_t q = q_desc + static_cast<uint32_t>(x) * kStep;
+                    const uint64_t k = k_desc + static_cast<uint32_t>((kt + t) % kSlots) * kStep;
 #pragma unroll
-                        for (int d = 0; d < D / 16; ++d) {
-                            const uint64_t off = (static_cast<uint32_t>(d / 4) * kBlockBytes + (d % 4) * 32) >> 4;
-                            mma_issue<false>(tS, q_desc + off, k + off, kIdescS, d != 0 ? 1u : 0u);
-                        }
-                        mma_commit(&s.s_full[w]);
-                        mma_commit(&s.k_empty[slot]);
-                        if (t + 1 == n) mma_commit(&s.q_empty[w]);
+                    for (int d = 0; d < D / 16; ++d) {
+                        const uint64_t off = (static_cast<uint32_t>(d / 4) * kBlockBytes + (d % 4) * 32) >> 4;
+                        mma_issue<false>(tmem + kColS + x * 128u, q + off, k + off, kIdescS, d != 0 ? 1u : 0u);
                     }
-                    __syncwarp();
-                } else if (elect_one()) {
-                    mbar_arrive(&s.k_empty[slot]);
+                    mma_commit(&s.s_full[x]);
+                    if (t + 1 == n[x]) mma_commit(&s.q_empty[x]);
                 }
-                ok = all(wait(s.v_full[slot], kt / kSlots, kWaitMma));
+                __syncwarp();
+                return true;
+            };
+            // O += P V
+            auto product = [&](int x, int t) {
+                if (!all(wait(s.p_high[x], i[x], kWaitMma) &&
+                         (t > 0 || used[x] == 0 || wait(s.o_empty[x], used[x] - 1, kWaitMma))))
+                    return false;
+                tc_fence_after();
+                const uint64_t v = v_desc + static_cast<uint32_t>((kt + t) % kSlots) * kStep;
+                const uint32_t tP = tmem + kColP + x * 128u, tO = tmem + kColO + x * 128u;
+                const uint32_t onto = t == 0 && redo == 0 ? 0u : 1u;   // done again, O starts from what is there
+                // tokens 64..127 first: their weights are ready first
+                if (elect_one()) {
+#pragma unroll
+                    for (int y = 4; y < 8; ++y) mma_issue_ta(tO, tP + y * 8, v + y * 128, kIdescO, y == 4 ? onto : 1u);
+                }
+                __syncwarp();
+                if (!all(wait(s.p_low[x], i[x], kWaitMma))) return false;
+                tc_fence_after();
+                if (elect_one()) {
+#pragma unroll
+                    for (int y = 0; y < 4; ++y) mma_issue_ta(tO, tP + y * 8, v + y * 128, kIdescO, 1u);
+                    mma_commit(&s.pv_done[x]);
+                }
+                __syncwarp();
+                ++i[x];
+                return true;
+            };
+            if (most > 0) ok = all(wait(s.k_full[kt % kSlots], kt / kSlots, kWaitMma));
+            for (int x = 0; ok && x < 2; ++x)
+                if (n[x] > 0) ok = scores(x, 0);
+            if (!ok) break;
+            if (most > 0 && elect_one()) mma_commit(&s.k_empty[kt % kSlots]);
+            __syncwarp();
+            for (int t = 0; t < most; ++t) {
+                const int slot = (kt + t) % kSlots;
+                ok = all(wait(s.v_full[slot], (kt + t) / kSlots, kWaitMma));
                 if (!ok) break;
-                if (t < n) {
-                    const int held = len - t * kTile;
-                    if (held < kTile) {                           // behind the sequence's end nothing may count
-                        const int pieces = (kTile - held) * 8;    // of 16 bytes, per block
-                        for (int y = 0; y < kHalves; ++y)
-                            for (int x = static_cast<int>(lane); x < pieces; x += 32)
-                                *reinterpret_cast<uint4*>(s.v[slot] + y * kBlockBytes + held * 128 + x * 16) =
-                                    make_uint4(0u, 0u, 0u, 0u);
-                        fence_proxy_async_smem();
-                        __syncwarp();
-                    }
-                    ok = all(wait(s.p_high[w], i, kWaitMma) && (t > 0 || used == 0 || wait(s.o_empty[w], used - 1, kWaitMma)));
-                    if (!ok) break;
-                    tc_fence_after();
-                    const uint64_t v = v_desc + static_cast<uint32_t>(slot) * kStep;
-                    const uint32_t onto = t == 0 && redo == 0 ? 0u : 1u;   // done again, O starts from what is there
-                    // tokens 64..127 first: their weights are ready first
-                    if (elect_one()) {
-#pragma unroll
-                        for (int x = 4; x < 8; ++x) mma_issue_ta(tO, tP + x * 8, v + x * 128, kIdescO, x == 4 ? onto : 1u);
-                    }
+                const int held = len - t * kTile;
+                if (held < kTile) {                               // behind the sequence's end nothing may count
+                    const int pieces = (kTile - held) * 8;        // of 16 bytes, per block
+                    for (int y = 0; y < kHalves; ++y)
+                        for (int x = static_cast<int>(lane); x < pieces; x += 32)
+                            *reinterpret_cast<uint4*>(s.v[slot] + y * kBlockBytes + held * 128 + x * 16) =
+                                make_uint4(0u, 0u, 0u, 0u);
+                    fence_proxy_async_smem();
                     __syncwarp();
-                    ok = all(wait(s.p_low[w], i, kWaitMma));
-                    if (!ok) break;
-                    tc_fence_after();
-                    if (elect_one()) {
+                }
 #pragma unroll
-                        for (int x = 0; x < 4; ++x) mma_issue_ta(tO, tP + x * 8, v + x * 128, kIdescO, 1u);
-                        mma_commit(&s.pv_done[w]);
-                        mma_commit(&s.v_empty[slot]);
+                for (int x = 0; x < 2; ++x) {
+                    if (ok && t < n[x]) ok = product(x, t);
+                    if (ok && t + 1 < n[x]) {
+                        ok = all(wait(s.k_full[(kt + t + 1) % kSlots], (kt + t + 1) / kSlots, kWaitMma));
+                        if (ok) ok = scores(x, t + 1);
                     }
-                    __syncwarp();
-                    ++i;
-                } else if (elect_one()) {
-                    mbar_arrive(&s.v_empty[slot]);
+                }
+                if (!ok) break;
+                if (elect_one()) {
+                    mma_commit(&s.v_empty[slot]);
+                    if (t + 1 < most) mma_commit(&s.k_empty[(kt + t + 1) % kSlots]);
                 }
                 __syncwarp();
             }
-            if (n > 0) ++used;
+            kt += most;
+#pragma unroll
+            for (int x = 0; x < 2; ++x) used[x] += n[x] > 0 ? 1 : 0;
         }
-        if (elect_one()) mma_commit(&s.drain[w]);
+        if (elect_one()) mma_commit(&s.drain);
         __syncwarp();
         const long long t0 = global_ns();
-        while (!mbar_try_wait(&s.drain[w], 0) && global_ns() - t0 < a.timeout_ns) {
+        while (!mbar_try_wait(&s.drain, 0) && global_ns() - t0 < a.timeout_ns) {
         }
         __syncwarp();
-    } else {
+    } else if (warp >= 4) {
         // ---------------- softmax and output of query tile w ----------------
         const int w = static_cast<int>(warp >= 8 ? 1 : 0);
         const uint32_t bar = 1u + static_cast<uint32_t>(w);
@@ -463,35 +481,41 @@ prompt_attention_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_co
                 tc_fence_after();
                 const int seen = limit - t * kTile;
                 const bool masked = __any_sync(0xFFFFFFFFu, seen < kTile);
-                // 64 scores at a time in registers: the first half for the maximum only
-                uint32_t r[64];
-                auto load = [&](int c0) {
-                    tmem_ld32(tS + c0, r);
-                    tmem_ld32(tS + c0 + 32, r + 32);
-                    tmem_wait_ld();
-                    if (masked) {
+                // 64 scores at a time in registers, 32 of them on their way while the others are worked on
+                uint32_t r[2][32];
+                auto load = [&](int x, int c0) { tmem_ld32(tS + c0, r[x]); };
+                auto hide = [&](int x, int c0) {
+                    if (!masked) return;
 #pragma unroll
-                        for (int c = 0; c < 64; ++c)
-                            if (c0 + c >= seen) r[c] = __float_as_uint(none);
-                    }
+                    for (int c = 0; c < 32; ++c)
+                        if (c0 + c >= seen) r[x][c] = __float_as_uint(none);
                 };
                 float best[4] = {none, none, none, none};
-                auto most = [&] {
+                auto most = [&](int x, int c0) {
+                    hide(x, c0);
                     if (!falling) {
 #pragma unroll
-                        for (int c = 0; c < 64; c += 8)
+                        for (int c = 0; c < 32; c += 8)
 #pragma unroll
-                            for (int x = 0; x < 4; ++x)
-                                best[x] = fmaxf(fmaxf(best[x], __uint_as_float(r[c + x])), __uint_as_float(r[c + 4 + x]));
+                            for (int e = 0; e < 4; ++e)
+                                best[e] = max3(best[e], __uint_as_float(r[x][c + e]), __uint_as_float(r[x][c + 4 + e]));
                     } else {
 #pragma unroll
-                        for (int c = 0; c < 64; ++c) best[c & 3] = fminf(best[c & 3], __uint_as_float(r[c]));
+                        for (int c = 0; c < 32; ++c) best[c & 3] = fminf(best[c & 3], __uint_as_float(r[x][c]));
                     }
                 };
-                load(0);
-                most();
-                load(64);
-                most();
+                load(0, 0);
+                load(1, 32);
+                tmem_wait_ld32(r[0]);
+                tmem_wait_ld32(r[1]);
+                most(0, 0);
+                load(0, 64);
+                most(1, 32);
+                load(1, 96);
+                tmem_wait_ld32(r[0]);
+                tmem_wait_ld32(r[1]);
+                most(0, 64);
+                most(1, 96);
                 const float top = falling ? fminf(fminf(best[0], best[1]), fminf(best[2], best[3]))
                                           : fmaxf(fmaxf(best[0], best[1]), fmaxf(best[2], best[3]));
                 const float mt = top == none ? -INFINITY : top * sl2;
@@ -521,36 +545,46 @@ prompt_attention_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_co
                     }
                 }
                 const float ref = m2 == -INFINITY ? 0.0f : m2;
-                float sum[4] = {0.0f, 0.0f, 0.0f, 0.0f};
-                auto weigh = [&](int c0) {                                // 64 weights, to P
+                float2 sum[4] = {};
+                const float2 slope = make_float2(sl2, sl2), shift = make_float2(-ref, -ref);
+                // 32 weights, to P.  Without a mask it is one straight piece of code, for which the compiler
+                // finds an order that keeps the exponential's unit (4 cycles a warp) at work.
+                auto weigh = [&](int x, int c0) {
+                    uint32_t p[16];
+                    if (!masked) {
 #pragma unroll
-                    for (int c = 0; c < 64; ++c)
-                        r[c] = __float_as_uint(exp2_approx(fmaf(__uint_as_float(r[c]), sl2, -ref)));
-                    if (masked) {
+                        for (int c = 0; c < 32; c += 2) {
+                            const float2 y = __ffma2_rn(make_float2(__uint_as_float(r[x][c]), __uint_as_float(r[x][c + 1])), slope, shift);
+                            const float2 e = make_float2(exp2_approx(y.x), exp2_approx(y.y));
+                            sum[(c >> 1) & 3] = __fadd2_rn(sum[(c >> 1) & 3], e);
+                            p[c >> 1] = pack2(e.x, e.y, T{});
+                        }
+                    } else {
 #pragma unroll
-                        for (int c = 0; c < 64; ++c)
-                            if (c0 + c >= seen) r[c] = 0u;
+                        for (int c = 0; c < 32; c += 2) {
+                            const float2 y = __ffma2_rn(make_float2(__uint_as_float(r[x][c]), __uint_as_float(r[x][c + 1])), slope, shift);
+                            const float2 e = make_float2(c0 + c < seen ? exp2_approx(y.x) : 0.0f,
+                                                         c0 + c + 1 < seen ? exp2_approx(y.y) : 0.0f);
+                            sum[(c >> 1) & 3] = __fadd2_rn(sum[(c >> 1) & 3], e);
+                            p[c >> 1] = pack2(e.x, e.y, T{});
+                        }
                     }
-#pragma unroll
-                    for (int c = 0; c < 64; c += 32) {
-                        uint32_t p[16];
-#pragma unroll
-                        for (int x = 0; x < 16; ++x)
-                            p[x] = pack2(__uint_as_float(r[c + 2 * x]), __uint_as_float(r[c + 2 * x + 1]), T{});
-                        tmem_st16(tP + (c0 + c) / 2, p);
-                    }
-#pragma unroll
-                    for (int c = 0; c < 64; ++c) sum[c & 3] += __uint_as_float(r[c]);
+                    tmem_st16(tP + c0 / 2, p);
                 };
-                weigh(64);                                                // P takes the place of scores 64..127
+                weigh(0, 64);                                             // P takes the place of scores 64..127
+                load(0, 0);
+                weigh(1, 96);
                 tmem_wait_st();
                 if (!it.redo) {
                     tc_fence_before();
                     mbar_arrive(&s.p_high[w]);
                 }
-                load(0);
-                weigh(0);
-                l += (sum[0] + sum[1]) + (sum[2] + sum[3]);
+                tmem_wait_ld32(r[0]);
+                load(1, 32);
+                weigh(0, 0);
+                tmem_wait_ld32(r[1]);
+                weigh(1, 32);
+                l += ((sum[0].x + sum[0].y) + (sum[1].x + sum[1].y)) + ((sum[2].x + sum[2].y) + (sum[3].x + sum[3].y));
                 tmem_wait_st();
                 if (it.redo) {
                     const int slot = (kt + t) % kSlots;
