@@ -6,12 +6,12 @@
 // streams the sequence's keys and values past its two tiles in tiles of 128 tokens.  While one tile's
 // scores go through the softmax, the tensor cores work for the other.
 //
-//   warp 0      takes the items and loads (TMA) queries, keys and values
-//   warp 1      clears the tokens outside every sequence
-//   warp 2      issues S = Q K^T and O += P V on tcgen05 (M = 128, fp32 in tensor memory; P replaces
-//               half of S)
-//   warps 4-7, 8-11  softmax and output of one query tile each: a thread per row, running maximum and
-//               sum in fp32, weights rounded to the inputs' type
+//   warps 0-7, 8-15  softmax and output of one query tile each: two threads per row, 64 of a key
+//                    tile's tokens each; running maximum and sum in fp32, weights rounded to the
+//                    inputs' type; at the end zeros for the tokens outside every sequence
+//   warp 16          takes the items and loads (TMA) queries, keys and values
+//   warp 17          issues S = Q K^T and O += P V on tcgen05 (M = 128, fp32 in tensor memory; P
+//                    replaces half of S)
 //
 // The running maximum is raised only when a tile exceeds it by 2^8 (O is then rescaled): weights up to
 // 2^8 lose nothing in a floating type, and the rescaling leaves the common path.
@@ -30,14 +30,17 @@ namespace dspark {
 namespace {
 
 constexpr int kTile = 128;                 // key tokens per tile, and MMA rows
-constexpr int kThreads = 384;
-constexpr int kRowThreads = 128;           // softmax threads of a query tile
+constexpr int kThreads = 576;               // 112 registers each
+constexpr int kRowThreads = 256;           // softmax threads of a query tile: two to a row, 64 of a key tile's tokens each
 constexpr float kRaise = 8.0f;             // log2 units
 constexpr int kAhead = 4;                  // items between the loads and the results
 constexpr int kRedo = 2 * kAhead;          // items of which a query tile waits to be done again: at most those under way
 constexpr int kSlots = 2;                  // key tiles, and value tiles, in flight
 constexpr int kOrdered = 256;              // up to so many sequences the items are put in order of their size
 constexpr uint32_t kColS = 0, kColP = 64, kColO = 256, kTmemCols = 512;    // S and O of tile 1: + 128
+// named barriers: + query tile; + 4 * query tile + quadrant, the two warps of the same rows; + query tile
+constexpr uint32_t kWarpLoad = 16, kWarpMma = 17;
+constexpr uint32_t kBarTile = 1, kBarRows = 3, kBarFirst = 11;
 constexpr uint32_t kWaitLoad = 0x901, kWaitMma = 0x902, kWaitSoftmax = 0x903;
 
 struct Plan {
@@ -166,16 +169,16 @@ struct PromptSmem {
     alignas(1024) uint8_t q[2][kTileBytes];
     alignas(1024) uint8_t k[kSlots][kTileBytes];
     alignas(1024) uint8_t v[kSlots][kTileBytes];
-    alignas(1024) float4 stage[2][kTile * 8];                     // 32 columns of a query tile's rows
+    alignas(1024) uint4 stage[16][128];                           // 32 columns of a warp's rows; a row of values where a tile is done again
     Item item[kAhead];
-    float row[2][D];
+    float half[2][2][kTile];                                      // by query tile and half of the key tiles: a row's largest score, or sum
     uint32_t masks[2][4];
     int redo[2][kRedo];                                           // items to be done again, by query tile
     unsigned int redo_count[2];                                   // entries written so far
     uint64_t item_full[kAhead], item_empty[kAhead];
     uint64_t q_full[2], q_empty[2];
     uint64_t k_full[kSlots], k_empty[kSlots], v_full[kSlots], v_empty[kSlots];
-    uint64_t s_full[2], p_high[2], p_low[2], pv_done[2], o_empty[2], drain;
+    uint64_t s_full[2], p_first[2], p_last[2], pv_done[2], o_empty[2], drain;
     uint32_t tmem_base;
 };
 
@@ -200,8 +203,8 @@ prompt_attention_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_co
             mbar_init(&s.q_full[i], 1);
             mbar_init(&s.q_empty[i], 1);
             mbar_init(&s.s_full[i], 1);
-            mbar_init(&s.p_high[i], kRowThreads);
-            mbar_init(&s.p_low[i], kRowThreads);
+            mbar_init(&s.p_first[i], kRowThreads);
+            mbar_init(&s.p_last[i], kRowThreads);
             mbar_init(&s.pv_done[i], 1);
             mbar_init(&s.o_empty[i], kRowThreads);
         }
@@ -218,7 +221,7 @@ prompt_attention_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_co
         prefetch_tensormap(&tmK);
         prefetch_tensormap(&tmV);
     }
-    if (warp == 2) {
+    if (warp == kWarpMma) {
         tmem_alloc(&s.tmem_base, kTmemCols);
         tmem_relinquish();
     }
@@ -234,7 +237,7 @@ prompt_attention_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_co
         return mbar_wait(&bar, static_cast<uint32_t>(use) & 1u, ws, a.timeout_ns, where);
     };
 
-    if (warp == 0) {
+    if (warp == kWarpLoad) {
         // ---------------- items and loads ----------------
         if (lane == 0) {
             const uint64_t keep = l2_policy_evict_last();
@@ -318,18 +321,7 @@ prompt_attention_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_co
                 }
             }
         }
-    } else if (warp == 1) {
-        // ---------------- tokens outside every sequence ----------------
-        const int begin = a.plan->begin, end = a.plan->end;
-        const int outside = begin + (a.T - end);
-        for (int x = blockIdx.x; x < outside; x += gridDim.x) {
-            const long long t = x < begin ? x : end + (x - begin);
-            uint4* dst = reinterpret_cast<uint4*>(static_cast<T*>(a.out) + t * a.Hq * D);
-            for (int y = static_cast<int>(lane); y < a.Hq * (D / 8); y += 32) dst[y] = make_uint4(0u, 0u, 0u, 0u);
-            if (a.lse)
-                for (int y = static_cast<int>(lane); y < a.Hq; y += 32) a.lse[t * a.Hq + y] = -INFINITY;
-        }
-    } else if (warp == 2) {
+    } else if (warp == kWarpMma) {
         // ---------------- products: the whole warp waits, one lane issues ----------------
         // The order is PV of tile 0, its next S, PV of tile 1, its next S, ...: the tensor cores run them in
         // this order, so S may be written as soon as the product that read P (in S) has been issued, and one
@@ -373,24 +365,30 @@ prompt_attention_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_co
             };
             // O += P V
             auto product = [&](int x, int t) {
-                if (!all(wait(s.p_high[x], i[x], kWaitMma) &&
+                if (!all(wait(s.p_first[x], i[x], kWaitMma) &&
                          (t > 0 || used[x] == 0 || wait(s.o_empty[x], used[x] - 1, kWaitMma))))
                     return false;
                 tc_fence_after();
                 const uint64_t v = v_desc + static_cast<uint32_t>((kt + t) % kSlots) * kStep;
                 const uint32_t tP = tmem + kColP + x * 128u, tO = tmem + kColO + x * 128u;
                 const uint32_t onto = t == 0 && redo == 0 ? 0u : 1u;   // done again, O starts from what is there
-                // tokens 64..127 first: their weights are ready first
+                // 16 tokens a product; of each half of the tile, the first 32 tokens' weights are ready first
                 if (elect_one()) {
 #pragma unroll
-                    for (int y = 4; y < 8; ++y) mma_issue_ta(tO, tP + y * 8, v + y * 128, kIdescO, y == 4 ? onto : 1u);
+                    for (int z = 0; z < 4; ++z) {
+                        const int y = z + (z & 2);
+                        mma_issue_ta(tO, tP + y * 8, v + y * 128, kIdescO, z == 0 ? onto : 1u);
+                    }
                 }
                 __syncwarp();
-                if (!all(wait(s.p_low[x], i[x], kWaitMma))) return false;
+                if (!all(wait(s.p_last[x], i[x], kWaitMma))) return false;
                 tc_fence_after();
                 if (elect_one()) {
 #pragma unroll
-                    for (int y = 0; y < 4; ++y) mma_issue_ta(tO, tP + y * 8, v + y * 128, kIdescO, 1u);
+                    for (int z = 0; z < 4; ++z) {
+                        const int y = 2 + z + (z & 2);
+                        mma_issue_ta(tO, tP + y * 8, v + y * 128, kIdescO, 1u);
+                    }
                     mma_commit(&s.pv_done[x]);
                 }
                 __syncwarp();
@@ -442,28 +440,30 @@ prompt_attention_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_co
         while (!mbar_try_wait(&s.drain, 0) && global_ns() - t0 < a.timeout_ns) {
         }
         __syncwarp();
-    } else if (warp >= 4) {
+    } else {
         // ---------------- softmax and output of query tile w ----------------
-        const int w = static_cast<int>(warp >= 8 ? 1 : 0);
-        const uint32_t bar = 1u + static_cast<uint32_t>(w);
+        const int w = static_cast<int>(warp >> 3);
+        const int part = static_cast<int>(warp >> 2) & 1;  // 64 of the key tile's tokens, half of the output's columns
         const uint32_t quad = warp & 3u;
+        const uint32_t bar_tile = kBarTile + static_cast<uint32_t>(w), bar_rows = kBarRows + 4u * static_cast<uint32_t>(w) + quad;
         const uint32_t lanes = (quad * 32u) << 16;
-        const uint32_t tS = tmem + lanes + kColS + w * 128u, tP = tmem + lanes + kColP + w * 128u, tO = tmem + lanes + kColO + w * 128u;
+        const uint32_t tS = tmem + lanes + kColS + w * 128u + part * 64u, tP = tmem + lanes + kColP + w * 128u + part * 32u;
+        const uint32_t tO = tmem + lanes + kColO + w * 128u + part * (D / 2u);
         const int row = static_cast<int>(quad * 32u + lane);
-        const int row_tok = row / a.group, row_head = row - row_tok * a.group;
+        const int row_tok = row / a.group;
         const bool row_used = row < a.tile_tokens * a.group;
         const float sl2 = a.scale * kLog2e;
         const bool falling = sl2 < 0.0f;                          // the largest score is the smallest product
         const float none = falling ? INFINITY : -INFINITY;
         int i = 0;                                                // own key tiles
         int kt = 0;                                               // key tiles
-        int used = 0;                                             // own query tiles
         for (int count = 0;; ++count) {
-            ok = named_bar_and(bar, kRowThreads, wait(s.item_full[count % kAhead], count / kAhead, kWaitSoftmax));
+            ok = named_bar_and(bar_tile, kRowThreads, wait(s.item_full[count % kAhead], count / kAhead, kWaitSoftmax));
             if (!ok) break;
-            const Item it = s.item[count % kAhead];
+            const Item& it = s.item[count % kAhead];
             if (it.h < 0) break;
             const int n = it.n[w], len = it.end - it.begin;
+            const bool redo = it.redo != 0;
             if (n == 0) {
                 kt += it.n[1 - w];
                 mbar_arrive(&s.item_empty[count % kAhead]);
@@ -475,65 +475,60 @@ prompt_attention_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_co
             float m2 = -INFINITY, l = 0.0f;
             for (int t = 0; t < n; ++t, ++i) {
                 bool go = wait(s.s_full[w], i, kWaitSoftmax);
-                if (it.redo) go = named_bar_and(bar, kRowThreads, go);    // these meet in barriers below
-                ok = all(go);
-                if (!ok) break;
-                tc_fence_after();
-                const int seen = limit - t * kTile;
-                const bool masked = __any_sync(0xFFFFFFFFu, seen < kTile);
-                // 64 scores at a time in registers, 32 of them on their way while the others are worked on
+                if (redo) go = named_bar_and(bar_tile, kRowThreads, go);  // these meet in barriers below
+                go = all(go);
+                // 64 scores in registers
                 uint32_t r[2][32];
-                auto load = [&](int x, int c0) { tmem_ld32(tS + c0, r[x]); };
-                auto hide = [&](int x, int c0) {
-                    if (!masked) return;
+                const int seen = limit - t * kTile - part * 64;
+                const bool masked = __any_sync(0xFFFFFFFFu, seen < 64);
+                tc_fence_after();
+                tmem_ld32(tS, r[0]);
+                tmem_ld32(tS + 32, r[1]);
+                tmem_wait_ld32(r[0]);
+                tmem_wait_ld32(r[1]);
+                if (masked) {
 #pragma unroll
-                    for (int c = 0; c < 32; ++c)
-                        if (c0 + c >= seen) r[x][c] = __float_as_uint(none);
-                };
+                    for (int c = 0; c < 64; ++c)
+                        if (c >= seen) r[c >> 5][c & 31] = __float_as_uint(none);
+                }
                 float best[4] = {none, none, none, none};
-                auto most = [&](int x, int c0) {
-                    hide(x, c0);
-                    if (!falling) {
+                if (!falling) {
 #pragma unroll
-                        for (int c = 0; c < 32; c += 8)
+                    for (int c = 0; c < 64; c += 8)
 #pragma unroll
-                            for (int e = 0; e < 4; ++e)
-                                best[e] = max3(best[e], __uint_as_float(r[x][c + e]), __uint_as_float(r[x][c + 4 + e]));
-                    } else {
+                        for (int e = 0; e < 4; ++e)
+                            best[e] = max3(best[e], __uint_as_float(r[c >> 5][(c & 31) + e]),
+                                           __uint_as_float(r[c >> 5][(c & 31) + 4 + e]));
+                } else {
 #pragma unroll
-                        for (int c = 0; c < 32; ++c) best[c & 3] = fminf(best[c & 3], __uint_as_float(r[x][c]));
-                    }
-                };
-                load(0, 0);
-                load(1, 32);
-                tmem_wait_ld32(r[0]);
-                tmem_wait_ld32(r[1]);
-                most(0, 0);
-                load(0, 64);
-                most(1, 32);
-                load(1, 96);
-                tmem_wait_ld32(r[0]);
-                tmem_wait_ld32(r[1]);
-                most(0, 64);
-                most(1, 96);
+                    for (int c = 0; c < 64; ++c) best[c & 3] = fminf(best[c & 3], __uint_as_float(r[c >> 5][c & 31]));
+                }
                 const float top = falling ? fminf(fminf(best[0], best[1]), fminf(best[2], best[3]))
                                           : fmaxf(fmaxf(best[0], best[1]), fmaxf(best[2], best[3]));
-                const float mt = top == none ? -INFINITY : top * sl2;
-                if (t == 0) {
-                    m2 = mt;
-                } else {
-                    const bool raise = valid && mt > m2 + kRaise;
-                    if (__any_sync(0xFFFFFFFFu, raise)) {
-                        ok = all(wait(s.pv_done[w], i - 1, kWaitSoftmax));
-                        if (!ok && !it.redo) break;                       // else at the vote below
+                float mt = top == none ? -INFINITY : top * sl2;
+                // The two threads of a row meet: P may then replace the scores, and if either finds the maximum
+                // too low (or has given up) they exchange theirs.
+                bool raise = t == 0 || !go || (valid && mt > m2 + kRaise);
+                if (t > 0) raise = !named_bar_and(bar_rows, 64, !raise);
+                ok = go;
+                if (raise) {
+                    s.half[w][part][row] = mt;
+                    if (t > 0) go = go && all(wait(s.pv_done[w], i - 1, kWaitSoftmax));
+                    ok = named_bar_and(bar_rows, 64, go);
+                    if (!ok && !redo) break;                              // else at the vote below
+                    mt = fmaxf(mt, s.half[w][1 - part][row]);
+                    if (t == 0) {
+                        m2 = mt;
+                    } else if (ok) {
                         tc_fence_after();
-                        const float f = raise ? exp2_approx(m2 - mt) : 1.0f;
-                        if (raise) {
+                        const bool up = valid && mt > m2 + kRaise;
+                        const float f = up ? exp2_approx(m2 - mt) : 1.0f;
+                        if (up) {
                             l *= f;
                             m2 = mt;
                         }
 #pragma unroll 1
-                        for (uint32_t c = 0; c < D; c += 16) {
+                        for (uint32_t c = 0; c < D / 2; c += 16) {
                             uint32_t o[16];
                             tmem_ld16(tO + c, o);
                             tmem_wait_ld();
@@ -545,144 +540,156 @@ prompt_attention_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_co
                     }
                 }
                 const float ref = m2 == -INFINITY ? 0.0f : m2;
-                float2 sum[4] = {};
+                float2 sum[2] = {};
                 const float2 slope = make_float2(sl2, sl2), shift = make_float2(-ref, -ref);
                 // 32 weights, to P.  Without a mask it is one straight piece of code, for which the compiler
                 // finds an order that keeps the exponential's unit (4 cycles a warp) at work.
-                auto weigh = [&](int x, int c0) {
+                auto weigh = [&](int x) {
                     uint32_t p[16];
                     if (!masked) {
 #pragma unroll
                         for (int c = 0; c < 32; c += 2) {
                             const float2 y = __ffma2_rn(make_float2(__uint_as_float(r[x][c]), __uint_as_float(r[x][c + 1])), slope, shift);
                             const float2 e = make_float2(exp2_approx(y.x), exp2_approx(y.y));
-                            sum[(c >> 1) & 3] = __fadd2_rn(sum[(c >> 1) & 3], e);
+                            sum[(c >> 1) & 1] = __fadd2_rn(sum[(c >> 1) & 1], e);
                             p[c >> 1] = pack2(e.x, e.y, T{});
                         }
                     } else {
 #pragma unroll
                         for (int c = 0; c < 32; c += 2) {
                             const float2 y = __ffma2_rn(make_float2(__uint_as_float(r[x][c]), __uint_as_float(r[x][c + 1])), slope, shift);
-                            const float2 e = make_float2(c0 + c < seen ? exp2_approx(y.x) : 0.0f,
-                                                         c0 + c + 1 < seen ? exp2_approx(y.y) : 0.0f);
-                            sum[(c >> 1) & 3] = __fadd2_rn(sum[(c >> 1) & 3], e);
+                            const float2 e = make_float2(x * 32 + c < seen ? exp2_approx(y.x) : 0.0f,
+                                                         x * 32 + c + 1 < seen ? exp2_approx(y.y) : 0.0f);
+                            sum[(c >> 1) & 1] = __fadd2_rn(sum[(c >> 1) & 1], e);
                             p[c >> 1] = pack2(e.x, e.y, T{});
                         }
                     }
-                    tmem_st16(tP + c0 / 2, p);
+                    tmem_st16(tP + x * 16, p);
+                    tmem_wait_st();
                 };
-                weigh(0, 64);                                             // P takes the place of scores 64..127
-                load(0, 0);
-                weigh(1, 96);
-                tmem_wait_st();
-                if (!it.redo) {
+                weigh(0);
+                if (!redo) {
                     tc_fence_before();
-                    mbar_arrive(&s.p_high[w]);
+                    mbar_arrive(&s.p_first[w]);
                 }
-                tmem_wait_ld32(r[0]);
-                load(1, 32);
-                weigh(0, 0);
-                tmem_wait_ld32(r[1]);
-                weigh(1, 32);
-                l += ((sum[0].x + sum[0].y) + (sum[1].x + sum[1].y)) + ((sum[2].x + sum[2].y) + (sum[3].x + sum[3].y));
-                tmem_wait_st();
-                if (it.redo) {
+                weigh(1);
+                l += (sum[0].x + sum[0].y) + (sum[1].x + sum[1].y);
+                if (redo) {
                     const int slot = (kt + t) % kSlots;
                     bool there = ok && wait(s.v_full[slot], (kt + t) / kSlots, kWaitSoftmax);
                     // O is about to be changed here: the products before must be complete
                     if (there && t > 0) there = wait(s.pv_done[w], i - 1, kWaitSoftmax);
-                    ok = named_bar_and(bar, kRowThreads, there);
-                    if (!ok) break;
-                    tc_fence_after();
-                    if (t == 0) {
+                    there = all(there);
+                    if (there && t == 0) {
                         uint32_t zero[16];
 #pragma unroll
                         for (int c = 0; c < 16; ++c) zero[c] = 0u;
-                        for (uint32_t c = 0; c < D; c += 16) tmem_st16(tO + c, zero);
+                        for (uint32_t c = 0; c < D / 2; c += 16) tmem_st16(tO + c, zero);
                         tmem_wait_st();
                     }
-                    move_infinities<T>(s.v[slot], kBlockBytes, kHalves, row, len - t * kTile, 0, min(seen, kTile), tP, tO,
-                                       s.row[w], s.masks[w], bar);
-                    fence_proxy_async_smem();
                     tc_fence_before();
-                    mbar_arrive(&s.p_high[w]);
+                    ok = named_bar_and(bar_tile, kRowThreads, there);     // P and O of both halves are in place
+                    if (!ok) break;
+                    tc_fence_after();
+                    if (part == 0) {
+                        move_infinities<T>(s.v[slot], kBlockBytes, kHalves, row, len - t * kTile, 0,
+                                           min(limit - t * kTile, kTile), tP, tO, reinterpret_cast<float*>(s.stage[8 * w]), s.masks[w],
+                                           kBarFirst + static_cast<uint32_t>(w));
+                        fence_proxy_async_smem();
+                    }
+                    tc_fence_before();
+                    mbar_arrive(&s.p_first[w]);
                 }
                 tc_fence_before();
-                mbar_arrive(&s.p_low[w]);
+                mbar_arrive(&s.p_last[w]);
             }
             kt += max(n, it.n[1 - w]);
 
             // ---------------- the query tile's rows ----------------
             if (ok) ok = all(wait(s.pv_done[w], i - 1, kWaitSoftmax));
-            ok = named_bar_and(bar, kRowThreads, ok);                     // the warps meet again: give up together
+            s.half[w][part][row] = l;
+            ok = named_bar_and(bar_tile, kRowThreads, ok);                // the warps meet again: give up together
             if (!ok) break;
             {
                 tc_fence_after();
+                l = s.half[w][0][row] + s.half[w][1][row];
                 const float f = l != 0.0f ? 1.0f / l : 0.0f;
                 float check[4] = {l * 0.0f, 0.0f, 0.0f, 0.0f};            // 0, or NaN
                 // 32 columns at a time through shared memory, so that four lanes write a row's piece together
-                float4* stage = s.stage[w] + quad * 256;
+                uint4* stage = s.stage[warp];
                 const int piece = static_cast<int>(lane) & 3;             // eight columns
                 const int first = it.tok + w * a.tile_tokens;
                 const int rows = min(a.tile_tokens, len - first) * a.group;
                 const long long row0 = static_cast<long long>(it.begin + first) * a.Hq + it.h * a.group;
-                long long to[4];                                          // this lane's four rows (-1: none)
+                T* to[4];                                                 // this lane's four rows (null: none)
 #pragma unroll
                 for (int y = 0; y < 4; ++y) {
                     const int rr = static_cast<int>(quad) * 32 + y * 8 + (static_cast<int>(lane) >> 2);
                     const int rt = rr / a.group;
-                    to[y] = rr >= rows ? -1 : (row0 + static_cast<long long>(rt) * a.Hq + (rr - rt * a.group)) * D + piece * 8;
+                    to[y] = rr >= rows ? nullptr
+                                       : static_cast<T*>(a.out) + (row0 + static_cast<long long>(rt) * a.Hq + (rr - rt * a.group)) * D +
+                                             part * (D / 2) + piece * 8;
                 }
-#pragma unroll 1
-                for (int c = 0; c < D; c += 32) {
+#pragma unroll
+                for (int c = 0; c < D / 2; c += 32) {
                     float o[32];
                     tmem_ld32(tO + c, reinterpret_cast<uint32_t*>(o));
-                    tmem_wait_ld();
-                    if (c + 32 == D) {
+                    tmem_wait_ld32(reinterpret_cast<uint32_t*>(o));
+                    if (c + 32 == D / 2) {
                         tc_fence_before();
                         mbar_arrive(&s.o_empty[w]);
                     }
                     __syncwarp();                                         // the columns before have been read
 #pragma unroll
-                    for (int x = 0; x < 8; ++x) {
+                    for (int x = 0; x < 4; ++x) {
 #pragma unroll
-                        for (int e = 0; e < 4; ++e) check[e] = fmaf(o[4 * x + e], 0.0f, check[e]);
-                        stage[lane * 8 + (x ^ (lane & 7))] =
-                            make_float4(o[4 * x] * f, o[4 * x + 1] * f, o[4 * x + 2] * f, o[4 * x + 3] * f);
+                        for (int e = 0; e < 8; ++e) {
+                            check[e & 3] = fmaf(o[8 * x + e], 0.0f, check[e & 3]);
+                            o[8 * x + e] *= f;
+                        }
+                        stage[lane * 4 + (x ^ ((lane >> 1) & 3))] = pack8(o + 8 * x, T{});
                     }
                     __syncwarp();
 #pragma unroll
                     for (int y = 0; y < 4; ++y) {
-                        if (to[y] < 0) continue;
                         const int from = y * 8 + (static_cast<int>(lane) >> 2);
-                        const float4 p = stage[from * 8 + ((2 * piece) ^ (from & 7))];
-                        const float4 q = stage[from * 8 + ((2 * piece + 1) ^ (from & 7))];
-                        const float v[8] = {p.x, p.y, p.z, p.w, q.x, q.y, q.z, q.w};
-                        *reinterpret_cast<uint4*>(static_cast<T*>(a.out) + to[y] + c) = pack8(v, T{});
+                        if (to[y]) *reinterpret_cast<uint4*>(to[y] + c) = stage[from * 4 + (piece ^ ((from >> 1) & 3))];
                     }
                 }
-                if (valid && a.lse)
-                    a.lse[static_cast<long long>(it.begin + tok) * a.Hq + it.h * a.group + row_head] = lse_of(m2, l);
+                if (valid && a.lse && part == 0)
+                    a.lse[static_cast<long long>(it.begin + tok) * a.Hq + it.h * a.group + (row - row_tok * a.group)] = lse_of(m2, l);
                 // a row that is not finite: the tile is done again (before the item is given up, so that the
                 // loading warp learns of it in time)
-                if (!it.redo) {
+                if (!redo) {
                     const bool fine = !valid || check[0] + check[1] + check[2] + check[3] == 0.0f;
-                    if (!named_bar_and(bar, kRowThreads, fine) && row == 0) {
+                    if (!named_bar_and(bar_tile, kRowThreads, fine) && row == 0 && part == 0) {
                         const unsigned int at = s.redo_count[w];
                         s.redo[w][at % kRedo] = it.id;
                         __threadfence_block();
                         *reinterpret_cast<volatile unsigned int*>(&s.redo_count[w]) = at + 1;
                     }
                 }
-                ++used;
                 mbar_arrive(&s.item_empty[count % kAhead]);
             }
         }
     }
 
+    // ---------------- tokens outside every sequence ----------------
+    if (warp < kWarpLoad) {
+        const int begin = a.plan->begin, end = a.plan->end;
+        const int outside = begin + (a.T - end);
+        for (int x = blockIdx.x * static_cast<int>(kWarpLoad) + static_cast<int>(warp); x < outside; x += gridDim.x * static_cast<int>(kWarpLoad)) {
+            const long long t = x < begin ? x : end + (x - begin);
+            uint4* dst = reinterpret_cast<uint4*>(static_cast<T*>(a.out) + t * a.Hq * D);
+            for (int y = static_cast<int>(lane); y < a.Hq * (D / 8); y += 32) dst[y] = make_uint4(0u, 0u, 0u, 0u);
+            if (a.lse)
+                for (int y = static_cast<int>(lane); y < a.Hq; y += 32) a.lse[t * a.Hq + y] = -INFINITY;
+        }
+    }
+
     tc_fence_before();
     __syncthreads();
-    if (warp == 2) {
+    if (warp == kWarpMma) {
         __syncwarp();
         tc_fence_after();
         tmem_dealloc(tmem, kTmemCols);
