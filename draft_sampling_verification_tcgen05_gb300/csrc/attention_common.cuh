@@ -158,6 +158,16 @@ __device__ __noinline__ void move_infinities(uint8_t* tile, uint32_t block_bytes
     }
 }
 
+// mbar_wait with the waiting itself out of line: what is inlined where a wait is usually over is a few
+// instructions.
+inline __device__ __noinline__ bool mbar_wait_longer(uint64_t* bar, uint32_t parity, WsHeader* ws, long long timeout_ns, uint32_t where) {
+    return mbar_wait(bar, parity, ws, timeout_ns, where);
+}
+
+__device__ __forceinline__ bool mbar_wait_short(uint64_t* bar, uint32_t parity, WsHeader* ws, long long timeout_ns, uint32_t where) {
+    return mbar_try_wait(bar, parity) || mbar_wait_longer(bar, parity, ws, timeout_ns, where);
+}
+
 // Whether the phase of the given parity is complete, without waiting.
 __device__ __forceinline__ bool mbar_test(uint64_t* bar, uint32_t parity) {
     uint32_t ok;

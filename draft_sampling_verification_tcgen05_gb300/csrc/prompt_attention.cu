@@ -10,8 +10,8 @@
 //                    tile's tokens each; running maximum and sum in fp32, weights rounded to the
 //                    inputs' type; at the end zeros for the tokens outside every sequence
 //   warp 16          takes the items and loads (TMA) queries, keys and values
-//   warp 17          issues S = Q K^T and O += P V on tcgen05 (M = 128, fp32 in tensor memory; P
-//                    replaces half of S)
+//   warps 17, 18     issue S = Q K^T and O += P V of one query tile each on tcgen05 (M = 128, fp32 in
+//                    tensor memory; P replaces half of S)
 //
 // The running maximum is raised only when a tile exceeds it by 2^8 (O is then rescaled): weights up to
 // 2^8 lose nothing in a floating type, and the rescaling leaves the common path.
@@ -30,7 +30,7 @@ namespace dspark {
 namespace {
 
 constexpr int kTile = 128;                 // key tokens per tile, and MMA rows
-constexpr int kThreads = 576;               // 112 registers each
+constexpr int kThreads = 608;
 constexpr int kRowThreads = 256;           // softmax threads of a query tile: two to a row, 64 of a key tile's tokens each
 constexpr float kRaise = 8.0f;             // log2 units
 constexpr int kAhead = 4;                  // items between the loads and the results
@@ -178,7 +178,7 @@ struct PromptSmem {
     uint64_t item_full[kAhead], item_empty[kAhead];
     uint64_t q_full[2], q_empty[2];
     uint64_t k_full[kSlots], k_empty[kSlots], v_full[kSlots], v_empty[kSlots];
-    uint64_t s_full[2], p_first[2], p_last[2], pv_done[2], o_empty[2], drain;
+    uint64_t s_full[2], p_first[2], p_last[2], pv_done[2], o_empty[2], turn[2], drain;
     uint32_t tmem_base;
 };
 
@@ -197,12 +197,13 @@ prompt_attention_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_co
     if (threadIdx.x == 0) {
         for (int i = 0; i < kAhead; ++i) {
             mbar_init(&s.item_full[i], 1);
-            mbar_init(&s.item_empty[i], 2 * kRowThreads + 1);
+            mbar_init(&s.item_empty[i], 2 * kRowThreads + 2);
         }
         for (int i = 0; i < 2; ++i) {
             mbar_init(&s.q_full[i], 1);
             mbar_init(&s.q_empty[i], 1);
             mbar_init(&s.s_full[i], 1);
+            mbar_init(&s.turn[i], 1);
             mbar_init(&s.p_first[i], kRowThreads);
             mbar_init(&s.p_last[i], kRowThreads);
             mbar_init(&s.pv_done[i], 1);
@@ -210,11 +211,11 @@ prompt_attention_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_co
         }
         for (int i = 0; i < kSlots; ++i) {
             mbar_init(&s.k_full[i], 1);
-            mbar_init(&s.k_empty[i], 1);
+            mbar_init(&s.k_empty[i], 2);
             mbar_init(&s.v_full[i], 1);
-            mbar_init(&s.v_empty[i], 1);
+            mbar_init(&s.v_empty[i], 2);
         }
-        mbar_init(&s.drain, 1);
+        mbar_init(&s.drain, 2);
         s.redo_count[0] = s.redo_count[1] = 0u;
         fence_mbarrier_init();
         prefetch_tensormap(&tmQ);
@@ -234,7 +235,7 @@ prompt_attention_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_co
     bool ok = true;
     auto all = [&](bool x) { return __all_sync(0xFFFFFFFFu, x); };
     auto wait = [&](uint64_t& bar, int use, uint32_t where) {            // use: how often it completed before
-        return mbar_wait(&bar, static_cast<uint32_t>(use) & 1u, ws, a.timeout_ns, where);
+        return mbar_wait_short(&bar, static_cast<uint32_t>(use) & 1u, ws, a.timeout_ns, where);
     };
 
     if (warp == kWarpLoad) {
@@ -321,118 +322,109 @@ prompt_attention_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_co
                 }
             }
         }
-    } else if (warp == kWarpMma) {
-        // ---------------- products: the whole warp waits, one lane issues ----------------
-        // The order is PV of tile 0, its next S, PV of tile 1, its next S, ...: the tensor cores run them in
-        // this order, so S may be written as soon as the product that read P (in S) has been issued, and one
-        // query tile's products run while the other is in its softmax.
+    } else if (warp >= kWarpMma) {
+        // ---------------- products of query tile w: the whole warp waits, one lane issues ----------------
+        // The tensor cores run one tile's products in the order of issue, so S may be written as soon as the
+        // product that read P (in S) has been issued.  The tiles take turns with the end of a product and the
+        // next scores: then one tile's products run while the other is in its softmax (left alone, the two
+        // ran in step and waited for each other's tensor work).  The waits of a turn are done before it, since
+        // one takes about as long as the tensor cores' queue lasts.
+        const int w = static_cast<int>(warp - kWarpMma);
         constexpr uint32_t kIdescS = attn_idesc<T, false>(kTile, kTile);
         constexpr uint32_t kIdescO = attn_idesc<T, true>(kTile, D);
         constexpr uint32_t kStep = kTileBytes >> 4;               // a tile, in descriptor units
-        const uint64_t q_desc = sw128_kmajor_desc(smem_u32(s.q[0]));
+        const uint64_t q_desc = sw128_kmajor_desc(smem_u32(s.q[w]));
         const uint64_t k_desc = sw128_kmajor_desc(smem_u32(s.k[0]));
         const uint64_t v_desc = sw128_token_rows_desc(smem_u32(s.v[0]), kBlockBytes);
-        int kt = 0, i[2] = {0, 0}, used[2] = {0, 0};              // key tiles, own key tiles, own query tiles
+        const uint32_t tS = tmem + kColS + w * 128u, tP = tmem + kColP + w * 128u, tO = tmem + kColO + w * 128u;
+        int kt = 0, i = 0, used = 0, turn = 0;                    // key tiles, own key tiles, own query tiles, turns
+        auto take_turn = [&] {
+            const bool mine = w == 0 ? turn == 0 || wait(s.turn[0], turn - 1, kWaitMma) : wait(s.turn[1], turn, kWaitMma);
+            ++turn;
+            return all(mine);
+        };
         for (int count = 0; ok; ++count) {
             ok = all(wait(s.item_full[count % kAhead], count / kAhead, kWaitMma));
             if (!ok) break;
             const Item& it = s.item[count % kAhead];
             const int h = __shfl_sync(0xFFFFFFFFu, it.h, 0);
             if (h < 0) break;
-            const int n[2] = {__shfl_sync(0xFFFFFFFFu, it.n[0], 0), __shfl_sync(0xFFFFFFFFu, it.n[1], 0)};
+            const int n = __shfl_sync(0xFFFFFFFFu, it.n[w], 0), other = __shfl_sync(0xFFFFFFFFu, it.n[1 - w], 0);
             const int len = __shfl_sync(0xFFFFFFFFu, it.end - it.begin, 0);
             const int redo = __shfl_sync(0xFFFFFFFFu, it.redo, 0);
             __syncwarp();
             if (lane == 0) mbar_arrive(&s.item_empty[count % kAhead]);
-            const int most = max(n[0], n[1]);
-            // S of query tile x and key tile t
-            auto scores = [&](int x, int t) {
-                if (t == 0 && !all(wait(s.q_full[x], used[x], kWaitMma))) return false;
-                tc_fence_after();
-                if (elect_one()) {
-                    const uint64_t q = q_desc + static_cast<uint32_t>(x) * kStep;
-                    const uint64_t k = k_desc + static_cast<uint32_t>((kt + t) % kSlots) * kStep;
-#pragma unroll
-                    for (int d = 0; d < D / 16; ++d) {
-                        const uint64_t off = (static_cast<uint32_t>(d / 4) * kBlockBytes + (d % 4) * 32) >> 4;
-                        mma_issue<false>(tmem + kColS + x * 128u, q + off, k + off, kIdescS, d != 0 ? 1u : 0u);
-                    }
-                    mma_commit(&s.s_full[x]);
-                    if (t + 1 == n[x]) mma_commit(&s.q_empty[x]);
-                }
-                __syncwarp();
-                return true;
-            };
-            // O += P V
-            auto product = [&](int x, int t) {
-                if (!all(wait(s.p_first[x], i[x], kWaitMma) &&
-                         (t > 0 || used[x] == 0 || wait(s.o_empty[x], used[x] - 1, kWaitMma))))
-                    return false;
-                tc_fence_after();
-                const uint64_t v = v_desc + static_cast<uint32_t>((kt + t) % kSlots) * kStep;
-                const uint32_t tP = tmem + kColP + x * 128u, tO = tmem + kColO + x * 128u;
-                const uint32_t onto = t == 0 && redo == 0 ? 0u : 1u;   // done again, O starts from what is there
-                // 16 tokens a product; of each half of the tile, the first 32 tokens' weights are ready first
-                if (elect_one()) {
-#pragma unroll
-                    for (int z = 0; z < 4; ++z) {
-                        const int y = z + (z & 2);
-                        mma_issue_ta(tO, tP + y * 8, v + y * 128, kIdescO, z == 0 ? onto : 1u);
-                    }
-                }
-                __syncwarp();
-                if (!all(wait(s.p_last[x], i[x], kWaitMma))) return false;
-                tc_fence_after();
-                if (elect_one()) {
-#pragma unroll
-                    for (int z = 0; z < 4; ++z) {
-                        const int y = 2 + z + (z & 2);
-                        mma_issue_ta(tO, tP + y * 8, v + y * 128, kIdescO, 1u);
-                    }
-                    mma_commit(&s.pv_done[x]);
-                }
-                __syncwarp();
-                ++i[x];
-                return true;
-            };
-            if (most > 0) ok = all(wait(s.k_full[kt % kSlots], kt / kSlots, kWaitMma));
-            for (int x = 0; ok && x < 2; ++x)
-                if (n[x] > 0) ok = scores(x, 0);
-            if (!ok) break;
-            if (most > 0 && elect_one()) mma_commit(&s.k_empty[kt % kSlots]);
-            __syncwarp();
-            for (int t = 0; t < most; ++t) {
-                const int slot = (kt + t) % kSlots;
-                ok = all(wait(s.v_full[slot], (kt + t) / kSlots, kWaitMma));
+            const int most = max(n, other);
+            if (most == 0) continue;
+            // turn t: the end of the product of key tile t - 1 and the scores of key tile t
+            for (int t = 0; t <= most; ++t) {
+                const uint64_t v = v_desc + static_cast<uint32_t>((kt + t - 1) % kSlots) * kStep;
+                const uint64_t k = k_desc + static_cast<uint32_t>((kt + t) % kSlots) * kStep;
+                // what is usually there comes first, the weights last
+                if (t < most) ok = all(wait(s.k_full[(kt + t) % kSlots], (kt + t) / kSlots, kWaitMma));
+                if (ok && t == 0 && n > 0) ok = all(wait(s.q_full[w], used, kWaitMma));
                 if (!ok) break;
-                const int held = len - t * kTile;
-                if (held < kTile) {                               // behind the sequence's end nothing may count
-                    const int pieces = (kTile - held) * 8;        // of 16 bytes, per block
-                    for (int y = 0; y < kHalves; ++y)
-                        for (int x = static_cast<int>(lane); x < pieces; x += 32)
-                            *reinterpret_cast<uint4*>(s.v[slot] + y * kBlockBytes + held * 128 + x * 16) =
-                                make_uint4(0u, 0u, 0u, 0u);
-                    fence_proxy_async_smem();
-                    __syncwarp();
-                }
+                if (t > 0) {
+                    const int slot = (kt + t - 1) % kSlots;
+                    ok = all(wait(s.v_full[slot], (kt + t - 1) / kSlots, kWaitMma));
+                    if (!ok) break;
+                    if (t <= n) {
+                        const int held = len - (t - 1) * kTile;
+                        if (held < kTile) {                       // behind the sequence's end nothing may count
+                            const int pieces = (kTile - held) * 8;    // of 16 bytes, per block
+                            for (int y = 0; y < kHalves; ++y)
+                                for (int x = static_cast<int>(lane); x < pieces; x += 32)
+                                    *reinterpret_cast<uint4*>(s.v[slot] + y * kBlockBytes + held * 128 + x * 16) =
+                                        make_uint4(0u, 0u, 0u, 0u);
+                            fence_proxy_async_smem();
+                            __syncwarp();
+                        }
+                        ok = all(wait(s.p_first[w], i, kWaitMma) && (t > 1 || used == 0 || wait(s.o_empty[w], used - 1, kWaitMma)));
+                        if (!ok) break;
+                        tc_fence_after();
+                        const uint32_t onto = t == 1 && redo == 0 ? 0u : 1u;   // done again, O starts from what is there
+                        // 16 tokens a product; of each half of the tile, the first 32 tokens' weights are ready first
+                        if (elect_one()) {
 #pragma unroll
-                for (int x = 0; x < 2; ++x) {
-                    if (ok && t < n[x]) ok = product(x, t);
-                    if (ok && t + 1 < n[x]) {
-                        ok = all(wait(s.k_full[(kt + t + 1) % kSlots], (kt + t + 1) / kSlots, kWaitMma));
-                        if (ok) ok = scores(x, t + 1);
+                            for (int z = 0; z < 4; ++z) {
+                                const int y = z + (z & 2);
+                                mma_issue_ta(tO, tP + y * 8, v + y * 128, kIdescO, z == 0 ? onto : 1u);
+                            }
+                        }
+                        __syncwarp();
                     }
                 }
+                ok = take_turn();
+                if (ok && t > 0 && t <= n) ok = all(wait(s.p_last[w], i++, kWaitMma));
                 if (!ok) break;
+                tc_fence_after();
                 if (elect_one()) {
-                    mma_commit(&s.v_empty[slot]);
-                    if (t + 1 < most) mma_commit(&s.k_empty[(kt + t + 1) % kSlots]);
+                    if (t > 0 && t <= n) {
+#pragma unroll
+                        for (int z = 0; z < 4; ++z) {
+                            const int y = 2 + z + (z & 2);
+                            mma_issue_ta(tO, tP + y * 8, v + y * 128, kIdescO, 1u);
+                        }
+                        mma_commit(&s.pv_done[w]);
+                    }
+                    if (t < n) {
+#pragma unroll
+                        for (int d = 0; d < D / 16; ++d) {
+                            const uint64_t off = (static_cast<uint32_t>(d / 4) * kBlockBytes + (d % 4) * 32) >> 4;
+                            mma_issue<false>(tS, q_desc + off, k + off, kIdescS, d != 0 ? 1u : 0u);
+                        }
+                        mma_commit(&s.s_full[w]);
+                    }
+                    mbar_arrive(&s.turn[1 - w]);
+                    if (t + 1 == n) mma_commit(&s.q_empty[w]);
+                    if (t > 0) mma_commit(&s.v_empty[(kt + t - 1) % kSlots]);
+                    if (t < most) mma_commit(&s.k_empty[(kt + t) % kSlots]);
                 }
                 __syncwarp();
             }
+            if (!ok) break;
             kt += most;
-#pragma unroll
-            for (int x = 0; x < 2; ++x) used[x] += n[x] > 0 ? 1 : 0;
+            used += n > 0 ? 1 : 0;
         }
         if (elect_one()) mma_commit(&s.drain);
         __syncwarp();
