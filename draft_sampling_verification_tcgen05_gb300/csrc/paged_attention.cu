@@ -339,7 +339,7 @@ paged_attention_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_con
     bool ok = true;
     auto all = [&](bool x) { return __all_sync(0xFFFFFFFFu, x); };
     auto wait = [&](uint64_t& bar, int use, uint32_t where) {            // use: how often it completed before
-        return mbar_wait(&bar, static_cast<uint32_t>(use) & 1u, ws, a.timeout_ns, where);
+        return mbar_wait_short(&bar, static_cast<uint32_t>(use) & 1u, ws, a.timeout_ns, where);
     };
     for (int pass = 0;; ++pass) {
         if (warp < 2) {
