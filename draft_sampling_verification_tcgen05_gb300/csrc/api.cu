@@ -203,8 +203,9 @@ size_t dspark_workspace_size(int op, int B, int N, int V, int r) {
         case DSPARK_OP_VERIFY_GUMBEL:
             return verify_gumbel_workspace_bytes(B, N);
         case DSPARK_OP_KV_APPEND:
-        case DSPARK_OP_SAMPLE:
             return sizeof(WsHeader);
+        case DSPARK_OP_SAMPLE:
+            return sample_workspace_bytes(B);
         case DSPARK_OP_PROMPT_ATTENTION:
             return prompt_attention_workspace_bytes(B, N, V);
         case DSPARK_OP_PAGED_ATTENTION:
@@ -545,7 +546,7 @@ dspark_status dspark_sample(const void* logits, dspark_dtype dtype, const float*
     DSPARK_REQUIRE(dtype == DSPARK_F32 || dtype == DSPARK_BF16, "sample: dtype must be fp32 or bf16 (%d)", (int)dtype);
     DSPARK_REQUIRE(R >= 1 && V >= 1 && V <= (1 << 21), "sample: bad sizes (R=%d V=%d)", R, V);
     DSPARK_REQUIRE(aligned(logits, 16) && aligned(probs, 16), "sample: logits and probs must be 16-byte aligned");
-    if (bad_ws(workspace, ws_bytes, sizeof(WsHeader))) return DSPARK_ERR_INVALID_ARG;
+    if (bad_ws(workspace, ws_bytes, sample_workspace_bytes(R))) return DSPARK_ERR_INVALID_ARG;
     DeviceInfo dev;
     if (!current_device(&dev)) return DSPARK_ERR_UNSUPPORTED;
     return launch_sample(logits, dtype, temperature, top_k, top_p, min_p, u, R, V, tokens, probs, workspace,

@@ -106,6 +106,7 @@ dspark_status launch_prompt_attention(const void* q, const void* k, const void* 
                                       int Hkv, int D, void* out, float* lse, void* ws, cudaStream_t stream,
                                       const DeviceInfo& dev);
 
+size_t sample_workspace_bytes(int R);
 dspark_status launch_sample(const void* logits, dspark_dtype dtype, const float* temperature, const int32_t* top_k,
                             const float* top_p, const float* min_p, const float* u, int R, int V, int32_t* tokens,
                             float* probs, void* ws, cudaStream_t stream, const DeviceInfo& dev);

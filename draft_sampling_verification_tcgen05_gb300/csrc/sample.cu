@@ -5,7 +5,8 @@
 // floor(w * 2^40)), so the cut, the total and the token depend on no order of summation.
 //
 // With as many rows as SMs a row is a block's, which passes over it in memory (the rows under way
-// fit the L2 cache, so later passes find them there); with fewer rows a cluster of 2 to 16 blocks
+// fit the L2 cache, so later passes find them there), and the blocks take row after row from a queue,
+// the longest first; with fewer rows a cluster of 2 to 16 blocks
 // shares a row, each with a copy of its part in shared memory.  Sums, counts and lists then travel as
 // asynchronous stores into the receiving block's shared memory that complete on an mbarrier there (a
 // cluster's barrier waits for all earlier stores: 2000 cycles and more each time, an exchange takes a
@@ -26,6 +27,7 @@
 //      drawn mass again.  Probabilities: zeros and the list's entries, or a pass over the row
 // A row that needs 3 and 4 is bound by its instructions (an exponential and an exact mass per entry and
 // pass), the others by memory.
+#include "attention_common.cuh"
 #include "device_common.cuh"
 #include "half_common.cuh"
 #include "host_common.h"
@@ -47,6 +49,12 @@ constexpr int kFew = 256;                  // entries that are settled by compar
 constexpr int kBatch = 4;                  // 16-byte pieces that a thread has under way
 constexpr uint32_t kWaitPeer = 0xA01;
 
+struct Plan {
+    WsHeader header;
+    unsigned int next;                     // of the queue
+    int pad[63];
+};
+
 struct SampleArgs {
     const void* logits;
     const float* temperature;
@@ -55,10 +63,12 @@ struct SampleArgs {
     int R, V;
     int cluster, slice;                    // blocks of a row, entries of a block
     int resident;                          // a block's part is held in shared memory
-    int heavy_first;                       // blocks choose their rows by what they take
+    int queue;                             // blocks take row after row
     int32_t* tokens;
     float* probs;
     WsHeader* ws;
+    Plan* plan;
+    int32_t* order;                        // with a queue: the rows as they are taken
 };
 
 using u64 = unsigned long long;
@@ -150,51 +160,43 @@ struct alignas(16) Shared {
     u64 out[4];                            // what the first block tells the others
     u64 run[kWarps];                       // mass of the list's entries in each run of this block
     u64 found;                             // the entry that locate() was asked for
-    uint32_t list_count, pad;
+    uint32_t list_count, next;
     u64 bar_red[2], bar_out, bar_hist, bar_list, bar_segment, bar_found, bar_share, bar_bins;
 };
 
 struct Reduced { u64 a, b, c, d; };
 
+// ---------------------------------------------------------------------------
+// Plan: one block.  Clears the status word and the queue and, where the blocks take their rows from a
+// queue, orders the rows by what they take, the longest first.
+// ---------------------------------------------------------------------------
+__global__ void __launch_bounds__(kThreads) sample_plan_kernel(const __grid_constant__ SampleArgs p) {
+    constexpr int kKinds = 5;
+    __shared__ int s_at[kKinds];
+    const int tid = threadIdx.x;
+    grid_dependency_launch();                                                 // the other kernel's blocks get ready
+    if (tid < static_cast<int>(sizeof(Plan) / 4)) reinterpret_cast<uint32_t*>(p.plan)[tid] = 0u;
+    if (!p.queue) return;
+    auto kind = [&](int r) {                                // closed in on; all summed; on a long list; a short one; greedy
+        const int k = p.top_k[r];
+        if (!(p.temperature[r] > 0.0f) || k == 1) return 4;
+        if (k > 0 && k <= kList / 2) return k > kFew ? 2 : 3;
+        return p.top_p[r] < 1.0f ? 0 : 1;
+    };
+    if (tid < kKinds) s_at[tid] = 0;
+    __syncthreads();
+    for (int r = tid; r < p.R; r += kThreads)
+        for (int x = kind(r) + 1; x < kKinds; ++x) atomicAdd(&s_at[x], 1);    // rows ahead of the later kinds
+    __syncthreads();
+    for (int r = tid; r < p.R; r += kThreads) p.order[atomicAdd(&s_at[kind(r)], 1)] = r;
+}
+
 template <typename T>
-__global__ void __launch_bounds__(kThreads, 1) sample_kernel(const __grid_constant__ SampleArgs p) {
-    extern __shared__ __align__(16) uint8_t smem_raw[];
-    Shared& s = *reinterpret_cast<Shared*>(smem_raw);
-    T* const held = reinterpret_cast<T*>(smem_raw + sizeof(Shared));
+__device__ __forceinline__ void sample_row(const SampleArgs& p, Shared& s, T* const held, const long long r) {
     const int tid = threadIdx.x, V = p.V;
     const uint32_t warp = warp_id(), lane = lane_id();
     const int C = p.cluster;
     const uint32_t rank = C > 1 ? cluster_rank() : 0u;
-    // Rows that take the most passes first (with a block per row, more rows than SMs): without top-k, with
-    // top-p.  Every block finds its own row in that order.
-    long long r = blockIdx.x / C;
-    if (p.heavy_first) {
-        auto heavy = [&](int i) {
-            const int k = p.top_k[i];
-            return p.temperature[i] > 0.0f && (k <= 0 || k > kList / 2) && p.top_p[i] < 1.0f;
-        };
-        const int place = static_cast<int>(blockIdx.x);
-        int all = 0, seen = 0;
-        for (int i0 = 0; i0 < p.R; i0 += kThreads) all += __syncthreads_count(i0 + tid < p.R && heavy(i0 + tid));
-        const bool first = place < all;
-        const int want = first ? place : place - all;
-        for (int i0 = 0; i0 < p.R; i0 += kThreads) {
-            const bool mine = i0 + tid < p.R && heavy(i0 + tid) == first;
-            const int here = __syncthreads_count(mine);
-            if (want < seen + here) {
-                const uint32_t vote = __ballot_sync(0xFFFFFFFFu, mine);
-                if (lane == 0) s.run[warp] = __popc(vote);
-                __syncthreads();
-                int before = seen + __popc(vote & ((1u << lane) - 1u));
-                for (uint32_t w = 0; w < warp; ++w) before += static_cast<int>(s.run[w]);
-                if (mine && before == want) s.found = static_cast<u64>(i0 + tid);
-                __syncthreads();
-                break;
-            }
-            seen += here;
-        }
-        r = static_cast<long long>(s.found);
-    }
     const T* const global = static_cast<const T*>(p.logits) + r * V;
     const int v0 = min(V, static_cast<int>(rank) * p.slice), v1 = min(V, v0 + p.slice), n = v1 - v0;
 
@@ -1110,6 +1112,7 @@ __global__ void __launch_bounds__(kThreads, 1) sample_kernel(const __grid_consta
     }
 
     // ---- 5. the token, and the probabilities ----
+    if (p.queue && tid == 0) s.next = gridDim.x + atomicAdd(&p.plan->next, 1u);   // the next row: no earlier, for the order
     const float cut_logit = cut == 0 ? -INFINITY : key_logit(cut);
     auto kept = [&](float l, int v) {                                         // weight of a kept entry, else 0
         if (!(l >= cut_logit) || bits(l) == 0 || key_of(l, v) < cut) return 0.0f;
@@ -1166,6 +1169,23 @@ __global__ void __launch_bounds__(kThreads, 1) sample_kernel(const __grid_consta
     }
 }
 
+template <typename T>
+__global__ void __launch_bounds__(kThreads, 1) sample_kernel(const __grid_constant__ SampleArgs p) {
+    extern __shared__ __align__(16) uint8_t smem_raw[];
+    Shared& s = *reinterpret_cast<Shared*>(smem_raw);
+    T* const held = reinterpret_cast<T*>(smem_raw + sizeof(Shared));
+    grid_dependency_wait();
+    int place = static_cast<int>(blockIdx.x) / p.cluster;
+    while (true) {
+        sample_row(p, s, held, p.queue ? p.order[place] : place);
+        if (!p.queue) break;
+        __syncthreads();
+        place = static_cast<int>(s.next);
+        __syncthreads();
+        if (place >= p.R) break;
+    }
+}
+
 // ---------------------------------------------------------------------------
 // Host side.
 // ---------------------------------------------------------------------------
@@ -1177,7 +1197,7 @@ cudaError_t launch_typed(SampleArgs p, cudaStream_t stream, const DeviceInfo& de
     int c = 1;
     while (c < kMaxCluster && static_cast<long long>(p.R) * c < dev.sm_count && slice_of(2 * c) >= kMinSlice) c *= 2;
     p.cluster = c;
-    p.heavy_first = c == 1 && p.R > dev.sm_count ? 1 : 0;
+    p.queue = c == 1 && p.R > dev.sm_count ? 1 : 0;
     p.slice = slice_of(c);
     p.resident = sizeof(Shared) + static_cast<size_t>(p.slice) * sizeof(T) + 32 <= dev.smem_optin ? 1 : 0;
     const size_t smem = sizeof(Shared) + (p.resident ? static_cast<size_t>(p.slice) * sizeof(T) + 32 : 0);
@@ -1185,21 +1205,27 @@ cudaError_t launch_typed(SampleArgs p, cudaStream_t stream, const DeviceInfo& de
     if (e == cudaSuccess) e = cudaFuncSetAttribute(sample_kernel<T>, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
     if (e != cudaSuccess) return e;
     cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3(static_cast<unsigned>(p.R) * static_cast<unsigned>(c));
+    cfg.gridDim = dim3(p.queue ? static_cast<unsigned>(dev.sm_count) : static_cast<unsigned>(p.R) * static_cast<unsigned>(c));
     cfg.blockDim = dim3(kThreads);
     cfg.dynamicSmemBytes = smem;
     cfg.stream = stream;
-    cudaLaunchAttribute at[1];
+    cudaLaunchAttribute at[2];
     at[0].id = cudaLaunchAttributeClusterDimension;
     at[0].val.clusterDim.x = static_cast<unsigned>(c);
     at[0].val.clusterDim.y = 1;
     at[0].val.clusterDim.z = 1;
+    at[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    at[1].val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = at;
-    cfg.numAttrs = 1;
-    return cudaLaunchKernelEx(&cfg, sample_kernel<T>, p);
+    cfg.numAttrs = 2;
+    sample_plan_kernel<<<1, kThreads, 0, stream>>>(p);
+    e = cudaGetLastError();
+    return e != cudaSuccess ? e : cudaLaunchKernelEx(&cfg, sample_kernel<T>, p);
 }
 
 }  // namespace
+
+size_t sample_workspace_bytes(int R) { return R < 1 ? 0 : sizeof(Plan) + static_cast<size_t>(R) * sizeof(int32_t); }
 
 dspark_status launch_sample(const void* logits, dspark_dtype dtype, const float* temperature, const int32_t* top_k,
                             const float* top_p, const float* min_p, const float* u, int R, int V, int32_t* tokens,
@@ -1208,9 +1234,8 @@ dspark_status launch_sample(const void* logits, dspark_dtype dtype, const float*
         set_error("sample: too many rows (R=%d)", R);
         return DSPARK_ERR_UNSUPPORTED;
     }
-    dspark_status st = clear_workspace(ws, sizeof(WsHeader), stream);
-    if (st != DSPARK_OK) return st;
-    SampleArgs p{logits, temperature, top_k, top_p, min_p, u, R, V, 1, 0, 0, 0, tokens, probs, static_cast<WsHeader*>(ws)};
+    SampleArgs p{logits, temperature, top_k, top_p, min_p, u, R, V, 1, 0, 0, 0, tokens, probs, static_cast<WsHeader*>(ws),
+                 static_cast<Plan*>(ws), reinterpret_cast<int32_t*>(static_cast<uint8_t*>(ws) + sizeof(Plan))};
     const cudaError_t e = dtype == DSPARK_F32 ? launch_typed<float>(p, stream, dev)
                                               : launch_typed<__nv_bfloat16>(p, stream, dev);
     if (e != cudaSuccess) return cuda_error(e, "launch(sample)");

@@ -118,7 +118,7 @@ typedef enum {
  *   DSPARK_OP_PAGED_ATTENTION  partial results of split requests and their counters;
  *                           B, N as the call's, V = Hq, r = D
  *   DSPARK_OP_PROMPT_ATTENTION  the list of its work items; B as the call's, N = T, V = Hq
- *   DSPARK_OP_SAMPLE        256 (the status word)
+ *   DSPARK_OP_SAMPLE        grows with B (the rows' order); B = R, N = 1
  * Returns 0 for an unknown op or negative sizes.
  */
 DSPARK_API size_t dspark_workspace_size(int op, int B, int N, int V, int r);

@@ -24,8 +24,9 @@ def _refused(fn, good, changes):
 
 
 def test_workspace_sizes(L):
-    for op in (8, 12):
-        assert L.dspark_workspace_size(op, 4, 4, 1000, 64) == 256
+    assert L.dspark_workspace_size(8, 4, 4, 1000, 64) == 256
+    assert L.dspark_workspace_size(12, 4, 1, 1000, 0) >= 256 + 4 * 4
+    assert L.dspark_workspace_size(12, 0, 1, 1000, 0) == 0
     assert L.dspark_workspace_size(11, 4, 1000, 16, 0) >= 256 + 16 * (4 + 1000 // 64)
     assert L.dspark_workspace_size(11, 4, 0, 16, 0) == 0
     assert L.dspark_workspace_size(10, 4, 4, 32, 128) >= 256
@@ -59,7 +60,8 @@ def test_prompt_attention(L):
 
 
 def test_sample(L):
-    good = [FAKE, 0, FAKE, FAKE, FAKE, FAKE, FAKE, 4, 1000, FAKE, NULL, FAKE, 256, NULL]
+    need = L.dspark_workspace_size(12, 4, 1, 1000, 0)
+    good = [FAKE, 0, FAKE, FAKE, FAKE, FAKE, FAKE, 4, 1000, FAKE, NULL, FAKE, need, NULL]
     _refused(L.dspark_sample, good, [
         (0, NULL), (0, ODD), (1, 2), (2, NULL), (3, NULL), (4, NULL), (5, NULL), (6, NULL), (7, 0), (8, 0),
         (8, (1 << 21) + 1), (9, NULL), (10, ODD), (11, NULL), (12, 128)])
