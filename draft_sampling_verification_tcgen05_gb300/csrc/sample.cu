@@ -37,14 +37,18 @@
 namespace dspark {
 namespace {
 
-constexpr int kThreads = 1024;
-constexpr int kWarps = kThreads / 32;
 constexpr int kMaxCluster = 16;
+constexpr int kPlanThreads = 1024;
 constexpr int kList = 2048;                // entries of the list
 constexpr int kBins = 2048;
-constexpr int kPerThread = kBins / kThreads;
-constexpr int kParts = kThreads;           // of the list's range, a thread each
-constexpr int kHist = 3 * kParts > kBins ? 3 * kParts : kBins;
+// What depends on the threads of a block.
+template <int kThreads>
+struct Block {
+    static constexpr int kWarps = kThreads / 32;
+    static constexpr int kPerThread = kBins / kThreads;
+    static constexpr int kParts = kThreads;                       // of the list's range, a thread each
+    static constexpr int kHist = 3 * kParts > kBins ? 3 * kParts : kBins;
+};
 constexpr int kFew = 256;                  // entries that are settled by comparing each with all
 constexpr int kBatch = 4;                  // 16-byte pieces that a thread has under way
 constexpr uint32_t kWaitPeer = 0xA01;
@@ -145,7 +149,9 @@ __device__ __forceinline__ int floor_of(float y) {
     return static_cast<int>(__float_as_uint(__fadd_rz(y, 0x1p23f)) - kHalfBias);
 }
 
+template <int kThreads>
 struct alignas(16) Shared {
+    static constexpr int kWarps = Block<kThreads>::kWarps, kHist = Block<kThreads>::kHist;
     u64 red[2][kMaxCluster][4];            // values exchanged by the blocks, two exchanges in turn
     union {
         u64 list[kList];                   // argmax keys: of this block, then in the first block of all
@@ -170,7 +176,7 @@ struct Reduced { u64 a, b, c, d; };
 // Plan: one block.  Clears the status word and the queue and, where the blocks take their rows from a
 // queue, orders the rows by what they take, the longest first.
 // ---------------------------------------------------------------------------
-__global__ void __launch_bounds__(kThreads) sample_plan_kernel(const __grid_constant__ SampleArgs p) {
+__global__ void __launch_bounds__(kPlanThreads) sample_plan_kernel(const __grid_constant__ SampleArgs p) {
     constexpr int kKinds = 5;
     __shared__ int s_at[kKinds];
     const int tid = threadIdx.x;
@@ -185,14 +191,15 @@ __global__ void __launch_bounds__(kThreads) sample_plan_kernel(const __grid_cons
     };
     if (tid < kKinds) s_at[tid] = 0;
     __syncthreads();
-    for (int r = tid; r < p.R; r += kThreads)
+    for (int r = tid; r < p.R; r += kPlanThreads)
         for (int x = kind(r) + 1; x < kKinds; ++x) atomicAdd(&s_at[x], 1);    // rows ahead of the later kinds
     __syncthreads();
-    for (int r = tid; r < p.R; r += kThreads) p.order[atomicAdd(&s_at[kind(r)], 1)] = r;
+    for (int r = tid; r < p.R; r += kPlanThreads) p.order[atomicAdd(&s_at[kind(r)], 1)] = r;
 }
 
-template <typename T>
-__device__ __forceinline__ void sample_row(const SampleArgs& p, Shared& s, T* const held, const long long r) {
+template <typename T, int kThreads>
+__device__ __forceinline__ void sample_row(const SampleArgs& p, Shared<kThreads>& s, T* const held, const long long r) {
+    constexpr int kWarps = Block<kThreads>::kWarps, kPerThread = Block<kThreads>::kPerThread, kParts = Block<kThreads>::kParts;
     const int tid = threadIdx.x, V = p.V;
     const uint32_t warp = warp_id(), lane = lane_id();
     const int C = p.cluster;
@@ -1169,11 +1176,11 @@ __device__ __forceinline__ void sample_row(const SampleArgs& p, Shared& s, T* co
     }
 }
 
-template <typename T>
+template <typename T, int kThreads>
 __global__ void __launch_bounds__(kThreads, 1) sample_kernel(const __grid_constant__ SampleArgs p) {
     extern __shared__ __align__(16) uint8_t smem_raw[];
-    Shared& s = *reinterpret_cast<Shared*>(smem_raw);
-    T* const held = reinterpret_cast<T*>(smem_raw + sizeof(Shared));
+    Shared<kThreads>& s = *reinterpret_cast<Shared<kThreads>*>(smem_raw);
+    T* const held = reinterpret_cast<T*>(smem_raw + sizeof(s));
     grid_dependency_wait();
     int place = static_cast<int>(blockIdx.x) / p.cluster;
     while (true) {
@@ -1189,6 +1196,34 @@ __global__ void __launch_bounds__(kThreads, 1) sample_kernel(const __grid_consta
 // ---------------------------------------------------------------------------
 // Host side.
 // ---------------------------------------------------------------------------
+template <typename T, int kThreads>
+cudaError_t launch_blocks(SampleArgs p, cudaStream_t stream, const DeviceInfo& dev) {
+    using S = Shared<kThreads>;
+    p.resident = sizeof(S) + static_cast<size_t>(p.slice) * sizeof(T) + 32 <= dev.smem_optin ? 1 : 0;
+    const size_t smem = sizeof(S) + (p.resident ? static_cast<size_t>(p.slice) * sizeof(T) + 32 : 0);
+    auto kernel = sample_kernel<T, kThreads>;
+    cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem));
+    if (e == cudaSuccess) e = cudaFuncSetAttribute(kernel, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
+    if (e != cudaSuccess) return e;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(p.queue ? static_cast<unsigned>(dev.sm_count) : static_cast<unsigned>(p.R) * static_cast<unsigned>(p.cluster));
+    cfg.blockDim = dim3(kThreads);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = stream;
+    cudaLaunchAttribute at[2];
+    at[0].id = cudaLaunchAttributeClusterDimension;
+    at[0].val.clusterDim.x = static_cast<unsigned>(p.cluster);
+    at[0].val.clusterDim.y = 1;
+    at[0].val.clusterDim.z = 1;
+    at[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    at[1].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = at;
+    cfg.numAttrs = 2;
+    sample_plan_kernel<<<1, kPlanThreads, 0, stream>>>(p);
+    e = cudaGetLastError();
+    return e != cudaSuccess ? e : cudaLaunchKernelEx(&cfg, kernel, p);
+}
+
 template <typename T>
 cudaError_t launch_typed(SampleArgs p, cudaStream_t stream, const DeviceInfo& dev) {
     // Blocks per row: as many as give every SM one, while a block keeps kMinSlice entries.
@@ -1199,28 +1234,9 @@ cudaError_t launch_typed(SampleArgs p, cudaStream_t stream, const DeviceInfo& de
     p.cluster = c;
     p.queue = c == 1 && p.R > dev.sm_count ? 1 : 0;
     p.slice = slice_of(c);
-    p.resident = sizeof(Shared) + static_cast<size_t>(p.slice) * sizeof(T) + 32 <= dev.smem_optin ? 1 : 0;
-    const size_t smem = sizeof(Shared) + (p.resident ? static_cast<size_t>(p.slice) * sizeof(T) + 32 : 0);
-    cudaError_t e = cudaFuncSetAttribute(sample_kernel<T>, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem));
-    if (e == cudaSuccess) e = cudaFuncSetAttribute(sample_kernel<T>, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
-    if (e != cudaSuccess) return e;
-    cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3(p.queue ? static_cast<unsigned>(dev.sm_count) : static_cast<unsigned>(p.R) * static_cast<unsigned>(c));
-    cfg.blockDim = dim3(kThreads);
-    cfg.dynamicSmemBytes = smem;
-    cfg.stream = stream;
-    cudaLaunchAttribute at[2];
-    at[0].id = cudaLaunchAttributeClusterDimension;
-    at[0].val.clusterDim.x = static_cast<unsigned>(c);
-    at[0].val.clusterDim.y = 1;
-    at[0].val.clusterDim.z = 1;
-    at[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    at[1].val.programmaticStreamSerializationAllowed = 1;
-    cfg.attrs = at;
-    cfg.numAttrs = 2;
-    sample_plan_kernel<<<1, kThreads, 0, stream>>>(p);
-    e = cudaGetLastError();
-    return e != cudaSuccess ? e : cudaLaunchKernelEx(&cfg, sample_kernel<T>, p);
+    // Half the threads meet sooner at their barriers; with long parts the passes count, which want them all.
+    constexpr int kShortSlice = 32768;
+    return p.slice <= kShortSlice ? launch_blocks<T, 512>(p, stream, dev) : launch_blocks<T, 1024>(p, stream, dev);
 }
 
 }  // namespace
