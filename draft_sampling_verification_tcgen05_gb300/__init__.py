@@ -124,6 +124,12 @@ def _dt(t):
 
 
 def _need(t, name, dtypes, ndim=None):
+    # the usual case in few steps (a call of the small operators takes about as long as its checks)
+    try:
+        if t.is_cuda and t.dtype in dtypes and t.is_contiguous() and (ndim is None or t.ndim == ndim):
+            return
+    except AttributeError:
+        pass
     if not isinstance(t, _torch().Tensor) or not t.is_cuda:
         raise TypeError(f"{name} must be a CUDA tensor")
     if not t.is_contiguous():
@@ -148,10 +154,11 @@ class Workspace:
                                device=device if device is not None else "cuda")
         off = (-self.buf.data_ptr()) % 256
         self.view = self.buf[off:off + self.nbytes]
+        self.address = self.view.data_ptr()
 
     @property
     def ptr(self):
-        return ctypes.c_void_p(self.view.data_ptr())
+        return ctypes.c_void_p(self.address)
 
 
 def _ws(ws, op, B=0, N=0, V=0, r=0, device=None):
@@ -444,6 +451,12 @@ def _half(t, name):
 
 def _rows(t, name, dtype, D):
     """Checks a [T, H, D] tensor whose heads and values are contiguous; returns its token stride in elements."""
+    try:
+        (T, H, d), (token, head, value) = t.shape, t.stride()
+        if t.is_cuda and t.dtype == dtype and d == D and value == 1 and head == D:
+            return token if T > 1 else H * D
+    except (AttributeError, TypeError, ValueError):
+        pass
     torch = _torch()
     if not isinstance(t, torch.Tensor) or not t.is_cuda:
         raise TypeError(f"{name} must be a CUDA tensor")
@@ -479,8 +492,8 @@ def dspark_kv_append(q, k, v, positions, slots, cos_sin, k_cache, v_cache, inter
     _need(slots, "slots", (torch.int32,), 1)
     _need(cos_sin, "cos_sin", (torch.float32,), 2)
     num_pages, Hc, page, Dc = k_cache.shape
-    if tuple(v.shape) != (T, Hkv, D) or (Hc, Dc) != (Hkv, D) or v_cache.shape != k_cache.shape \
-            or positions.shape[0] != T or slots.shape[0] != T:
+    if v.shape != k.shape or Hc != Hkv or Dc != D or v_cache.shape != k_cache.shape \
+            or len(positions) != T or len(slots) != T:
         raise ValueError("shapes: k / v [T, Hkv, D], caches [num_pages, Hkv, page_size, D], positions / slots [T]")
     for w, name in ((q_norm, "q_norm"), (k_norm, "k_norm")):
         if w is not None:
@@ -495,14 +508,15 @@ def dspark_kv_append(q, k, v, positions, slots, cos_sin, k_cache, v_cache, inter
             raise ValueError("q must be [T, Hq, D] with the tokens of k")
         if q_out is None:
             q_out = torch.empty(T, Hq, D, dtype=k.dtype, device=k.device)
-        _need(q_out, "q_out", (k.dtype,), 3)
-        if tuple(q_out.shape) != (T, Hq, D):
-            raise ValueError("q_out must be [T, Hq, D]")
-    ws = _ws(workspace, OP_KV_APPEND, device=k.device)
+        else:
+            _need(q_out, "q_out", (k.dtype,), 3)
+            if q_out.shape != q.shape:
+                raise ValueError("q_out must be [T, Hq, D]")
+    ws = workspace if workspace is not None else Workspace(OP_KV_APPEND, device=k.device)
     _check(lib().dspark_kv_append(_ptr(q), _ptr(k), _ptr(v), dt, q_stride, k_stride, v_stride, _ptr(positions),
                                   _ptr(slots), _ptr(cos_sin), cos_sin.shape[0], cos_sin.shape[1], int(interleaved),
                                   _ptr(q_norm), _ptr(k_norm), eps, T, Hq, Hkv, D, _ptr(q_out), _ptr(k_cache),
-                                  _ptr(v_cache), num_pages, page, ws.ptr, ws.nbytes, _stream(stream)),
+                                  _ptr(v_cache), num_pages, page, ws.address, ws.nbytes, _stream(stream)),
            "dspark_kv_append")
     return q_out
 
@@ -534,15 +548,16 @@ def dspark_paged_attention(q, k_cache, v_cache, block_table, kv_len, scale: floa
             raise ValueError("lengths must be [B]")
     if out is None:
         out = torch.empty_like(q)
-    _need(out, "out", (q.dtype,), 4)
+    else:
+        _need(out, "out", (q.dtype,), 4)
     if lse is not None:
         _need(lse, "lse", (torch.float32,), 3)
-    if out.shape != q.shape or (lse is not None and lse.shape != q.shape[:3]):
+    if out.shape != q.shape or (lse is not None and lse.shape != (B, N, Hq)):
         raise ValueError("out must be [B, N, Hq, D] and lse [B, N, Hq]")
-    ws = _ws(workspace, OP_PAGED_ATTENTION, B, N, Hq, D, q.device)
+    ws = workspace if workspace is not None else Workspace(OP_PAGED_ATTENTION, B, N, Hq, D, q.device)
     _check(lib().dspark_paged_attention(_ptr(q), _ptr(k_cache), _ptr(v_cache), dt, _ptr(block_table),
                                         block_table.shape[1], _ptr(kv_len), _ptr(lengths), scale, int(causal), B, N,
-                                        Hq, Hkv, D, num_pages, page, _ptr(out), _ptr(lse), ws.ptr, ws.nbytes,
+                                        Hq, Hkv, D, num_pages, page, _ptr(out), _ptr(lse), ws.address, ws.nbytes,
                                         _stream(stream)), "dspark_paged_attention")
     return out
 
@@ -565,15 +580,16 @@ def dspark_prompt_attention(q, k, v, cu_seqlens, scale: float, causal: bool = Tr
         raise ValueError("shapes: q [T, Hq, D], k / v [T, Hkv, D]")
     if out is None:
         out = torch.empty(T, Hq, D, dtype=q.dtype, device=q.device)
-    _need(out, "out", (q.dtype,), 3)
+    else:
+        _need(out, "out", (q.dtype,), 3)
     if lse is not None:
         _need(lse, "lse", (torch.float32,), 2)
-    if out.shape != q.shape or (lse is not None and lse.shape != q.shape[:2]):
+    if out.shape != q.shape or (lse is not None and lse.shape != (T, Hq)):
         raise ValueError("out must be [T, Hq, D] and lse [T, Hq]")
     B = cu_seqlens.shape[0] - 1
-    ws = _ws(workspace, OP_PROMPT_ATTENTION, B, T, Hq, D, q.device)
+    ws = workspace if workspace is not None else Workspace(OP_PROMPT_ATTENTION, B, T, Hq, D, q.device)
     _check(lib().dspark_prompt_attention(_ptr(q), _ptr(k), _ptr(v), dt, q_stride, k_stride, v_stride, _ptr(cu_seqlens),
-                                         scale, int(causal), B, T, Hq, k.shape[1], D, _ptr(out), _ptr(lse), ws.ptr,
+                                         scale, int(causal), B, T, Hq, k.shape[1], D, _ptr(out), _ptr(lse), ws.address,
                                          ws.nbytes, _stream(stream)), "dspark_prompt_attention")
     return out
 
@@ -587,21 +603,23 @@ def dspark_sample(logits, temperature, top_k, top_p, min_p, u, tokens=None, prob
     torch = _torch()
     _need(logits, "logits", (torch.float32, torch.bfloat16), 2)
     R, V = logits.shape
+    f32 = (torch.float32,)
     for t, name in ((temperature, "temperature"), (top_p, "top_p"), (min_p, "min_p"), (u, "u")):
-        _need(t, name, (torch.float32,), 1)
-        if t.shape[0] != R:
+        _need(t, name, f32, 1)
+        if len(t) != R:
             raise ValueError(f"{name} must be [R]")
     _need(top_k, "top_k", (torch.int32,), 1)
     if tokens is None:
         tokens = torch.empty(R, dtype=torch.int32, device=logits.device)
-    _need(tokens, "tokens", (torch.int32,), 1)
+    else:
+        _need(tokens, "tokens", (torch.int32,), 1)
     if probs is not None:
         _need(probs, "probs", (torch.float32,), 2)
-    if top_k.shape[0] != R or tokens.shape[0] != R or (probs is not None and probs.shape != logits.shape):
+    if len(top_k) != R or len(tokens) != R or (probs is not None and probs.shape != logits.shape):
         raise ValueError("shapes: top_k / tokens [R], probs [R, V]")
-    ws = _ws(workspace, OP_SAMPLE, R, 1, V, 0, logits.device)
+    ws = workspace if workspace is not None else Workspace(OP_SAMPLE, R, 1, V, 0, logits.device)
     _check(lib().dspark_sample(_ptr(logits), _dt(logits), _ptr(temperature), _ptr(top_k), _ptr(top_p), _ptr(min_p),
-                               _ptr(u), R, V, _ptr(tokens), _ptr(probs), ws.ptr, ws.nbytes, _stream(stream)),
+                               _ptr(u), R, V, _ptr(tokens), _ptr(probs), ws.address, ws.nbytes, _stream(stream)),
            "dspark_sample")
     return tokens
 

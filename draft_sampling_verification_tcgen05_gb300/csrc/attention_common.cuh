@@ -168,17 +168,6 @@ __device__ __forceinline__ bool mbar_wait_short(uint64_t* bar, uint32_t parity, 
     return mbar_try_wait(bar, parity) || mbar_wait_longer(bar, parity, ws, timeout_ns, where);
 }
 
-// Whether the phase of the given parity is complete, without waiting.
-__device__ __forceinline__ bool mbar_test(uint64_t* bar, uint32_t parity) {
-    uint32_t ok;
-    asm volatile(
-        "{\n\t.reg .pred p;\n\t"
-        "mbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
-        "selp.u32 %0, 1, 0, p;\n\t}"
-        : "=r"(ok) : "r"(smem_u32(bar)), "r"(parity) : "memory");
-    return ok != 0;
-}
-
 // Named barrier that also tells whether `ok` holds in all its threads.
 __device__ __forceinline__ bool named_bar_and(uint32_t id, uint32_t nthreads, bool ok) {
     uint32_t r;
@@ -190,12 +179,6 @@ __device__ __forceinline__ bool named_bar_and(uint32_t id, uint32_t nthreads, bo
         : "=r"(r) : "r"(id), "r"(nthreads), "r"(static_cast<uint32_t>(ok)) : "memory");
     return r != 0;
 }
-
-// Register shares of a warpgroup (four warps, all of which execute this).
-template <int N>
-__device__ __forceinline__ void registers_give_up() { asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" :: "n"(N)); }
-template <int N>
-__device__ __forceinline__ void registers_take() { asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" :: "n"(N)); }
 
 // Quotients of non-negative values: the 32-bit division where it can serve (the 64-bit one is a long
 // dependent chain, and every role starts its work with one).

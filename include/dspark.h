@@ -645,7 +645,7 @@ DSPARK_API dspark_status dspark_prompt_attention(const void* q, const void* k, c
  * set NUMERIC; a row without a finite entry gives token 0, probs 0 and NUMERIC.  A negative or
  * non-finite temperature sets NUMERIC and is read as 0.  A top_p, min_p or u out of its range sets
  * INPUT_RANGE and is read as the nearest value in it (NaN: 1, 0 and 0).
- * workspace: >= dspark_workspace_size(DSPARK_OP_SAMPLE, ...) bytes.
+ * workspace: >= dspark_workspace_size(DSPARK_OP_SAMPLE, R, 1, V, 0).
  */
 DSPARK_API dspark_status dspark_sample(const void* logits, dspark_dtype dtype, const float* temperature,
                                const int32_t* top_k, const float* top_p, const float* min_p,
