@@ -13,9 +13,17 @@
  *   dspark_schedule       confidence-scheduled admission (survival chain,
  *                         global sort, throughput-optimal K, fill)
  *
+ * and, for the serving loop around them, each one or more launches:
+ *
+ *   dspark_kv_append         norm, rotation and paged-cache writes of new tokens
+ *   dspark_paged_attention   a window of new tokens per request over the cache
+ *   dspark_prompt_attention  attention within packed prompts
+ *   dspark_sample            truncated sampling and the distributions themselves
+ *
  * Conventions shared by every call
  *   - All array arguments are DEVICE pointers on the current CUDA device,
- *     contiguous and row-major, owned by the caller.  The library never
+ *     contiguous and row-major (but for the token strides that a call names),
+ *     owned by the caller.  The library never
  *     allocates, frees or synchronises inside these calls, so every call can
  *     be captured in a CUDA graph (the caller keeps the buffers at fixed
  *     addresses, as the draft step of "DSpark implementation and evaluation"
