@@ -133,7 +133,7 @@ __device__ __forceinline__ u64 mass_of(float w) {
     mass_halves(w, hi, lo);
     return (static_cast<u64>(hi) << 20) + lo;
 }
-// A sum of masses, of fewer than 4096 entries.
+// A sum of masses, of fewer than 4096 entries, which are counted apart (by the piece where all are added).
 struct MassSum {
     uint32_t hi = 0, lo = 0, n = 0;
     __device__ __forceinline__ void add(float w) {
@@ -141,8 +141,8 @@ struct MassSum {
         mass_halves_biased(w, h, l);
         hi += h;
         lo += l;
-        ++n;
     }
+    __device__ __forceinline__ void count(uint32_t k) { n += k; }             // entries that were added
     __device__ __forceinline__ u64 value() const {
         return (static_cast<u64>(hi - n * kHalfBias) << 20) + (lo - n * kHalfBias);
     }
@@ -480,6 +480,7 @@ __device__ __forceinline__ void sample_row(const SampleArgs& p, Shared<kThreads>
     // c: the largest entry; d: the smallest of the groups' largest, as its complement
     const Reduced x = reduce(odd, leads, best, least_group != 0 ? 0xFFFFFFFFu - least_group : 0u);
     if (x.a != 0) flags |= DSPARK_STATUS_NUMERIC;
+    const bool clean = x.a == 0;                                              // no NaN, no infinity but -infinity
     const uint32_t top_bits = static_cast<uint32_t>(x.c >> 32);
     if (top_bits == 0) flags |= DSPARK_STATUS_NUMERIC;
     if (rank == 0 && tid == 0 && flags) set_status(p.ws, flags);
@@ -897,13 +898,13 @@ __device__ __forceinline__ void sample_row(const SampleArgs& p, Shared<kThreads>
                 if (tid == 0) s.list_count = 0u;
                 for (int i = tid; i < kBins; i += kThreads) s.hist[i] = 0u;
                 __syncthreads();
-                const bool plain = linear && limit == 0 && min_p == 0.0f;    // no more than the range to look at
+                const bool plain = linear && limit == 0 && min_p == 0.0f && clean;    // no more than the range to look at
                 if (plain) {
                     pass(streamed, [&](int, const float (&x)[kPiece], const uint4&, int) {
 #pragma unroll
                         for (int e = 0; e < kPiece; ++e) {
                             const int part = min(kBins - 1, floor_of((m - x[e]) * scale));
-                            if (x[e] >= from && x[e] <= m) atomicAdd(&s.hist[part], 1u);
+                            if (x[e] >= from) atomicAdd(&s.hist[part], 1u);
                         }
                     });
                 } else {
@@ -1000,16 +1001,30 @@ __device__ __forceinline__ void sample_row(const SampleArgs& p, Shared<kThreads>
                     }
                 };
                 if (plain) {
+                    // The parts do not rise with the logit: bounds found once are compared with, instead of parts.
+                    auto largest = [&](int part) {                            // ordered bits, of a logit of this part or a later one
+                        uint32_t below = lo, above = top_bits + 1u;           // lo is in the last part, or beyond all
+                        while (above - below > 1u) {
+                            const uint32_t mid = below + (above - below) / 2u;
+                            const float l = float_from_order_bits(mid);
+                            if (min(kBins - 1, floor_of((m - l) * scale)) >= part) below = mid;
+                            else above = mid;
+                        }
+                        return below;
+                    };
+                    const float ceiling = first > 0 ? float_from_order_bits(largest(first)) : INFINITY;   // above it: summed
+                    const float ground = last < kBins - 1 ? float_from_order_bits(largest(last + 1) + 1u) : from;
                     uint32_t entries_above = 0;
                     pass(streamed, [&](int i, const float (&x)[kPiece], const uint4&, int) {
 #pragma unroll
                         for (int e = 0; e < kPiece; ++e) {
-                            const bool in = x[e] >= from && x[e] <= m;
-                            const int part = in ? min(kBins - 1, floor_of((m - x[e]) * scale)) : kBins;
-                            mass.add(part < first ? weight(x[e]) : 0.0f);
-                            entries_above += part < first ? 1u : 0u;
-                            if (part >= first && part <= last) inside(x[e], place0 + i * kPiece + e);
+                            const bool in = x[e] > ceiling;
+                            const float w = weight(x[e]);
+                            mass.add(in ? w : 0.0f);
+                            entries_above += in ? 1u : 0u;
+                            if (x[e] >= ground && !in) inside(x[e], place0 + i * kPiece + e);
                         }
+                        mass.count(kPiece);
                     });
                     more = entries_above;
                 } else {
@@ -1017,6 +1032,7 @@ __device__ __forceinline__ void sample_row(const SampleArgs& p, Shared<kThreads>
                         const int part = part_of(l, true);
                         if (part < first) {
                             mass.add(weight(l));
+                            mass.count(1);
                             ++more;
                         } else if (part <= last) {
                             inside(l, v);
@@ -1080,28 +1096,49 @@ __device__ __forceinline__ void sample_row(const SampleArgs& p, Shared<kThreads>
             }
         };
 
-        // what min-p leaves
+        // The mass, first of all entries alike where neither min-p nor top-k nor something odd is in the way (what lies
+        // outside the row weighs nothing); the smallest entry is then only asked for if the mass needs it.
         MassSum mass;
-        uint32_t count = 0;
-        float smallest = INFINITY;
-        pass(streamed, [&](int, const float (&x)[kPiece], const uint4&, int) {
+        float lowest = -INFINITY;
+        u64 entries = static_cast<u64>(V);
+        bool alike = clean && min_p == 0.0f && k == V;
+        if (alike) {
+            pass(streamed, [&](int, const float (&x)[kPiece], const uint4&, int) {
 #pragma unroll
-            for (int e = 0; e < kPiece; ++e) {
-                const bool finite = fabsf(x[e]) < INFINITY;
-                float w = finite ? weight(x[e]) : 0.0f;
-                const bool in = finite && w >= min_p;
-                if (!in) w = 0.0f;
-                mass.add(w);
-                count += in ? 1u : 0u;
-                if (in) smallest = fminf(smallest, x[e]);
-            }
-        });
-        const u64 own = mass.value();
-        const Reduced all = reduce(own, count, 0, count != 0 ? 0xFFFFFFFFu - float_order_bits(smallest) : 0u);
-        const float lowest = float_from_order_bits(0xFFFFFFFFu - static_cast<uint32_t>(all.d));
-        u64 entries = all.b;
-        total = all.a;
-        run_mass = warp_sum_u64(own);
+                for (int e = 0; e < kPiece; ++e) mass.add(weight(fmaxf(x[e], -INFINITY)));
+                mass.count(kPiece);
+            });
+            const u64 own = mass.value();
+            total = reduce(own, 0, 0, 0).a;
+            run_mass = warp_sum_u64(own);
+            const u64 need = max(1ull, share_of(total, P));
+            alike = need >= total || (total - need) / entries > 0;
+        }
+        if (!alike) {
+            // what min-p leaves
+            mass = MassSum();
+            uint32_t count = 0;
+            float smallest = INFINITY;
+            pass(streamed, [&](int, const float (&x)[kPiece], const uint4&, int) {
+#pragma unroll
+                for (int e = 0; e < kPiece; ++e) {
+                    const bool finite = fabsf(x[e]) < INFINITY;
+                    float w = finite ? weight(x[e]) : 0.0f;
+                    const bool in = finite && w >= min_p;
+                    if (!in) w = 0.0f;
+                    mass.add(w);
+                    count += in ? 1u : 0u;
+                    if (in) smallest = fminf(smallest, x[e]);
+                }
+                mass.count(kPiece);
+            });
+            const u64 own = mass.value();
+            const Reduced all = reduce(own, count, 0, count != 0 ? 0xFFFFFFFFu - float_order_bits(smallest) : 0u);
+            lowest = float_from_order_bits(0xFFFFFFFFu - static_cast<uint32_t>(all.d));
+            entries = all.b;
+            total = all.a;
+            run_mass = warp_sum_u64(own);
+        }
         runs_known = true;                                                    // if everything is kept
         if (static_cast<u64>(k) < entries) {
             close_in(static_cast<u64>(k), ~0ull - 1, lowest);
@@ -1135,7 +1172,10 @@ __device__ __forceinline__ void sample_row(const SampleArgs& p, Shared<kThreads>
             pass(streamed, [&](int i, const float (&y)[kPiece], const uint4&, int) {
 #pragma unroll
                 for (int e = 0; e < kPiece; ++e)
-                    if (y[e] >= cut_logit) mass.add(kept(y[e], place0 + i * kPiece + e));
+                    if (y[e] >= cut_logit) {
+                        mass.add(kept(y[e], place0 + i * kPiece + e));
+                        mass.count(1);
+                    }
             });
             report_run(warp_sum_u64(mass.value()));
         }
