@@ -27,9 +27,11 @@
 //      drawn mass again.  Probabilities: zeros and the list's entries, or a pass over the row
 // A row that needs 3 and 4 is bound by its instructions (an exponential and an exact mass per entry and
 // pass), the others by memory.  576 rows of 151936 with their distributions (700 MB), every third row without
-// top-k, take 330 us: 136 us for such a row on its SM, 43 us for one with a short list, 24 us for a greedy one.
-// Rows in their order 443 us, the longest first 366 us, from a queue 332 us; two blocks of half the threads per
-// SM 446 us (the rows under way no longer fit the L2 cache).  One row takes 12.5 us, a chain of exchanges.
+// top-k, take 314 us: about 130 us for such a row on its SM, 43 us for one with a short list, 24 us for a greedy
+// one.  Rows in their order 443 us, the longest first 366 us, from a queue 332 us, lean passes where neither top-k
+// nor min-p is set 314 us (with the sum above the cut and its list in passes of their own 326 us); two blocks of
+// half the threads per SM 446 us (the rows under way no longer fit the L2 cache).  One row takes 12.5 us, a chain of
+// exchanges.
 #include "attention_common.cuh"
 #include "device_common.cuh"
 #include "half_common.cuh"
