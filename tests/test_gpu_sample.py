@@ -81,6 +81,14 @@ def test_row_counts(cuda_lib, R):
     Rows(_normal(R, 1500, R), *_settings(rng, R)).check(cuda_lib)
 
 
+@pytest.mark.parametrize("bf16", [False, True])
+def test_more_long_rows_than_blocks(cuda_lib, bf16):
+    import torch
+    R, V = 170, 40001
+    rng = np.random.default_rng(V)
+    Rows(_normal(R, V, V, dtype=torch.bfloat16 if bf16 else None), *_settings(rng, R)).check(cuda_lib)
+
+
 @pytest.mark.parametrize("V,R", [(151936, 3), (151936, 41), (300007, 2), (1 << 21, 1)])
 def test_large_vocabularies(cuda_lib, V, R):
     rng = np.random.default_rng(V + R)
