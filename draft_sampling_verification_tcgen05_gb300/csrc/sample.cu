@@ -144,6 +144,15 @@ struct MassSum {
         hi += h;
         lo += l;
     }
+    // Two masses at once, by packed instructions (the same roundings).
+    __device__ __forceinline__ void add(float2 w) {
+        const float2 scale = make_float2(0x1p20f, 0x1p20f), one = make_float2(0x1p23f, 0x1p23f);
+        const float2 s = __fmul2_rn(w, scale), t = __fadd2_rz(s, one);
+        const float2 rest = __fadd2_rn(s, __fadd2_rn(one, make_float2(-t.x, -t.y)));
+        const float2 u = __fadd2_rz(__fmul2_rn(rest, scale), one);
+        hi += __float_as_uint(t.x) + __float_as_uint(t.y);
+        lo += __float_as_uint(u.x) + __float_as_uint(u.y);
+    }
     __device__ __forceinline__ void count(uint32_t k) { n += k; }             // entries that were added
     __device__ __forceinline__ u64 value() const {
         return (static_cast<u64>(hi - n * kHalfBias) << 20) + (lo - n * kHalfBias);
@@ -491,6 +500,10 @@ __device__ __forceinline__ void sample_row(const SampleArgs& p, Shared<kThreads>
     const float bottom = float_from_order_bits(0xFFFFFFFFu - static_cast<uint32_t>(x.d));
 
     auto weight = [&](float l) { return expf(__fmul_rn(__fsub_rn(l, m), inv)); };
+    auto weights = [&](float l, float k) {
+        const float2 y = __fmul2_rn(__fadd2_rn(make_float2(l, k), make_float2(-m, -m)), make_float2(inv, inv));
+        return make_float2(expf(y.x), expf(y.y));
+    };
 
     u64 cut = 0, total = 0;                                                   // the kept set: key >= cut; its mass
     u64 limit = 0;                                                            // likewise after top-k, while top-p is sought
@@ -1019,12 +1032,13 @@ __device__ __forceinline__ void sample_row(const SampleArgs& p, Shared<kThreads>
                     uint32_t entries_above = 0;
                     pass(streamed, [&](int i, const float (&x)[kPiece], const uint4&, int) {
 #pragma unroll
-                        for (int e = 0; e < kPiece; ++e) {
-                            const bool in = x[e] > ceiling;
-                            const float w = weight(x[e]);
-                            mass.add(in ? w : 0.0f);
-                            entries_above += in ? 1u : 0u;
-                            if (x[e] >= ground && !in) inside(x[e], place0 + i * kPiece + e);
+                        for (int e = 0; e < kPiece; e += 2) {
+                            const bool in0 = x[e] > ceiling, in1 = x[e + 1] > ceiling;
+                            const float2 w = weights(x[e], x[e + 1]);
+                            mass.add(make_float2(in0 ? w.x : 0.0f, in1 ? w.y : 0.0f));
+                            entries_above += (in0 ? 1u : 0u) + (in1 ? 1u : 0u);
+                            if (x[e] >= ground && !in0) inside(x[e], place0 + i * kPiece + e);
+                            if (x[e + 1] >= ground && !in1) inside(x[e + 1], place0 + i * kPiece + e + 1);
                         }
                         mass.count(kPiece);
                     });
@@ -1107,7 +1121,7 @@ __device__ __forceinline__ void sample_row(const SampleArgs& p, Shared<kThreads>
         if (alike) {
             pass(streamed, [&](int, const float (&x)[kPiece], const uint4&, int) {
 #pragma unroll
-                for (int e = 0; e < kPiece; ++e) mass.add(weight(fmaxf(x[e], -INFINITY)));
+                for (int e = 0; e < kPiece; e += 2) mass.add(weights(fmaxf(x[e], -INFINITY), fmaxf(x[e + 1], -INFINITY)));
                 mass.count(kPiece);
             });
             const u64 own = mass.value();
