@@ -790,7 +790,54 @@ __device__ __forceinline__ void sample_row(const SampleArgs& p, Shared<kThreads>
         const float reach = static_cast<float>(s.out[0] + 1);
         // a logit that no entry of those parts is below
         const float least = m - reach / scale * (1.0f + 1e-5f) - fabsf(m) * 2.5e-7f;
-        each(least, [&](float l, int v, bool in) { append(in && (m - l) * scale < reach, l, v); });
+        auto list = [&](float l, int v, bool in) { append(in && (m - l) * scale < reach, l, v); };
+        // Few of the parts whose largest entries are known reach it, and only those are looked at again: the
+        // j-th pieces of a lane, in all the full batches of this warp's run.
+        uint8_t* const hot = reinterpret_cast<uint8_t*>(s.segment) + warp * (32 * kBatch);
+        int parts = 0;
+#pragma unroll
+        for (int j = 0; j < kBatch; ++j) {
+            const uint32_t vote = __ballot_sync(0xFFFFFFFFu, tops[j] >= least);
+            if (tops[j] >= least) hot[parts + __popc(vote & ((1u << lane) - 1u))] = static_cast<uint8_t>(j * 32 + lane);
+            parts += __popc(vote);
+        }
+        __syncwarp();
+        const int full0 = run0 < whole0 ? min(run1, run0 + 32) : run0;         // as pass() goes
+        const int batches = max(0, (whole1 - full0) / (32 * kBatch)), full1 = full0 + 32 * kBatch * batches;
+        if (4 * parts * batches > run1 - run0) {
+            each(least, list);
+        } else {
+            auto look = [&](bool there, int i, const uint4& w) {
+                float x[kPiece];
+                unpack(w, i, x);
+#pragma unroll
+                for (int e = 0; e < kPiece; ++e) {
+                    const bool in = there && x[e] >= least && x[e] < INFINITY;
+                    if (__any_sync(0xFFFFFFFFu, in)) list(x[e], place0 + i * kPiece + e, in);
+                }
+            };
+            for (int end = 0; end < 2; ++end) {                               // what is in no full batch
+                const int to = end == 0 ? full0 : run1;
+                for (int i0 = end == 0 ? run0 : full1; i0 < to; i0 += 32) {
+                    const int i = i0 + static_cast<int>(lane);
+                    look(i < to, i, i < to ? fetch(i, streamed) : make_uint4(0u, 0u, 0u, 0u));
+                }
+            }
+            const int work = parts * batches;
+            for (int t0 = 0; t0 < work; t0 += 64) {
+                uint4 w[2];
+                int at_piece[2];
+#pragma unroll
+                for (int y = 0; y < 2; ++y) {
+                    const int t = t0 + 32 * y + static_cast<int>(lane);
+                    const int part = t / batches, id = t < work ? hot[part] : 0;
+                    at_piece[y] = t < work ? full0 + (t - part * batches) * (32 * kBatch) + id : run0;
+                    w[y] = t < work ? fetch(at_piece[y], streamed) : make_uint4(0u, 0u, 0u, 0u);
+                }
+#pragma unroll
+                for (int y = 0; y < 2; ++y) look(t0 + 32 * y + static_cast<int>(lane) < work, at_piece[y], w[y]);
+            }
+        }
         const int count = gather();
         if (count <= kList) {
             if (rank == 0) settle(count, 0, 0, static_cast<u64>(k), ~0ull);
