@@ -15,7 +15,7 @@
 //   1. the largest entry, and the largest of each thread; a greedy row is settled by that
 //   2. with a small top-k: a histogram of the largest logits of groups of entries (at least 2 k groups)
 //      gives a bound that at least k entries reach; those entries, usually a few more than k, go to a
-//      list, and one block settles min-p, top-p and the token on it: a histogram of counts and masses
+//      list from the threads' parts whose largest entry reaches it, and one block settles min-p, top-p and the token on it: a histogram of counts and masses
 //      over 1024 parts of the range, then over the part that holds the cut, until that is one entry
 //   3. else the total mass of the entries that min-p leaves; entries of mass at most (Q - need) / count
 //      cannot be needed for top-p
@@ -27,11 +27,11 @@
 //      drawn mass again.  Probabilities: zeros and the list's entries, or a pass over the row
 // A row that needs 3 and 4 is bound by its instructions (an exponential and an exact mass per entry and
 // pass), the others by memory.  576 rows of 151936 with their distributions (700 MB), every third row without
-// top-k, take 314 us: about 130 us for such a row on its SM, 43 us for one with a short list, 24 us for a greedy
-// one.  Rows in their order 443 us, the longest first 366 us, from a queue 332 us, lean passes where neither top-k
-// nor min-p is set 314 us (with the sum above the cut and its list in passes of their own 326 us); two blocks of
-// half the threads per SM 446 us (the rows under way no longer fit the L2 cache).  One row takes 12.5 us, a chain of
-// exchanges.
+// top-k, take 303 us, 2.3 TB/s: about 123 us for such a row on its SM, 41 us for one with a list, 24 us for a
+// greedy one.  Rows in their order 443 us, the longest first 366 us, from a queue 332 us, lean passes where neither
+// top-k nor min-p is set 314 us (with the sum above the cut and its list in passes of their own 326 us), packed
+// arithmetic 307 us, a list from the parts that reach it 303 us; two blocks of half the threads per SM 446 us (the
+// rows under way no longer fit the L2 cache).  One row takes 12.5 us, a chain of exchanges.
 #include "attention_common.cuh"
 #include "device_common.cuh"
 #include "half_common.cuh"
