@@ -87,6 +87,15 @@ def test_sizes(cuda_lib, T, Hq, Hkv, page):
     case.check(cuda_lib, norm=T % 2 == 0)
 
 
+@pytest.mark.parametrize("T,D,rot,interleaved", [(4501, 80, 32, False), (4501, 128, 64, True), (1103, 512, 496, True),
+                                                 (35003, 16, 16, False), (9001, 48, 48, True)])
+def test_many_tokens(cuda_lib, T, D, rot, interleaved):
+    # several rows to a lane, more of them than the last lanes' rows (9 heads)
+    case = Case(T, 5, 2, D, rot, 16, T // 16 + 2, "f16", seed=T + D, pad=T // 7)
+    case.check(cuda_lib, interleaved, norm=False)
+    case.check(cuda_lib, interleaved, norm=True)
+
+
 def test_in_place_queries_streams_and_graphs(cuda_lib):
     import torch
     case = Case(50, 4, 2, 128, 128, 16, 8, "bf16", seed=3)
