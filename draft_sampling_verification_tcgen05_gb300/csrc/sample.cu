@@ -22,7 +22,8 @@
 //   4. the cut is closed in on among the others: a histogram of counts over 2048 parts of their range,
 //      bounds of each part's mass from its edges, the parts that can hold the cut are the next range,
 //      and the mass above it is summed exactly; once the range's entries fit the list, they are settled
-//      there; a range of one repeated logit is settled by id
+//      there; a range that bounds do not make smaller (two logits, many times each, where the wanted mass is
+//      reached between them) is halved by an exact sum; a range of one repeated logit is settled by id
 //   5. the token, where the list did not give it: kept masses of the runs, then the run that holds the
 //      drawn mass again.  Probabilities: zeros and the list's entries, or a pass over the row
 // A row that needs 3 and 4 is bound by its instructions (an exponential and an exact mass per entry and
@@ -945,7 +946,11 @@ __device__ __forceinline__ void sample_row(const SampleArgs& p, Shared<kThreads>
             uint32_t hi = top_bits, lo = float_order_bits(lowest);
             for (int i = tid; i < kBins; i += kThreads) s.share[i] = 0u;
             exchange(0, 0, 0, 0);                                             // all blocks' shares are clear
-            for (int level = 0; level < 8; ++level) {                         // four settle any range; bounded all the same
+            // A level leaves a range of less than half, or the next one halves it: the range is one logit, at the
+            // latest, after twice the 32 bits.
+            constexpr int kLevels = 72;
+            bool halve = false;
+            for (int level = 0; level < kLevels; ++level) {
                 const float scale = linear ? kBins / (m - lowest) : 0.0f;
                 int shift = 0;
                 while (((hi - lo) >> shift) >= kBins) ++shift;
@@ -961,95 +966,102 @@ __device__ __forceinline__ void sample_row(const SampleArgs& p, Shared<kThreads>
                 for (int i = tid; i < kBins; i += kThreads) s.hist[i] = 0u;
                 __syncthreads();
                 const bool plain = linear && limit == 0 && min_p == 0.0f && clean;    // no more than the range to look at
-                if (plain) {
-                    pass(streamed, [&](int, const float (&x)[kPiece], const uint4&, int) {
+                // The first and last part that can hold the cut, and whether the entries in them fit the list; to halve
+                // the range, all the parts behind its middle.
+                int first = (static_cast<int>((hi - lo) >> shift) + 1) / 2, last = kBins - 1;
+                bool fits = false;
+                if (!halve) {
+                    if (plain) {
+                        pass(streamed, [&](int, const float (&x)[kPiece], const uint4&, int) {
 #pragma unroll
-                        for (int e = 0; e < kPiece; ++e) {
-                            const int part = min(kBins - 1, floor_of((m - x[e]) * scale));
-                            if (x[e] >= from) atomicAdd(&s.hist[part], 1u);
-                        }
-                    });
-                } else {
-                    every(from, [&](float l, int) {
-                        const int part = part_of(l, true);
-                        if (part < kBins) atomicAdd(&s.hist[part], 1u);
-                    });
-                }
-                __syncthreads();
-                if (C > 1) {
-                    // each block adds up its share of the bins over all blocks, for the first one
-                    const int share = kBins / C, bin0 = static_cast<int>(rank) * share;
-                    for (int i = tid; i < kBins; i += kThreads) {
-                        const uint32_t to = static_cast<uint32_t>(i / share);
-                        if (to != rank) send_add(remote(&s.share[i], to), s.hist[i], remote(&s.bar_share, to));
-                        else atomicAdd(&s.share[i], s.hist[i]);
-                    }
-                    receive(s.bar_share, used_share, static_cast<uint32_t>((C - 1) * share) * 4u);
-                    __syncthreads();
-                    for (int i = bin0 + tid; i < bin0 + share; i += kThreads) {
-                        if (rank != 0) send32(remote(&s.bins[i], 0), s.share[i], remote(&s.bar_bins, 0));
-                        else s.bins[i] = s.share[i];
-                        s.share[i] = 0u;                                      // the next level comes after an exchange
-                    }
-                    if (rank == 0) receive(s.bar_bins, used_bins, static_cast<uint32_t>(kBins - share) * 4u);
-                } else {
-                    for (int i = tid; i < kBins; i += kThreads) s.bins[i] = s.hist[i];
-                }
-                __syncthreads();
-                if (rank == 0) {
-                    // bounds of each part's mass from its edges, with room for the rounding of edges and expf
-                    u64 c[kPerThread], least[kPerThread], most[kPerThread], in_least = 0, in_most = 0;
-#pragma unroll
-                    for (int e = 0; e < kPerThread; ++e) {
-                        const int i = tid * kPerThread + e;
-                        c[e] = s.bins[i];
-                        least[e] = most[e] = c[e];
-                        if (want_count == ~0ull) {
-                            float hi_edge, lo_edge;
-                            if (linear) {
-                                const float rounding = fabsf(m) * 2.5e-7f;
-                                hi_edge = m - (i / scale) * (1.0f - 1e-5f) + rounding;
-                                lo_edge = i == kBins - 1 ? lowest : m - ((i + 1) / scale) * (1.0f + 1e-5f) - rounding;
-                            } else {
-                                const uint32_t first = hi - min(hi - lo, static_cast<uint32_t>(i) << shift);
-                                const uint32_t last = hi - min(hi - lo, (static_cast<uint32_t>(i + 1) << shift) - 1u);
-                                hi_edge = float_from_order_bits(first);
-                                lo_edge = float_from_order_bits(last);
+                            for (int e = 0; e < kPiece; ++e) {
+                                const int part = min(kBins - 1, floor_of((m - x[e]) * scale));
+                                if (x[e] >= from) atomicAdd(&s.hist[part], 1u);
                             }
-                            most[e] = c[e] * (mass_of(fminf(1.0f, weight(hi_edge) * (1.0f + 1e-4f))) + 1);
-                            least[e] = c[e] * mass_of(fminf(1.0f, fmaxf(0.0f, weight(lo_edge) * (1.0f - 1e-4f))));
-                        }
-                        in_least += least[e];
-                        in_most += most[e];
-                    }
-                    u64 least_before = in_least, most_before = in_most;
-                    if (tid == 0) s.out[0] = s.out[1] = kBins - 1;            // first and last part that can hold the cut
-                    scan(least_before, most_before, 0, 0);
-                    least_before -= in_least;
-                    most_before -= in_most;
-                    const u64 want = want_count != ~0ull ? want_count - above : want_mass - over;
-#pragma unroll
-                    for (int e = 0; e < kPerThread; ++e) {
-                        const u64 i = static_cast<u64>(tid * kPerThread + e);
-                        if (most_before < want && most_before + most[e] >= want) s.out[0] = i;
-                        if (least_before < want && least_before + least[e] >= want) s.out[1] = i;
-                        least_before += least[e];
-                        most_before += most[e];
+                        });
+                    } else {
+                        every(from, [&](float l, int) {
+                            const int part = part_of(l, true);
+                            if (part < kBins) atomicAdd(&s.hist[part], 1u);
+                        });
                     }
                     __syncthreads();
-                    // the entries in those parts
-                    u64 inside = 0, none = 0, zero = 0, nil = 0;
-#pragma unroll
-                    for (int e = 0; e < kPerThread; ++e) {
-                        const u64 i = static_cast<u64>(tid * kPerThread + e);
-                        if (i >= s.out[0] && i <= s.out[1]) inside += c[e];
+                    if (C > 1) {
+                        // each block adds up its share of the bins over all blocks, for the first one
+                        const int share = kBins / C, bin0 = static_cast<int>(rank) * share;
+                        for (int i = tid; i < kBins; i += kThreads) {
+                            const uint32_t to = static_cast<uint32_t>(i / share);
+                            if (to != rank) send_add(remote(&s.share[i], to), s.hist[i], remote(&s.bar_share, to));
+                            else atomicAdd(&s.share[i], s.hist[i]);
+                        }
+                        receive(s.bar_share, used_share, static_cast<uint32_t>((C - 1) * share) * 4u);
+                        __syncthreads();
+                        for (int i = bin0 + tid; i < bin0 + share; i += kThreads) {
+                            if (rank != 0) send32(remote(&s.bins[i], 0), s.share[i], remote(&s.bar_bins, 0));
+                            else s.bins[i] = s.share[i];
+                            s.share[i] = 0u;                                  // the next level comes after an exchange
+                        }
+                        if (rank == 0) receive(s.bar_bins, used_bins, static_cast<uint32_t>(kBins - share) * 4u);
+                    } else {
+                        for (int i = tid; i < kBins; i += kThreads) s.bins[i] = s.hist[i];
                     }
-                    block(inside, none, zero, nil);
-                    if (tid == 0) s.out[2] = inside;
+                    __syncthreads();
+                    if (rank == 0) {
+                        // bounds of each part's mass from its edges, with room for the rounding of edges and expf
+                        u64 c[kPerThread], least[kPerThread], most[kPerThread], in_least = 0, in_most = 0;
+#pragma unroll
+                        for (int e = 0; e < kPerThread; ++e) {
+                            const int i = tid * kPerThread + e;
+                            c[e] = s.bins[i];
+                            least[e] = most[e] = c[e];
+                            if (want_count == ~0ull) {
+                                float hi_edge, lo_edge;
+                                if (linear) {
+                                    const float rounding = fabsf(m) * 2.5e-7f;
+                                    hi_edge = m - (i / scale) * (1.0f - 1e-5f) + rounding;
+                                    lo_edge = i == kBins - 1 ? lowest : m - ((i + 1) / scale) * (1.0f + 1e-5f) - rounding;
+                                } else {
+                                    const uint32_t first = hi - min(hi - lo, static_cast<uint32_t>(i) << shift);
+                                    const uint32_t last = hi - min(hi - lo, (static_cast<uint32_t>(i + 1) << shift) - 1u);
+                                    hi_edge = float_from_order_bits(first);
+                                    lo_edge = float_from_order_bits(last);
+                                }
+                                most[e] = c[e] * (mass_of(fminf(1.0f, weight(hi_edge) * (1.0f + 1e-4f))) + 1);
+                                least[e] = c[e] * mass_of(fminf(1.0f, fmaxf(0.0f, weight(lo_edge) * (1.0f - 1e-4f))));
+                            }
+                            in_least += least[e];
+                            in_most += most[e];
+                        }
+                        u64 least_before = in_least, most_before = in_most;
+                        if (tid == 0) s.out[0] = s.out[1] = kBins - 1;        // first and last part that can hold the cut
+                        scan(least_before, most_before, 0, 0);
+                        least_before -= in_least;
+                        most_before -= in_most;
+                        const u64 want = want_count != ~0ull ? want_count - above : want_mass - over;
+#pragma unroll
+                        for (int e = 0; e < kPerThread; ++e) {
+                            const u64 i = static_cast<u64>(tid * kPerThread + e);
+                            if (most_before < want && most_before + most[e] >= want) s.out[0] = i;
+                            if (least_before < want && least_before + least[e] >= want) s.out[1] = i;
+                            least_before += least[e];
+                            most_before += most[e];
+                        }
+                        __syncthreads();
+                        // the entries in those parts
+                        u64 inside = 0, none = 0, zero = 0, nil = 0;
+#pragma unroll
+                        for (int e = 0; e < kPerThread; ++e) {
+                            const u64 i = static_cast<u64>(tid * kPerThread + e);
+                            if (i >= s.out[0] && i <= s.out[1]) inside += c[e];
+                        }
+                        block(inside, none, zero, nil);
+                        if (tid == 0) s.out[2] = inside;
+                    }
+                    hear();
+                    first = static_cast<int>(s.out[0]);
+                    last = static_cast<int>(s.out[1]);
+                    fits = s.out[2] <= kList;
                 }
-                hear();
-                const int first = static_cast<int>(s.out[0]), last = static_cast<int>(s.out[1]);
-                const bool fits = s.out[2] <= kList;
                 __syncthreads();                                              // the bins' place may become the list's
                 // above those parts: summed; in them: listed if they fit, else bounded
                 u64 more = 0, high = 0, low = 0;
@@ -1103,8 +1115,13 @@ __device__ __forceinline__ void sample_row(const SampleArgs& p, Shared<kThreads>
                     });
                 }
                 const u64 own = mass.value();
-                run_mass += warp_sum_u64(own);
                 const Reduced y = reduce(own, more, high, low);
+                if (halve && (want_count != ~0ull ? above + y.b >= want_count : over + y.a >= want_mass)) {
+                    lo = hi - (static_cast<uint32_t>(first) << shift) + 1u;   // it is in the upper half
+                    halve = false;
+                    continue;
+                }
+                run_mass += warp_sum_u64(own);
                 over += y.a;
                 above += y.b;
                 if (fits) {
@@ -1129,8 +1146,11 @@ __device__ __forceinline__ void sample_row(const SampleArgs& p, Shared<kThreads>
                     return;
                 }
                 linear = false;
+                const uint32_t width = hi - lo;
                 hi = static_cast<uint32_t>(y.c);
                 lo = 0xFFFFFFFFu - static_cast<uint32_t>(y.d);
+                // Bounds cannot part large groups of equal logits where the wanted mass is reached between them.
+                halve = hi - lo > width / 2u;
                 if (hi == lo) {
                     // one logit, repeated: so many of them by id
                     const u64 q = mass_of(weight(float_from_order_bits(hi)));
@@ -1157,6 +1177,7 @@ __device__ __forceinline__ void sample_row(const SampleArgs& p, Shared<kThreads>
                     return;
                 }
             }
+            if (rank == 0 && tid == 0) set_status(p.ws, DSPARK_STATUS_INTERNAL);   // not reached: see kLevels
         };
 
         // The mass, first of all entries alike where neither min-p nor top-k nor something odd is in the way (what lies
