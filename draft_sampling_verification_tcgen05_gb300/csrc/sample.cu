@@ -58,6 +58,14 @@ struct Block {
 constexpr int kFew = 256;                  // entries that are settled by comparing each with all
 constexpr int kBatch = 4;                  // 16-byte pieces that a thread has under way
 constexpr uint32_t kWaitPeer = 0xA01;
+// A test build makes a wait run out: limits of 2 ms, and block DSPARK_LATE_RANK of a cluster 20 ms late at its
+// exchange DSPARK_LATE_AT (expressions in the names of sample_row).
+#ifdef DSPARK_LATE_AT
+constexpr long long kPeerLimitNs = 2000000;
+#else
+constexpr long long kPeerLimitNs = kDefaultTimeoutNs;
+#endif
+constexpr long long kUnderWayNs = 100000;  // far more than a store into another block's shared memory takes
 
 struct Plan {
     WsHeader header;
@@ -212,8 +220,10 @@ __global__ void __launch_bounds__(kPlanThreads) sample_plan_kernel(const __grid_
     for (int r = tid; r < p.R; r += kPlanThreads) p.order[atomicAdd(&s_at[kind(r)], 1)] = r;
 }
 
+// One row.  False, in all threads of the block, where a wait for the other blocks gave up: nothing is sent
+// or written any more then.
 template <typename T, int kThreads>
-__device__ __forceinline__ void sample_row(const SampleArgs& p, Shared<kThreads>& s, T* const held, const long long r) {
+__device__ __forceinline__ bool sample_row(const SampleArgs& p, Shared<kThreads>& s, T* const held, const long long r) {
     constexpr int kWarps = Block<kThreads>::kWarps, kPerThread = Block<kThreads>::kPerThread, kParts = Block<kThreads>::kParts;
     const int tid = threadIdx.x, V = p.V;
     const uint32_t warp = warp_id(), lane = lane_id();
@@ -233,11 +243,14 @@ __device__ __forceinline__ void sample_row(const SampleArgs& p, Shared<kThreads>
         // the others may write here from now on; waited for ahead of the first exchange
         asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
     }
-    // Waits for `bytes` that other blocks send to `bar` here; `uses` counts its phases.
+    // Waits for `bytes` that other blocks send to `bar` here; `uses` counts its phases.  All of the block's threads
+    // come out with the same `ok`: whoever finds it false leaves sample_row.
+    bool ok = true;
     auto receive = [&](u64& bar, int& uses, uint32_t bytes) {
         uint64_t* b = reinterpret_cast<uint64_t*>(&bar);
         if (tid == 0) mbar_arrive_expect_tx(b, bytes);
-        mbar_wait(b, static_cast<uint32_t>(uses++) & 1u, p.ws, kDefaultTimeoutNs, kWaitPeer);
+        const bool there = mbar_wait(b, static_cast<uint32_t>(uses++) & 1u, p.ws, kPeerLimitNs, kWaitPeer);
+        ok = __syncthreads_and(there) != 0;
     };
     int used_red[2] = {0, 0}, used_out = 0, used_hist = 0, used_list = 0, used_segment = 0, used_found = 0, used_share = 0,
         used_bins = 0;
@@ -262,9 +275,19 @@ __device__ __forceinline__ void sample_row(const SampleArgs& p, Shared<kThreads>
 
     // ---- exchanges ----
     int turn = 0;
+#ifdef DSPARK_LATE_AT
+    int exchanges = 0;
+#endif
     // Every block's four values, added up (a, b) or by maximum (c, d); the arguments count in thread 0 only.
     // Afterwards s.red[turn ^ 1][i] holds block i's.
     auto exchange = [&](u64 a, u64 b, u64 c, u64 d) {
+#ifdef DSPARK_LATE_AT
+        if (C > 1 && exchanges++ == DSPARK_LATE_AT && rank == DSPARK_LATE_RANK) {
+            const long long t0 = global_ns();
+            while (global_ns() - t0 < 20000000) {
+            }
+        }
+#endif
         if (tid == 0) {
             u64* mine = s.red[turn][rank];
             mine[0] = a; mine[1] = b; mine[2] = c; mine[3] = d;
@@ -277,6 +300,7 @@ __device__ __forceinline__ void sample_row(const SampleArgs& p, Shared<kThreads>
             receive(s.bar_red[turn], used_red[turn], static_cast<uint32_t>(C - 1) * 32u);
         }
         Reduced x{0, 0, 0, 0};
+        if (!ok) return x;
         for (int i = 0; i < C; ++i) {
             const u64* y = s.red[turn][i];
             x.a += y[0];
@@ -491,6 +515,7 @@ __device__ __forceinline__ void sample_row(const SampleArgs& p, Shared<kThreads>
     }
     // c: the largest entry; d: the smallest of the groups' largest, as its complement
     const Reduced x = reduce(odd, leads, best, least_group != 0 ? 0xFFFFFFFFu - least_group : 0u);
+    if (!ok) return false;
     if (x.a != 0) flags |= DSPARK_STATUS_NUMERIC;
     const bool clean = x.a == 0;                                              // no NaN, no infinity but -infinity
     const uint32_t top_bits = static_cast<uint32_t>(x.c >> 32);
@@ -555,6 +580,7 @@ __device__ __forceinline__ void sample_row(const SampleArgs& p, Shared<kThreads>
         __syncthreads();
         const uint32_t mine = s.list_count;
         const Reduced all = exchange(mine, 0, 0, 0);
+        if (!ok) return 0;
         if (all.a <= kList && C > 1) {
             if (rank != 0) {
                 uint32_t before = 0;
@@ -563,6 +589,7 @@ __device__ __forceinline__ void sample_row(const SampleArgs& p, Shared<kThreads>
                     send(remote(&s.list[before + i], 0), s.list[i], remote(&s.bar_list, 0));
             } else {
                 receive(s.bar_list, used_list, 8u * static_cast<uint32_t>(all.a - mine));
+                if (!ok) return 0;
             }
         }
         __syncthreads();
@@ -772,6 +799,7 @@ __device__ __forceinline__ void sample_row(const SampleArgs& p, Shared<kThreads>
         }
         if (rank == 0) {
             if (C > 1) receive(s.bar_hist, used_hist, 4u * static_cast<uint32_t>(x.b - s.red[turn ^ 1][0][1]));
+            if (!ok) return false;
             __syncthreads();
             // the first bin up to which there are k
             u64 c[kPerThread], sum = 0, none = 0;
@@ -788,6 +816,7 @@ __device__ __forceinline__ void sample_row(const SampleArgs& p, Shared<kThreads>
             }
         }
         hear();
+        if (!ok) return false;
         const float reach = static_cast<float>(s.out[0] + 1);
         // a logit that no entry of those parts is below
         const float least = m - reach / scale * (1.0f + 1e-5f) - fabsf(m) * 2.5e-7f;
@@ -840,9 +869,11 @@ __device__ __forceinline__ void sample_row(const SampleArgs& p, Shared<kThreads>
             }
         }
         const int count = gather();
+        if (!ok) return false;
         if (count <= kList) {
             if (rank == 0) settle(count, 0, 0, static_cast<u64>(k), ~0ull);
             settled_on_list();
+            if (!ok) return false;
             settled = true;
         }
     }
@@ -852,6 +883,7 @@ __device__ __forceinline__ void sample_row(const SampleArgs& p, Shared<kThreads>
     auto locate = [&](u64 t, auto value, auto found) {
         if (rank == 0) {
             if (C > 1) receive(s.bar_segment, used_segment, static_cast<uint32_t>(C - 1) * kWarps * 8u);
+            if (!ok) return;
             __syncthreads();
         }
         if (rank == 0 && warp == 0) {
@@ -872,6 +904,7 @@ __device__ __forceinline__ void sample_row(const SampleArgs& p, Shared<kThreads>
             }
         }
         hear();
+        if (!ok) return;
         if (s.out[0] == rank * kWarps + warp) {
             // a lane sums neighbouring pieces of the run; then the lanes share the pieces of the one it is in
             u64 left = s.out[1];
@@ -946,6 +979,7 @@ __device__ __forceinline__ void sample_row(const SampleArgs& p, Shared<kThreads>
             uint32_t hi = top_bits, lo = float_order_bits(lowest);
             for (int i = tid; i < kBins; i += kThreads) s.share[i] = 0u;
             exchange(0, 0, 0, 0);                                             // all blocks' shares are clear
+            if (!ok) return;
             // A level leaves a range of less than half, or the next one halves it: the range is one logit, at the
             // latest, after twice the 32 bits.
             constexpr int kLevels = 72;
@@ -995,6 +1029,7 @@ __device__ __forceinline__ void sample_row(const SampleArgs& p, Shared<kThreads>
                             else atomicAdd(&s.share[i], s.hist[i]);
                         }
                         receive(s.bar_share, used_share, static_cast<uint32_t>((C - 1) * share) * 4u);
+                        if (!ok) return;
                         __syncthreads();
                         for (int i = bin0 + tid; i < bin0 + share; i += kThreads) {
                             if (rank != 0) send32(remote(&s.bins[i], 0), s.share[i], remote(&s.bar_bins, 0));
@@ -1002,6 +1037,7 @@ __device__ __forceinline__ void sample_row(const SampleArgs& p, Shared<kThreads>
                             s.share[i] = 0u;                                  // the next level comes after an exchange
                         }
                         if (rank == 0) receive(s.bar_bins, used_bins, static_cast<uint32_t>(kBins - share) * 4u);
+                        if (!ok) return;
                     } else {
                         for (int i = tid; i < kBins; i += kThreads) s.bins[i] = s.hist[i];
                     }
@@ -1058,6 +1094,7 @@ __device__ __forceinline__ void sample_row(const SampleArgs& p, Shared<kThreads>
                         if (tid == 0) s.out[2] = inside;
                     }
                     hear();
+                    if (!ok) return;
                     first = static_cast<int>(s.out[0]);
                     last = static_cast<int>(s.out[1]);
                     fits = s.out[2] <= kList;
@@ -1116,6 +1153,7 @@ __device__ __forceinline__ void sample_row(const SampleArgs& p, Shared<kThreads>
                 }
                 const u64 own = mass.value();
                 const Reduced y = reduce(own, more, high, low);
+                if (!ok) return;
                 if (halve && (want_count != ~0ull ? above + y.b >= want_count : over + y.a >= want_mass)) {
                     lo = hi - (static_cast<uint32_t>(first) << shift) + 1u;   // it is in the upper half
                     halve = false;
@@ -1126,8 +1164,10 @@ __device__ __forceinline__ void sample_row(const SampleArgs& p, Shared<kThreads>
                 above += y.b;
                 if (fits) {
                     const int count = gather();
+                    if (!ok) return;
                     if (rank == 0) settle(count, above, over, want_count, want_mass);
                     settled_on_list();
+                    if (!ok) return;
                     if (token < 0) {
                         // the runs' sums: the list's kept entries join those above it
                         __syncthreads();
@@ -1170,8 +1210,10 @@ __device__ __forceinline__ void sample_row(const SampleArgs& p, Shared<kThreads>
                         else if (lane < static_cast<uint32_t>(C))
                             send(remote(&s.found, lane), key, remote(&s.bar_found, lane));
                     });
+                    if (!ok) return;
                     if (C > 1) receive(s.bar_found, used_found, 8u);
                     else __syncthreads();
+                    if (!ok) return;
                     cut = s.found;
                     total = over + take * q;
                     return;
@@ -1194,6 +1236,7 @@ __device__ __forceinline__ void sample_row(const SampleArgs& p, Shared<kThreads>
             });
             const u64 own = mass.value();
             total = reduce(own, 0, 0, 0).a;
+            if (!ok) return false;
             run_mass = warp_sum_u64(own);
             const u64 need = max(1ull, share_of(total, P));
             alike = need >= total || (total - need) / entries > 0;
@@ -1218,6 +1261,7 @@ __device__ __forceinline__ void sample_row(const SampleArgs& p, Shared<kThreads>
             });
             const u64 own = mass.value();
             const Reduced all = reduce(own, count, 0, count != 0 ? 0xFFFFFFFFu - float_order_bits(smallest) : 0u);
+            if (!ok) return false;
             lowest = float_from_order_bits(0xFFFFFFFFu - static_cast<uint32_t>(all.d));
             entries = all.b;
             total = all.a;
@@ -1226,6 +1270,7 @@ __device__ __forceinline__ void sample_row(const SampleArgs& p, Shared<kThreads>
         runs_known = true;                                                    // if everything is kept
         if (static_cast<u64>(k) < entries) {
             close_in(static_cast<u64>(k), ~0ull - 1, lowest);
+            if (!ok) return false;
             limit = cut;
             entries = static_cast<u64>(k);
         }
@@ -1238,6 +1283,7 @@ __device__ __forceinline__ void sample_row(const SampleArgs& p, Shared<kThreads>
             token = -1;                                                       // what top-k's list said is not the last word
             in_list = false;
             close_in(~0ull, need, least);
+            if (!ok) return false;
         }
         if (token < 0 && runs_known) report_run(run_mass);
     }
@@ -1264,10 +1310,11 @@ __device__ __forceinline__ void sample_row(const SampleArgs& p, Shared<kThreads>
             report_run(warp_sum_u64(mass.value()));
         }
         locate(share_of(total, U), [&](float l, int v) { return mass_of(kept(l, v)); }, set_token);
+        if (!ok) return false;
     } else if (rank == 0 && warp == 0) {
         set_token(token);
     }
-    if (p.probs == nullptr) return;
+    if (p.probs == nullptr) return true;
     const float norm = 0x1p40f / __ull2float_rn(total);
     float* const probs = p.probs + r * V;
     auto share = [&](float w) { return w >= 0x1p-40f ? w * norm : 0.0f; };    // 0 where the mass is
@@ -1301,6 +1348,7 @@ __device__ __forceinline__ void sample_row(const SampleArgs& p, Shared<kThreads>
             }
         });
     }
+    return true;
 }
 
 template <typename T, int kThreads>
@@ -1310,13 +1358,24 @@ __global__ void __launch_bounds__(kThreads, 1) sample_kernel(const __grid_consta
     T* const held = reinterpret_cast<T*>(smem_raw + sizeof(s));
     grid_dependency_wait();
     int place = static_cast<int>(blockIdx.x) / p.cluster;
+    bool ok;
     while (true) {
-        sample_row(p, s, held, p.queue ? p.order[place] : place);
+        ok = sample_row(p, s, held, p.queue ? p.order[place] : place);
         if (!p.queue) break;
         __syncthreads();
         place = static_cast<int>(s.next);
         __syncthreads();
         if (place >= p.R) break;
+    }
+    if (!ok) {
+        // No block may end while another can still send to it.  One that has received everything has nothing under
+        // way to it; one that gave up stays until all others have ended or come here (the barrier counts threads
+        // that have ended as arrived), and until what they sent before has had time to arrive.
+        asm volatile("barrier.cluster.arrive.relaxed;" ::: "memory");
+        asm volatile("barrier.cluster.wait;" ::: "memory");
+        const long long t0 = global_ns();
+        while (global_ns() - t0 < kUnderWayNs) {
+        }
     }
 }
 
