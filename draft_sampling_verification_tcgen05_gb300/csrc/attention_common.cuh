@@ -10,13 +10,20 @@ namespace dspark {
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.6931471805599453f;
 
+// kHeadroom: how far below a tile's maximum, in log2 units, the softmax puts its reference.  The weights of the
+// product with the values have the values' type, since kind::f16 takes no other.  bf16 has fp32's exponents, so
+// their size does not matter.  fp16 rounds what is below 2^-14 to a fixed step of 2^-24, and the sum of the weights,
+// in fp32, does not: many small weights beside a large one would be lost from the product alone.  With the largest
+// weight at 2^7 (2^15 before the reference follows) that step is 2^-31 of it.
 template <typename T> struct HalfType;
 template <> struct HalfType<__nv_bfloat16> {
     static constexpr uint32_t kMmaFormat = 1;
+    static constexpr float kHeadroom = 0.0f;
     static constexpr CUtensorMapDataType kMapType = CU_TENSOR_MAP_DATA_TYPE_BFLOAT16;
 };
 template <> struct HalfType<__half> {
     static constexpr uint32_t kMmaFormat = 0;
+    static constexpr float kHeadroom = 7.0f;
     static constexpr CUtensorMapDataType kMapType = CU_TENSOR_MAP_DATA_TYPE_FLOAT16;
 };
 

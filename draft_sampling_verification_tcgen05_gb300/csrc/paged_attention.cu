@@ -28,7 +28,7 @@
 //
 // The running maximum is raised only when a tile exceeds it by 2^8 (O, in tensor memory, is then
 // rescaled): weights up to 2^8 lose nothing in a floating type, and the rescaling leaves the
-// common path.
+// common path.  In fp16 the exponentials' reference is 2^7 below it (kHeadroom).
 //
 // A row must not see what lies outside its limit, but 0 * infinity is not 0.  Values past the
 // request's end are zeroed in shared memory before the product (by the warp that issues it, while
@@ -590,7 +590,8 @@ paged_attention_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_con
                     }
                     const float most = falling ? fminf(fminf(lo[0], lo[1]), fminf(lo[2], lo[3]))
                                                : fmaxf(fmaxf(hi[0], hi[1]), fmaxf(hi[2], hi[3]));
-                    const float mt = most == none ? -INFINITY : most * sl2;       // NaN scores leave no maximum behind
+                    // NaN scores leave no maximum behind
+                    const float mt = most == none ? -INFINITY : most * sl2 - HalfType<T>::kHeadroom;
                     if (t == g.t0) {
                         m2 = mt;
                     } else {

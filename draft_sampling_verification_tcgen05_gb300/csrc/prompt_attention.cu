@@ -14,7 +14,8 @@
 //                    tensor memory; P replaces half of S)
 //
 // The running maximum is raised only when a tile exceeds it by 2^8 (O is then rescaled): weights up to
-// 2^8 lose nothing in a floating type, and the rescaling leaves the common path.
+// 2^8 lose nothing in a floating type, and the rescaling leaves the common path.  In fp16 the exponentials'
+// reference is 2^7 below it (kHeadroom).
 //
 // A row must not see what lies outside its limit, but 0 * infinity is not 0.  Values past the
 // sequence's end are zeroed in shared memory before the product.  A query tile whose result is not
@@ -506,7 +507,7 @@ prompt_attention_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_co
                 }
                 const float top = falling ? fminf(fminf(best[0], best[1]), fminf(best[2], best[3]))
                                           : fmaxf(fmaxf(best[0], best[1]), fmaxf(best[2], best[3]));
-                float mt = top == none ? -INFINITY : top * sl2;
+                float mt = top == none ? -INFINITY : top * sl2 - HalfType<T>::kHeadroom;
                 // The two threads of a row meet: P may then replace the scores, and if either finds the maximum
                 // too low (or has given up) they exchange theirs.
                 bool raise = t == 0 || !go || (valid && mt > m2 + kRaise);
