@@ -10,6 +10,7 @@ in the library's CUDA kernels; there is no fallback of any kind -- if
 from __future__ import annotations
 
 import ctypes
+import functools
 import os
 
 __all__ = [
@@ -165,6 +166,25 @@ def _ws(ws, op, B=0, N=0, V=0, r=0, device=None):
     return ws if ws is not None else Workspace(op, B, N, V, r, device)
 
 
+def _on_its_stream(f):
+    """Runs f with the stream that it is given (its last argument) as the current one.  The outputs and the workspace
+    that it allocates then belong to that stream; memory of the current stream would be free for that one's work,
+    the workspace's as soon as f returns, while the other stream still uses it."""
+    count = f.__code__.co_argcount
+
+    @functools.wraps(f)
+    def call(*args, **kw):
+        stream = args[-1] if len(args) == count else kw.get("stream")
+        if stream is None:
+            return f(*args, **kw)
+        cuda = _torch().cuda
+        with cuda.stream(stream if isinstance(stream, cuda.Stream) else cuda.ExternalStream(stream.cuda_stream)):
+            return f(*args, **kw)
+
+    return call
+
+
+@_on_its_stream
 def dspark_draft_logits(hidden, lm_head, logits=None, workspace=None, stream=None):
     """logits[m, v] = sum_h hidden[m, h] * lm_head[v, h]  (hidden [M,H], lm_head [V,H]; bf16 or fp32)."""
     torch = _torch()
@@ -184,6 +204,7 @@ def dspark_draft_logits(hidden, lm_head, logits=None, workspace=None, stream=Non
     return logits
 
 
+@_on_its_stream
 def dspark_markov_sample(base_logits, anchor, w1, w2, temperature, seed: int, offset: int,
                          draft_tokens=None, lse=None, workspace=None, stream=None):
     """Sequential Markov-biased Gumbel-max sampling; returns draft_tokens [B, N] int32.
@@ -216,6 +237,7 @@ def dspark_markov_sample(base_logits, anchor, w1, w2, temperature, seed: int, of
     return draft_tokens
 
 
+@_on_its_stream
 def dspark_markov_sample_conf(base_logits, anchor, w1, w2, temperature, seed: int, offset: int, hidden, w_h, w_e,
                               beta: float, tau, draft_tokens=None, conf=None, lse=None, workspace=None, stream=None):
     """dspark_markov_sample with the calibrated confidence head evaluated at every step; returns
@@ -255,6 +277,7 @@ def dspark_markov_sample_conf(base_logits, anchor, w1, w2, temperature, seed: in
     return draft_tokens, conf
 
 
+@_on_its_stream
 def dspark_markov_sample_reduced(base_logits, anchor, w1, w2, temperature, seed: int, offset: int, d2t,
                                  mode: int, V_target: int, draft_tokens=None, lse=None, workspace=None,
                                  stream=None):
@@ -282,6 +305,7 @@ def dspark_markov_sample_reduced(base_logits, anchor, w1, w2, temperature, seed:
     return draft_tokens
 
 
+@_on_its_stream
 def dspark_verify(p_target, p_draft, draft_tokens, lengths, seed: int, offset: int,
                   out_tokens=None, num_accepted=None, workspace=None, stream=None):
     """Lossless rejection-sampling verification; returns (out_tokens [B, gamma+1], num_accepted [B])."""
@@ -305,6 +329,7 @@ def dspark_verify(p_target, p_draft, draft_tokens, lengths, seed: int, offset: i
     return out_tokens, num_accepted
 
 
+@_on_its_stream
 def dspark_verify_gumbel(target_logits, temperature, draft_tokens, lengths, seed: int, offset: int,
                          out_tokens=None, num_accepted=None, workspace=None, stream=None):
     """Verification with the draft's Gumbel noise (the draft sampler's seed and offset); returns
@@ -331,6 +356,7 @@ def dspark_verify_gumbel(target_logits, temperature, draft_tokens, lengths, seed
     return out_tokens, num_accepted
 
 
+@_on_its_stream
 def dspark_verify_greedy(target, draft_tokens, lengths=None, out_tokens=None, num_accepted=None,
                          workspace=None, stream=None):
     """Greedy (temperature-0) verification; returns (out_tokens [B, gamma+1], num_accepted [B])."""
@@ -354,6 +380,7 @@ def dspark_verify_greedy(target, draft_tokens, lengths=None, out_tokens=None, nu
     return out_tokens, num_accepted
 
 
+@_on_its_stream
 def dspark_verify_logits(target_logits, target_temperature, base_logits, anchor, w1, w2, draft_temperature,
                          draft_lse, draft_tokens, lengths, seed: int, offset: int, out_tokens=None,
                          num_accepted=None, workspace=None, stream=None):
@@ -391,6 +418,7 @@ def dspark_verify_logits(target_logits, target_temperature, base_logits, anchor,
     return out_tokens, num_accepted
 
 
+@_on_its_stream
 def dspark_confidence(hidden, w1, anchor, draft_tokens, w_h, w_e, beta: float, tau, conf=None,
                       workspace=None, stream=None):
     """Calibrated confidence head; returns conf [B, N] (the scheduler's cond_accept)."""
@@ -417,6 +445,7 @@ def dspark_confidence(hidden, w1, anchor, draft_tokens, w_h, w_e, beta: float, t
     return conf
 
 
+@_on_its_stream
 def dspark_schedule(cond_accept, sps, K_in: int, survival=None, K_out=None, lengths=None,
                     selected=None, workspace=None, stream=None):
     """Confidence-scheduled admission; returns (survival, K_out [1], lengths [B], selected [B*N])."""
@@ -471,6 +500,7 @@ def _rows(t, name, dtype, D):
     return token if T > 1 else H * D
 
 
+@_on_its_stream
 def dspark_kv_append(q, k, v, positions, slots, cos_sin, k_cache, v_cache, interleaved: bool = False, q_norm=None,
                      k_norm=None, eps: float = 1e-6, q_out=None, workspace=None, stream=None):
     """Writes k and v [T, Hkv, D] of new tokens to their slots of a paged cache, the keys (and the queries
@@ -521,6 +551,7 @@ def dspark_kv_append(q, k, v, positions, slots, cos_sin, k_cache, v_cache, inter
     return q_out
 
 
+@_on_its_stream
 def dspark_paged_attention(q, k_cache, v_cache, block_table, kv_len, scale: float, lengths=None, causal: bool = True,
                            out=None, lse=None, workspace=None, stream=None):
     """Attention of a window of N new tokens per request, q [B, N, Hq, D], over a paged cache
@@ -562,6 +593,7 @@ def dspark_paged_attention(q, k_cache, v_cache, block_table, kv_len, scale: floa
     return out
 
 
+@_on_its_stream
 def dspark_prompt_attention(q, k, v, cu_seqlens, scale: float, causal: bool = True, out=None, lse=None,
                             workspace=None, stream=None):
     """Attention within packed prompts: q [T, Hq, D], k / v [T, Hkv, D] (any token stride), sequence b the
@@ -594,6 +626,7 @@ def dspark_prompt_attention(q, k, v, cu_seqlens, scale: float, causal: bool = Tr
     return out
 
 
+@_on_its_stream
 def dspark_sample(logits, temperature, top_k, top_p, min_p, u, tokens=None, probs=None, workspace=None, stream=None):
     """Sampling with temperature, top-k, min-p and top-p from the given uniforms u [R]; returns tokens [R] int32.
 
