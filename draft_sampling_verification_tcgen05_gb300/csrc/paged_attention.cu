@@ -39,9 +39,9 @@
 //
 // Bound by the cache's bytes where they are many: 5 requests over 70000 to 131071 tokens, 8 key heads of
 // 128 (1.83 GB), take 268 us, the copy's 6.8 TB/s; 64 windows of 17 tokens over 100 to 8000 (629 MB)
-// 119 us, 5.3 TB/s, where a tile's softmax over 68 rows (two copies do not fit) is nearly as long as
-// its loads.  200 blocks of 8 tokens over 9 to 2000 (85 MB, D = 64) take 34 us: a unit of three tiles
-// is bound by its way through the products and the softmax.  One token over 4097 takes 18.5 us, most of
+// 118 us, 5.3 TB/s, where a tile's softmax over 68 rows (two copies do not fit) is nearly as long as
+// its loads.  200 blocks of 8 tokens over 9 to 2000 (85 MB, D = 64) take 31 us: a unit of three tiles
+// is bound by its way through the products and the softmax.  One token over 4097 takes 14.5 us, most of
 // it the three kernels' starts and the chain from the plan to the join.
 #include "attention_common.cuh"
 #include "host_common.h"

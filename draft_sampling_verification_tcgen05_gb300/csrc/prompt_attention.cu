@@ -24,13 +24,13 @@
 // bit as without them.
 //
 // Meant to be bound by the tensor cores: a key tile's products of both query tiles take 2048 cycles (D = 128,
-// 64 for each of 32 instructions).  8192 tokens of 32 heads of 128 on 8, causal, take 371 us: 1.48 PFLOP/s,
-// 0.78 of what a large product reaches, 3000 cycles a key tile.  What is left is a chain: with D = 128 the
-// two S and O fill tensor memory, so a tile's next S waits for its own P (768 cycles of products), and its
-// softmax (about 1500 cycles, half of them the exponential's unit) for S.  Measured on the way: a thread per row
-// 522 us with a warp issuing for each query tile (they ran in step), 416 us with one warp issuing for both;
-// two threads per row 416 us; the tiles taking turns, waits ahead of the turn and out of line 372 us.  Starting
-// the second tile half a step late, and with D = 64 a P apart from S, made no difference.
+// 64 for each of 32 instructions).  8192 tokens of 32 heads of 128 on 8, causal, take 371 us (385 us in a long run,
+// where the clock is lower): 1.48 PFLOP/s, 0.78 of what a large product reaches, 3000 cycles a key tile.  What is
+// left is a chain: with D = 128 the two S and O fill tensor memory, so a tile's next S waits for its own P (768
+// cycles of products), and its softmax (about 1500 cycles, half of them the exponential's unit) for S.  Measured on
+// the way: a thread per row 522 us with a warp issuing for each query tile (they ran in step), 416 us with one warp
+// issuing for both; two threads per row 416 us; the tiles taking turns, waits ahead of the turn and out of line
+// 372 us.  Starting the second tile half a step late, and with D = 64 a P apart from S, made no difference.
 #include "attention_common.cuh"
 #include "host_common.h"
 

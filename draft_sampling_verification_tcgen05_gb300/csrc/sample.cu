@@ -32,7 +32,7 @@
 // greedy one.  Rows in their order 443 us, the longest first 366 us, from a queue 332 us, lean passes where neither
 // top-k nor min-p is set 314 us (with the sum above the cut and its list in passes of their own 326 us), packed
 // arithmetic 307 us, a list from the parts that reach it 303 us; two blocks of half the threads per SM 446 us (the
-// rows under way no longer fit the L2 cache).  One row takes 12.5 us, a chain of exchanges.
+// rows under way no longer fit the L2 cache).  One row takes 11 us, a chain of exchanges.
 #include "attention_common.cuh"
 #include "device_common.cuh"
 #include "half_common.cuh"
@@ -1412,7 +1412,10 @@ cudaError_t launch_blocks(SampleArgs p, cudaStream_t stream, const DeviceInfo& d
 
 template <typename T>
 cudaError_t launch_typed(SampleArgs p, cudaStream_t stream, const DeviceInfo& dev) {
-    // Blocks per row: as many as give every SM one, while a block keeps kMinSlice entries.
+    // Blocks per row: doubled until every SM has one, while a block keeps kMinSlice entries.  That may end at up to
+    // twice the SMs, which costs a second round of blocks and still wins with long rows: 39 rows of 151936 take 72 us
+    // on 4 blocks each and 107 us on 2, 77 rows 109 us on 2 and 166 us on 1 (86 us on 4), 120 rows 123 and 169 us.
+    // Where it does not: 72 rows of 32000 on 4 blocks 49 us, on 2 39 us; 150 rows of 151936 on 2 114 us, on 1 107 us.
     constexpr int kMinSlice = 4096;
     auto slice_of = [&](int blocks) { return ((p.V + blocks - 1) / blocks + 7) / 8 * 8; };
     int c = 1;
@@ -1421,8 +1424,8 @@ cudaError_t launch_typed(SampleArgs p, cudaStream_t stream, const DeviceInfo& de
     p.queue = c == 1 && p.R > dev.sm_count ? 1 : 0;
     p.slice = slice_of(c);
     // Half the threads meet sooner at their barriers; with long parts the passes count, which want them all.
-    // 512 against 1024 threads: parts of 9496 entries 11.0 and 14.3 us (one row), of 16000 48 and 52 us (72
-    // rows), of 37984 both 72 us (36 rows), of 75968 103 and 97 us (72 rows).
+    // 512 against 1024 threads: parts of 9496 entries 11 and 15 us (one row), of 16000 38 and 42 us (76 rows), of
+    // 35000 58 and 61 us (100 rows), of 37984 76 and 72 us (38 rows), of 75968 133 and 109 us (76 rows).
     constexpr int kShortSlice = 32768;
     return p.slice <= kShortSlice ? launch_blocks<T, 512>(p, stream, dev) : launch_blocks<T, 1024>(p, stream, dev);
 }

@@ -84,7 +84,7 @@ typedef enum {
     DSPARK_OP_VERIFY_LOGITS = 6,
     DSPARK_OP_VERIFY_GUMBEL = 7,
     DSPARK_OP_KV_APPEND = 8,
-    /* 9 is no operation */
+    /* 9: unused */
     DSPARK_OP_PAGED_ATTENTION = 10,
     DSPARK_OP_PROMPT_ATTENTION = 11,
     DSPARK_OP_SAMPLE = 12
@@ -123,7 +123,7 @@ typedef enum {
  *   DSPARK_OP_VERIFY_LOGITS grows with B*V/2048 (normaliser partials); N = gamma
  *   DSPARK_OP_VERIFY_GUMBEL grows with B*(N+1) (row keys); N = gamma
  *   DSPARK_OP_KV_APPEND     256 (the status word)
- *   DSPARK_OP_PAGED_ATTENTION  partial results of split requests and their counters;
+ *   DSPARK_OP_PAGED_ATTENTION  the plan and the partial results of split requests;
  *                           B, N as the call's, V = Hq, r = D
  *   DSPARK_OP_PROMPT_ATTENTION  the list of its work items; B as the call's, N = T, V = Hq
  *   DSPARK_OP_SAMPLE        grows with B (the rows' order); B = R, N = 1
@@ -575,7 +575,9 @@ DSPARK_API dspark_status dspark_kv_append(const void* q, const void* k, const vo
  * gives out 0 and lse -infinity.  Values in the cache that a row does not see do not reach its
  * output, infinities and NaN among them.
  * Scores, statistics and sums are fp32; the weights exp(s_j - max) are rounded to dtype for their
- * product with v.
+ * product with v (fp16: scaled up, so that the rounding is at most 2^-32 of the row's largest weight
+ * or 2^-11 of the weight itself).  An infinite value that a row sees with a weight that rounds to 0
+ * gives NaN.
  *
  *   q            [B, N, Hq, D] dtype (bf16 or fp16), device
  *   k_cache, v_cache  [num_pages, Hkv, page, D] dtype, device
@@ -583,7 +585,7 @@ DSPARK_API dspark_status dspark_kv_append(const void* q, const void* k, const vo
  *                block_table[b, j / page]; entries past a request's pages are not read
  *   kv_len       [B] int32 in [0, max_pages * page], device
  *   lengths      [B] int32 in [0, N], device, or NULL (= N)
- *   out          [B, N, Hq, D] dtype output
+ *   out          [B, N, Hq, D] dtype output; does not overlap q or the caches
  *   lse          [B, N, Hq] fp32 output, or NULL
  * Requirements: B, N >= 1, B <= 65535, N <= 65535, Hkv >= 1, Hq a multiple of Hkv with
  * Hq / Hkv <= 128, D 64 or 128, page a power of two from 8 to 256, max_pages * page <= 2^30,
@@ -612,7 +614,7 @@ DSPARK_API dspark_status dspark_paged_attention(const void* q, const void* k_cac
  *                q_stride, k_stride, v_stride elements apart (views of a fused projection), heads
  *                and values contiguous
  *   cu_seqlens   [B + 1] int32, device, non-decreasing in [0, T]
- *   out          [T, Hq, D] dtype output, contiguous
+ *   out          [T, Hq, D] dtype output, contiguous; does not overlap q, k or v
  *   lse          [T, Hq] fp32 output, or NULL
  * Requirements: B, T >= 1, B <= 65535, T <= 2^24, Hkv >= 1, Hq a multiple of Hkv with
  * Hq / Hkv <= 128, D 64 or 128, scale finite; q, k, v, out 16-byte aligned, strides multiples of
@@ -647,7 +649,7 @@ DSPARK_API dspark_status dspark_prompt_attention(const void* q, const void* k, c
  *   temperature  [R] fp32 >= 0;  top_k [R] int32;  top_p [R] fp32 in [0, 1];
  *   min_p        [R] fp32 in [0, 1];  u [R] fp32 in [0, 1), device
  *   tokens       [R] int32 output
- *   probs        [R, V] fp32 output, or NULL
+ *   probs        [R, V] fp32 output, or NULL; does not overlap logits
  * Requirements: R >= 1, 1 <= V <= 2^21; logits and probs 16-byte aligned.
  * Device-side: entries that are -infinity are masked (weight 0); NaN and +infinity are skipped and
  * set NUMERIC; a row without a finite entry gives token 0, probs 0 and NUMERIC.  A negative or
