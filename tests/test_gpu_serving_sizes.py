@@ -69,3 +69,38 @@ def test_long_windows_over_a_prefix(cuda_lib, N, G, D, dtype):
     case = PagedCase(len(lens), N, 2 * G, 2, D, 32, lens, dtype, seed=N)
     for causal in (True, False):
         case.check(cuda_lib, lengths=lengths, causal=causal, rows=250)
+
+
+def test_prompt_offsets_past_32_bits(cuda_lib):
+    """Queries and outputs of more than 2^31 values: the last sequence as in a call of its own."""
+    import torch
+    Hq, D, n, B = 128, 128, 70, 2000
+    T = B * n
+    assert T * Hq * D > 1 << 31
+    q = torch.zeros(T, Hq, D, dtype=torch.bfloat16, device="cuda")
+    k, v = (torch.zeros(T, 1, D, dtype=torch.bfloat16, device="cuda") for _ in range(2))
+    small = _inputs(n, Hq, 1, D, "bf16", 1, fused=False)
+    for whole, part in zip((q, k, v), small):
+        whole[-n:] = part
+    cu = torch.arange(0, T + 1, n, dtype=torch.int32, device="cuda")
+    lse, want_lse = torch.empty(T, Hq, device="cuda"), torch.empty(n, Hq, device="cuda")
+    out = cuda_lib.dspark_prompt_attention(q, k, v, cu, D ** -0.5, lse=lse)
+    want = cuda_lib.dspark_prompt_attention(*small, cu[:2].contiguous(), D ** -0.5, lse=want_lse)
+    assert torch.equal(out[-n:], want) and torch.equal(lse[-n:], want_lse)
+    assert not out[:-n].any()
+
+
+def test_sampling_offsets_past_32_bits(cuda_lib):
+    """More than 2^31 logits and probabilities: the last rows as in a call of their own."""
+    import torch
+    R, V, last = 14200, 151936, 20
+    assert R * V > 1 << 31
+    rng = np.random.default_rng(5)
+    small = Rows(_normal(last, V, 5), *_settings(rng, last))
+    want, want_probs = small.run(cuda_lib)
+    big = Rows(torch.zeros(R, V, device="cuda"), np.zeros(R), np.zeros(R, int), np.ones(R), np.zeros(R), np.zeros(R))
+    for name in ("logits", "T", "k", "p", "mp", "u"):
+        getattr(big, name)[-last:] = getattr(small, name)
+    tok, probs = big.run(cuda_lib)
+    assert torch.equal(tok[-last:], want) and torch.equal(probs[-last:], want_probs)
+    assert not tok[:-last].any() and bool((probs[:-last, 0] == 1).all())
