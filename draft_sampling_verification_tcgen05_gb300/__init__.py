@@ -22,6 +22,9 @@ __all__ = [
     "dspark_verify", "dspark_schedule", "dspark_read_status", "dspark_status_string",
     "OP_KV_APPEND", "OP_PAGED_ATTENTION", "OP_PROMPT_ATTENTION", "OP_SAMPLE",
     "dspark_kv_append", "dspark_paged_attention", "dspark_prompt_attention", "dspark_sample",
+    "OP_TREE_ATTENTION", "OP_WINDOW_ATTENTION", "OP_VERIFY_TREE", "OP_KV_COMPACT", "OP_KV_COPY_PAGES",
+    "dspark_tree_attention", "dspark_window_attention", "dspark_verify_tree", "dspark_verify_tree_tokens",
+    "dspark_kv_compact", "dspark_kv_copy_pages",
     "dspark_selftest_wait_timeout", "STATUS_TIMEOUT", "STATUS_NUMERIC", "STATUS_INPUT_RANGE",
     "STATUS_INTERNAL", "STATUS_INDEX",
 ]
@@ -34,6 +37,7 @@ OP_DRAFT_LOGITS, OP_MARKOV_SAMPLE, OP_VERIFY, OP_SCHEDULE, OP_VERIFY_GREEDY, OP_
 OP_VERIFY_LOGITS = 6
 OP_VERIFY_GUMBEL = 7
 OP_KV_APPEND, OP_PAGED_ATTENTION, OP_PROMPT_ATTENTION, OP_SAMPLE = 8, 10, 11, 12
+OP_TREE_ATTENTION, OP_WINDOW_ATTENTION, OP_VERIFY_TREE, OP_KV_COMPACT, OP_KV_COPY_PAGES = 13, 14, 15, 16, 17
 F32, BF16, F16 = 0, 1, 2
 D2T_INDEX, D2T_OFFSET = 0, 1
 OK, ERR_INVALID_ARG, ERR_UNSUPPORTED, ERR_CUDA, ERR_TIMEOUT, ERR_NUMERIC, ERR_INPUT_RANGE = range(7)
@@ -83,6 +87,14 @@ def lib() -> ctypes.CDLL:
     L.dspark_prompt_attention.argtypes = [vp, vp, vp, i32, i64, i64, i64, vp, f32, i32, i32, i32, i32, i32, i32,
                                           vp, vp, vp, sz, vp]
     L.dspark_sample.argtypes = [vp, i32, vp, vp, vp, vp, vp, i32, i32, vp, vp, vp, sz, vp]
+    L.dspark_window_attention.argtypes = [vp, vp, vp, i32, vp, i32, vp, vp, i32, i32, f32, i32, i32, i32, i32, i32, i32, i32, i32,
+                                          vp, vp, vp, sz, vp]
+    L.dspark_tree_attention.argtypes = [vp, vp, vp, i32, vp, i32, vp, vp, vp, i32, i32, f32, i32, i32, i32, i32, i32, i32, i32,
+                                        vp, vp, vp, sz, vp]
+    L.dspark_verify_tree.argtypes = [vp, i32, vp, vp, vp, vp, vp, i32, i32, i32, vp, vp, vp, vp, sz, vp]
+    L.dspark_verify_tree_tokens.argtypes = [vp, vp, vp, vp, i32, i32, vp, vp, vp, vp, sz, vp]
+    L.dspark_kv_compact.argtypes = [vp, vp, i32, i64, vp, i32, vp, vp, vp, vp, i32, i32, i32, i32, i32, i32, vp, vp, sz, vp]
+    L.dspark_kv_copy_pages.argtypes = [vp, vp, i32, i64, vp, vp, vp, i32, i32, i32, i32, i32, vp, sz, vp]
     L.dspark_read_status.argtypes = [vp, u32p, vp]
     L.dspark_status_string.argtypes = [i32]
     L.dspark_status_string.restype = ctypes.c_char_p
@@ -91,6 +103,8 @@ def lib() -> ctypes.CDLL:
     L.dspark_selftest_wait_timeout.argtypes = [vp, sz, ctypes.c_longlong, vp]
     for f in ("dspark_draft_logits", "dspark_markov_sample", "dspark_verify", "dspark_schedule",
               "dspark_kv_append", "dspark_paged_attention", "dspark_prompt_attention", "dspark_sample",
+              "dspark_tree_attention", "dspark_window_attention", "dspark_verify_tree", "dspark_verify_tree_tokens",
+              "dspark_kv_compact", "dspark_kv_copy_pages",
               "dspark_read_status", "dspark_selftest_wait_timeout"):
         getattr(L, f).restype = i32
     _lib = L
@@ -551,16 +565,8 @@ def dspark_kv_append(q, k, v, positions, slots, cos_sin, k_cache, v_cache, inter
     return q_out
 
 
-@_on_its_stream
-def dspark_paged_attention(q, k_cache, v_cache, block_table, kv_len, scale: float, lengths=None, causal: bool = True,
-                           out=None, lse=None, workspace=None, stream=None):
-    """Attention of a window of N new tokens per request, q [B, N, Hq, D], over a paged cache
-    [num_pages, Hkv, page_size, D] that holds them already; returns out [B, N, Hq, D].
-
-    block_table [B, max_pages], kv_len [B] (cached tokens, the window's among them), lengths [B] (the
-    window's tokens, or None for N) int32.  Pass an fp32 [B, N, Hq] tensor as `lse` to receive the
-    log-sum-exp of each row's scores.
-    """
+def _paged(q, k_cache, v_cache, block_table, kv_len, lengths, out, lse):
+    """Checks what the attentions over a paged cache take; returns (dtype code, out)."""
     torch = _torch()
     dt = _half(q, "q")
     _need(q, "q", (q.dtype,), 4)
@@ -569,8 +575,7 @@ def dspark_paged_attention(q, k_cache, v_cache, block_table, kv_len, scale: floa
     _need(block_table, "block_table", (torch.int32,), 2)
     _need(kv_len, "kv_len", (torch.int32,), 1)
     B, N, Hq, D = q.shape
-    num_pages, Hkv, page, Dc = k_cache.shape
-    if Dc != D or v_cache.shape != k_cache.shape or block_table.shape[0] != B or kv_len.shape[0] != B:
+    if k_cache.shape[3] != D or v_cache.shape != k_cache.shape or block_table.shape[0] != B or kv_len.shape[0] != B:
         raise ValueError("shapes: q [B, N, Hq, D], caches [num_pages, Hkv, page_size, D], block_table [B, max_pages], "
                          "kv_len [B]")
     if lengths is not None:
@@ -585,6 +590,22 @@ def dspark_paged_attention(q, k_cache, v_cache, block_table, kv_len, scale: floa
         _need(lse, "lse", (torch.float32,), 3)
     if out.shape != q.shape or (lse is not None and lse.shape != (B, N, Hq)):
         raise ValueError("out must be [B, N, Hq, D] and lse [B, N, Hq]")
+    return dt, out
+
+
+@_on_its_stream
+def dspark_paged_attention(q, k_cache, v_cache, block_table, kv_len, scale: float, lengths=None, causal: bool = True,
+                           out=None, lse=None, workspace=None, stream=None):
+    """Attention of a window of N new tokens per request, q [B, N, Hq, D], over a paged cache
+    [num_pages, Hkv, page_size, D] that holds them already; returns out [B, N, Hq, D].
+
+    block_table [B, max_pages], kv_len [B] (cached tokens, the window's among them), lengths [B] (the
+    window's tokens, or None for N) int32.  Pass an fp32 [B, N, Hq] tensor as `lse` to receive the
+    log-sum-exp of each row's scores.
+    """
+    dt, out = _paged(q, k_cache, v_cache, block_table, kv_len, lengths, out, lse)
+    B, N, Hq, D = q.shape
+    num_pages, Hkv, page, _ = k_cache.shape
     ws = workspace if workspace is not None else Workspace(OP_PAGED_ATTENTION, B, N, Hq, D, q.device)
     _check(lib().dspark_paged_attention(_ptr(q), _ptr(k_cache), _ptr(v_cache), dt, _ptr(block_table),
                                         block_table.shape[1], _ptr(kv_len), _ptr(lengths), scale, int(causal), B, N,
@@ -655,6 +676,191 @@ def dspark_sample(logits, temperature, top_k, top_p, min_p, u, tokens=None, prob
                                _ptr(u), R, V, _ptr(tokens), _ptr(probs), ws.address, ws.nbytes, _stream(stream)),
            "dspark_sample")
     return tokens
+
+
+@_on_its_stream
+def dspark_window_attention(q, k_cache, v_cache, block_table, kv_len, window: int, sinks: int, scale: float, lengths=None,
+                            causal: bool = True, out=None, lse=None, workspace=None, stream=None):
+    """dspark_paged_attention with a sliding window: the row at position p sees the first `sinks` tokens of its
+    request and those after p - window (up to itself with `causal`)."""
+    dt, out = _paged(q, k_cache, v_cache, block_table, kv_len, lengths, out, lse)
+    B, N, Hq, D = q.shape
+    num_pages, Hkv, page, _ = k_cache.shape
+    ws = workspace if workspace is not None else Workspace(OP_WINDOW_ATTENTION, B, N, Hq, D, q.device)
+    _check(lib().dspark_window_attention(_ptr(q), _ptr(k_cache), _ptr(v_cache), dt, _ptr(block_table), block_table.shape[1],
+                                         _ptr(kv_len), _ptr(lengths), window, sinks, scale, int(causal), B, N, Hq, Hkv, D,
+                                         num_pages, page, _ptr(out), _ptr(lse), ws.address, ws.nbytes, _stream(stream)),
+           "dspark_window_attention")
+    return out
+
+
+@_on_its_stream
+def dspark_tree_attention(q, k_cache, v_cache, block_table, kv_len, parents, scale: float, lengths=None, window: int = 0,
+                          sinks: int = 0, out=None, lse=None, workspace=None, stream=None):
+    """Attention of a tree of N new tokens per request, q [B, N, Hq, D], over a paged cache that holds them already as
+    each request's last tokens; returns out [B, N, Hq, D].
+
+    parents [B, N] int32: the node that a node follows, before it in the order, or -1.  A row sees the tokens before
+    the tree (with a window the first `sinks` of them and those after its position - window), its ancestors and itself.
+    The other arguments are dspark_paged_attention's.
+    """
+    dt, out = _paged(q, k_cache, v_cache, block_table, kv_len, lengths, out, lse)
+    B, N, Hq, D = q.shape
+    num_pages, Hkv, page, _ = k_cache.shape
+    _need(parents, "parents", (_torch().int32,), 2)
+    if parents.shape != (B, N):
+        raise ValueError("parents must be [B, N]")
+    ws = workspace if workspace is not None else Workspace(OP_TREE_ATTENTION, B, N, Hq, D, q.device)
+    _check(lib().dspark_tree_attention(_ptr(q), _ptr(k_cache), _ptr(v_cache), dt, _ptr(block_table), block_table.shape[1],
+                                       _ptr(kv_len), _ptr(lengths), _ptr(parents), window, sinks, scale, B, N, Hq, Hkv, D,
+                                       num_pages, page, _ptr(out), _ptr(lse), ws.address, ws.nbytes, _stream(stream)),
+           "dspark_tree_attention")
+    return out
+
+
+def _tree(parents, draft_tokens, lengths, out_tokens, num_accepted, path):
+    """Checks a tree and its outputs; returns (out_tokens, num_accepted, path)."""
+    torch = _torch()
+    i32 = (torch.int32,)
+    _need(draft_tokens, "draft_tokens", i32, 2)
+    _need(parents, "parents", i32, 2)
+    B, N = draft_tokens.shape
+    if parents.shape != (B, N):
+        raise ValueError("parents and draft_tokens must be [B, N]")
+    if lengths is not None:
+        _need(lengths, "lengths", i32, 1)
+        if len(lengths) != B:
+            raise ValueError("lengths must be [B]")
+    out = []
+    for t, name, shape in ((out_tokens, "out_tokens", (B, N)), (num_accepted, "num_accepted", (B,)), (path, "path", (B, N))):
+        if t is None:
+            t = torch.empty(shape, dtype=torch.int32, device=draft_tokens.device)
+        else:
+            _need(t, name, i32, len(shape))
+            if t.shape != shape:
+                raise ValueError(f"{name} must be {list(shape)}")
+        out.append(t)
+    return out
+
+
+@_on_its_stream
+def dspark_verify_tree(target, parents, draft_tokens, temperature=None, u=None, lengths=None, out_tokens=None, num_accepted=None,
+                       path=None, workspace=None, stream=None):
+    """Verification of a drafted tree from the target's logits [B, N, V] (fp32 or bf16; row i scores what follows node
+    i); returns (out_tokens [B, N], num_accepted [B], path [B, N]), padded with -1.
+
+    parents, draft_tokens [B, N] int32: node 0 is the root, the last token accepted before.  temperature [B] fp32
+    (None: greedy) with the uniforms u [B, N] fp32 of the nodes' draws; lengths [B] int32: the nodes of each request.
+    path lists the nodes that stay (the root, then the accepted ones), dspark_kv_compact's argument.
+    """
+    torch = _torch()
+    _need(target, "target", (torch.float32, torch.bfloat16), 3)
+    outs = _tree(parents, draft_tokens, lengths, out_tokens, num_accepted, path)
+    B, N, V = target.shape
+    if draft_tokens.shape != (B, N):
+        raise ValueError("shapes: target [B, N, V], parents / draft_tokens [B, N]")
+    if temperature is not None:
+        _need(temperature, "temperature", (torch.float32,), 1)
+        if u is None:
+            raise ValueError("temperatures need the uniforms u [B, N]")
+        _need(u, "u", (torch.float32,), 2)
+        if len(temperature) != B or u.shape != (B, N):
+            raise ValueError("temperature must be [B] and u [B, N]")
+    ws = workspace if workspace is not None else Workspace(OP_VERIFY_TREE, B, N, device=target.device)
+    _check(lib().dspark_verify_tree(_ptr(target), _dt(target), _ptr(temperature), _ptr(u), _ptr(parents), _ptr(draft_tokens),
+                                    _ptr(lengths), B, N, V, _ptr(outs[0]), _ptr(outs[1]), _ptr(outs[2]), ws.address, ws.nbytes,
+                                    _stream(stream)), "dspark_verify_tree")
+    return tuple(outs)
+
+
+@_on_its_stream
+def dspark_verify_tree_tokens(target_tokens, parents, draft_tokens, lengths=None, out_tokens=None, num_accepted=None, path=None,
+                              workspace=None, stream=None):
+    """dspark_verify_tree with the target's token behind every node given: target_tokens [B, N] int32 (dspark_sample's
+    output for the nodes' rows, where requests bring top-k, top-p or min-p)."""
+    _need(target_tokens, "target_tokens", (_torch().int32,), 2)
+    outs = _tree(parents, draft_tokens, lengths, out_tokens, num_accepted, path)
+    B, N = target_tokens.shape
+    if draft_tokens.shape != (B, N):
+        raise ValueError("shapes: target_tokens / parents / draft_tokens [B, N]")
+    ws = workspace if workspace is not None else Workspace(OP_VERIFY_TREE, B, N, device=target_tokens.device)
+    _check(lib().dspark_verify_tree_tokens(_ptr(target_tokens), _ptr(parents), _ptr(draft_tokens), _ptr(lengths), B, N,
+                                           _ptr(outs[0]), _ptr(outs[1]), _ptr(outs[2]), ws.address, ws.nbytes,
+                                           _stream(stream)), "dspark_verify_tree_tokens")
+    return tuple(outs)
+
+
+def _caches(k_cache, v_cache):
+    """Checks caches [num_pages, Hkv, page_size, D], or of several layers [layers, ...] (any layer stride); returns
+    (layers, layer stride in values, num_pages, Hkv, page_size, D)."""
+    torch = _torch()
+    for t, name in ((k_cache, "k_cache"), (v_cache, "v_cache")):
+        if not isinstance(t, torch.Tensor) or not t.is_cuda:
+            raise TypeError(f"{name} must be a CUDA tensor")
+        if t.dtype != torch.bfloat16 and t.dtype != torch.float16:
+            raise TypeError(f"{name} has dtype {t.dtype}, expected torch.bfloat16 or torch.float16")
+        if t.dim() not in (4, 5) or t.numel() == 0 or not t[(0,) * (t.dim() - 4)].is_contiguous():
+            raise ValueError(f"{name} must be [num_pages, Hkv, page_size, D], or [layers, ...] of such, contiguous within a layer")
+    if v_cache.shape != k_cache.shape or v_cache.dtype != k_cache.dtype:
+        raise ValueError("k_cache and v_cache must have the same shape and dtype")
+    shape = tuple(k_cache.shape[-4:])
+    layers = k_cache.shape[0] if k_cache.dim() == 5 else 1
+    stride = k_cache.stride(0) if layers > 1 else shape[0] * shape[1] * shape[2] * shape[3]
+    if layers > 1 and v_cache.stride(0) != stride:
+        raise ValueError("k_cache and v_cache must have the same layer stride")
+    return (layers, stride) + shape
+
+
+@_on_its_stream
+def dspark_kv_compact(k_cache, v_cache, block_table, kv_len, path, num_accepted, lengths=None, kv_len_out=None, workspace=None,
+                      stream=None):
+    """Moves the keys and values of each tree's accepted path (dspark_verify_tree's path and num_accepted) behind the
+    tokens before the tree, in place, in all layers of the caches ([num_pages, Hkv, page_size, D] or [layers, ...]);
+    returns kv_len_out [B] int32, the cached tokens afterwards."""
+    torch = _torch()
+    i32 = (torch.int32,)
+    layers, stride, num_pages, Hkv, page, D = _caches(k_cache, v_cache)
+    _need(block_table, "block_table", i32, 2)
+    _need(kv_len, "kv_len", i32, 1)
+    _need(path, "path", i32, 2)
+    _need(num_accepted, "num_accepted", i32, 1)
+    B, N = path.shape
+    if block_table.shape[0] != B or len(kv_len) != B or len(num_accepted) != B:
+        raise ValueError("shapes: block_table [B, max_pages], kv_len / num_accepted [B], path [B, N]")
+    if lengths is not None:
+        _need(lengths, "lengths", i32, 1)
+        if len(lengths) != B:
+            raise ValueError("lengths must be [B]")
+    if kv_len_out is None:
+        kv_len_out = torch.empty_like(kv_len)
+    else:
+        _need(kv_len_out, "kv_len_out", i32, 1)
+        if len(kv_len_out) != B:
+            raise ValueError("kv_len_out must be [B]")
+    ws = workspace if workspace is not None else Workspace(OP_KV_COMPACT, device=k_cache.device)
+    _check(lib().dspark_kv_compact(_ptr(k_cache), _ptr(v_cache), layers, stride, _ptr(block_table), block_table.shape[1],
+                                   _ptr(kv_len), _ptr(lengths), _ptr(path), _ptr(num_accepted), B, N, Hkv, D, num_pages, page,
+                                   _ptr(kv_len_out), ws.address, ws.nbytes, _stream(stream)), "dspark_kv_compact")
+    return kv_len_out
+
+
+@_on_its_stream
+def dspark_kv_copy_pages(k_cache, v_cache, src, dst, used=None, workspace=None, stream=None):
+    """Copies page src[m] to page dst[m] (its first used[m] tokens, or all) in all layers of the caches; src, dst, used
+    [M] int32.  A page that is written appears only once in the call."""
+    torch = _torch()
+    i32 = (torch.int32,)
+    layers, stride, num_pages, Hkv, page, D = _caches(k_cache, v_cache)
+    _need(src, "src", i32, 1)
+    _need(dst, "dst", i32, 1)
+    M = len(src)
+    if used is not None:
+        _need(used, "used", i32, 1)
+    if len(dst) != M or (used is not None and len(used) != M):
+        raise ValueError("src, dst and used must be [M]")
+    ws = workspace if workspace is not None else Workspace(OP_KV_COPY_PAGES, device=k_cache.device)
+    _check(lib().dspark_kv_copy_pages(_ptr(k_cache), _ptr(v_cache), layers, stride, _ptr(src), _ptr(dst), _ptr(used), M, Hkv, D,
+                                      num_pages, page, ws.address, ws.nbytes, _stream(stream)), "dspark_kv_copy_pages")
 
 
 def dspark_read_status(workspace: Workspace, stream=None):

@@ -210,6 +210,14 @@ size_t dspark_workspace_size(int op, int B, int N, int V, int r) {
             return prompt_attention_workspace_bytes(B, N, V);
         case DSPARK_OP_PAGED_ATTENTION:
             return paged_attention_workspace_bytes(B, N, V, r);
+        case DSPARK_OP_TREE_ATTENTION:
+            return tree_attention_workspace_bytes(B, N, V, r);
+        case DSPARK_OP_WINDOW_ATTENTION:
+            return window_attention_workspace_bytes(B, N, V, r);
+        case DSPARK_OP_VERIFY_TREE:
+        case DSPARK_OP_KV_COMPACT:
+        case DSPARK_OP_KV_COPY_PAGES:
+            return sizeof(WsHeader);
         default:
             return 0;
     }
@@ -480,33 +488,163 @@ dspark_status dspark_kv_append(const void* q, const void* k, const void* v, dspa
                             workspace, static_cast<cudaStream_t>(stream), dev);
 }
 
+// Arguments that the attentions over a paged cache share.
+static dspark_status check_paged(const char* op, const void* q, const void* k_cache, const void* v_cache, dspark_dtype dtype,
+                                 const int32_t* block_table, int max_pages, const int32_t* kv_len, float scale, int B, int N,
+                                 int Hq, int Hkv, int D, int num_pages, int page, const void* out) {
+    DSPARK_REQUIRE(q && k_cache && v_cache && block_table && kv_len && out, "%s: null pointer", op);
+    DSPARK_REQUIRE(dtype == DSPARK_BF16 || dtype == DSPARK_F16, "%s: dtype must be bf16 or fp16 (%d)", op, (int)dtype);
+    DSPARK_REQUIRE(B >= 1 && B <= 65535 && N >= 1 && N <= 65535 && Hkv >= 1 && Hq >= Hkv && Hq % Hkv == 0 &&
+                       Hq / Hkv <= 128 && Hq <= 65535,
+                   "%s: bad sizes (B=%d N=%d Hq=%d Hkv=%d)", op, B, N, Hq, Hkv);
+    DSPARK_REQUIRE(D == 64 || D == 128, "%s: D must be 64 or 128 (%d)", op, D);
+    DSPARK_REQUIRE(page >= 8 && page <= 256 && (page & (page - 1)) == 0,
+                   "%s: page must be a power of two from 8 to 256 (%d)", op, page);
+    DSPARK_REQUIRE(num_pages >= 1 && max_pages >= 1 && static_cast<long long>(max_pages) * page <= (1ll << 30) &&
+                       static_cast<long long>(num_pages) * page < (1ll << 31),
+                   "%s: bad cache (num_pages=%d max_pages=%d page=%d)", op, num_pages, max_pages, page);
+    DSPARK_REQUIRE(std::isfinite(scale), "%s: scale must be finite", op);
+    DSPARK_REQUIRE(aligned(q, 16) && aligned(k_cache, 16) && aligned(v_cache, 16) && aligned(out, 16),
+                   "%s: q, the caches and out must be 16-byte aligned", op);
+    return DSPARK_OK;
+}
+
 dspark_status dspark_paged_attention(const void* q, const void* k_cache, const void* v_cache, dspark_dtype dtype,
                                      const int32_t* block_table, int max_pages, const int32_t* kv_len,
                                      const int32_t* lengths, float scale, int causal, int B, int N, int Hq, int Hkv,
                                      int D, int num_pages, int page, void* out, float* lse, void* workspace,
                                      size_t ws_bytes, void* stream) {
     g_error[0] = '\0';
-    DSPARK_REQUIRE(q && k_cache && v_cache && block_table && kv_len && out, "paged_attention: null pointer");
-    DSPARK_REQUIRE(dtype == DSPARK_BF16 || dtype == DSPARK_F16, "paged_attention: dtype must be bf16 or fp16 (%d)",
-                   (int)dtype);
-    DSPARK_REQUIRE(B >= 1 && B <= 65535 && N >= 1 && N <= 65535 && Hkv >= 1 && Hq >= Hkv && Hq % Hkv == 0 &&
-                       Hq / Hkv <= 128 && Hq <= 65535,
-                   "paged_attention: bad sizes (B=%d N=%d Hq=%d Hkv=%d)", B, N, Hq, Hkv);
-    DSPARK_REQUIRE(D == 64 || D == 128, "paged_attention: D must be 64 or 128 (%d)", D);
-    DSPARK_REQUIRE(page >= 8 && page <= 256 && (page & (page - 1)) == 0,
-                   "paged_attention: page must be a power of two from 8 to 256 (%d)", page);
-    DSPARK_REQUIRE(num_pages >= 1 && max_pages >= 1 && static_cast<long long>(max_pages) * page <= (1ll << 30) &&
-                       static_cast<long long>(num_pages) * page < (1ll << 31),
-                   "paged_attention: bad cache (num_pages=%d max_pages=%d page=%d)", num_pages, max_pages, page);
-    DSPARK_REQUIRE(std::isfinite(scale), "paged_attention: scale must be finite");
-    DSPARK_REQUIRE(aligned(q, 16) && aligned(k_cache, 16) && aligned(v_cache, 16) && aligned(out, 16),
-                   "paged_attention: q, the caches and out must be 16-byte aligned");
+    const dspark_status st = check_paged("paged_attention", q, k_cache, v_cache, dtype, block_table, max_pages, kv_len, scale, B, N,
+                                         Hq, Hkv, D, num_pages, page, out);
+    if (st != DSPARK_OK) return st;
     if (bad_ws(workspace, ws_bytes, paged_attention_workspace_bytes(B, N, Hq, D))) return DSPARK_ERR_INVALID_ARG;
     DeviceInfo dev;
     if (!current_device(&dev)) return DSPARK_ERR_UNSUPPORTED;
     return launch_paged_attention(q, k_cache, v_cache, dtype, block_table, max_pages, kv_len, lengths, scale, causal, B,
                                   N, Hq, Hkv, D, num_pages, page, out, lse, workspace,
                                   static_cast<cudaStream_t>(stream), dev);
+}
+
+dspark_status dspark_window_attention(const void* q, const void* k_cache, const void* v_cache, dspark_dtype dtype,
+                                      const int32_t* block_table, int max_pages, const int32_t* kv_len,
+                                      const int32_t* lengths, int window, int sinks, float scale, int causal, int B, int N,
+                                      int Hq, int Hkv, int D, int num_pages, int page, void* out, float* lse,
+                                      void* workspace, size_t ws_bytes, void* stream) {
+    g_error[0] = '\0';
+    const dspark_status st = check_paged("window_attention", q, k_cache, v_cache, dtype, block_table, max_pages, kv_len, scale, B,
+                                         N, Hq, Hkv, D, num_pages, page, out);
+    if (st != DSPARK_OK) return st;
+    DSPARK_REQUIRE(window >= 1 && sinks >= 0, "window_attention: need window >= 1 and sinks >= 0 (%d %d)", window, sinks);
+    if (bad_ws(workspace, ws_bytes, window_attention_workspace_bytes(B, N, Hq, D))) return DSPARK_ERR_INVALID_ARG;
+    DeviceInfo dev;
+    if (!current_device(&dev)) return DSPARK_ERR_UNSUPPORTED;
+    return launch_masked_attention(q, k_cache, v_cache, dtype, block_table, max_pages, kv_len, lengths, nullptr, window, sinks,
+                                   scale, causal, B, N, Hq, Hkv, D, num_pages, page, out, lse, workspace,
+                                   static_cast<cudaStream_t>(stream), dev);
+}
+
+dspark_status dspark_tree_attention(const void* q, const void* k_cache, const void* v_cache, dspark_dtype dtype,
+                                    const int32_t* block_table, int max_pages, const int32_t* kv_len,
+                                    const int32_t* lengths, const int32_t* parents, int window, int sinks, float scale, int B,
+                                    int N, int Hq, int Hkv, int D, int num_pages, int page, void* out, float* lse,
+                                    void* workspace, size_t ws_bytes, void* stream) {
+    g_error[0] = '\0';
+    const dspark_status st = check_paged("tree_attention", q, k_cache, v_cache, dtype, block_table, max_pages, kv_len, scale, B, N,
+                                         Hq, Hkv, D, num_pages, page, out);
+    if (st != DSPARK_OK) return st;
+    DSPARK_REQUIRE(parents, "tree_attention: null parents");
+    DSPARK_REQUIRE(N <= kTreeMost, "tree_attention: at most %d nodes (N=%d)", kTreeMost, N);
+    DSPARK_REQUIRE((window == 0 || window >= N) && sinks >= 0, "tree_attention: need window 0 or >= N, sinks >= 0 (%d %d)", window,
+                   sinks);
+    if (bad_ws(workspace, ws_bytes, tree_attention_workspace_bytes(B, N, Hq, D))) return DSPARK_ERR_INVALID_ARG;
+    DeviceInfo dev;
+    if (!current_device(&dev)) return DSPARK_ERR_UNSUPPORTED;
+    return launch_masked_attention(q, k_cache, v_cache, dtype, block_table, max_pages, kv_len, lengths, parents, window, sinks,
+                                   scale, 1, B, N, Hq, Hkv, D, num_pages, page, out, lse, workspace,
+                                   static_cast<cudaStream_t>(stream), dev);
+}
+
+dspark_status dspark_verify_tree(const void* target, dspark_dtype dtype, const float* temperature, const float* u,
+                                 const int32_t* parents, const int32_t* draft_tokens, const int32_t* lengths, int B, int N,
+                                 int V, int32_t* out_tokens, int32_t* num_accepted, int32_t* path, void* workspace,
+                                 size_t ws_bytes, void* stream) {
+    g_error[0] = '\0';
+    DSPARK_REQUIRE(target && parents && draft_tokens && out_tokens && num_accepted && path, "verify_tree: null pointer");
+    DSPARK_REQUIRE(temperature == nullptr || u != nullptr, "verify_tree: null u with temperatures");
+    DSPARK_REQUIRE(dtype == DSPARK_F32 || dtype == DSPARK_BF16, "verify_tree: dtype must be fp32 or bf16 (%d)", (int)dtype);
+    DSPARK_REQUIRE(B >= 1 && B <= 65535 && N >= 1 && N <= kTreeMost && V >= 1 && V <= (1 << 21),
+                   "verify_tree: bad sizes (B=%d N=%d V=%d)", B, N, V);
+    DSPARK_REQUIRE(aligned(target, 16), "verify_tree: target must be 16-byte aligned");
+    if (bad_ws(workspace, ws_bytes, sizeof(WsHeader))) return DSPARK_ERR_INVALID_ARG;
+    DeviceInfo dev;
+    if (!current_device(&dev)) return DSPARK_ERR_UNSUPPORTED;
+    return launch_verify_tree(target, dtype, temperature, u, parents, draft_tokens, lengths, B, N, V, out_tokens, num_accepted,
+                              path, workspace, static_cast<cudaStream_t>(stream), dev);
+}
+
+dspark_status dspark_verify_tree_tokens(const int32_t* target_tokens, const int32_t* parents, const int32_t* draft_tokens,
+                                        const int32_t* lengths, int B, int N, int32_t* out_tokens, int32_t* num_accepted,
+                                        int32_t* path, void* workspace, size_t ws_bytes, void* stream) {
+    g_error[0] = '\0';
+    DSPARK_REQUIRE(target_tokens && parents && draft_tokens && out_tokens && num_accepted && path,
+                   "verify_tree_tokens: null pointer");
+    DSPARK_REQUIRE(B >= 1 && B <= 65535 && N >= 1 && N <= kTreeMost, "verify_tree_tokens: bad sizes (B=%d N=%d)", B, N);
+    if (bad_ws(workspace, ws_bytes, sizeof(WsHeader))) return DSPARK_ERR_INVALID_ARG;
+    DeviceInfo dev;
+    if (!current_device(&dev)) return DSPARK_ERR_UNSUPPORTED;
+    return launch_verify_tree_tokens(target_tokens, parents, draft_tokens, lengths, B, N, out_tokens, num_accepted, path,
+                                     workspace, static_cast<cudaStream_t>(stream));
+}
+
+// The caches of the calls that move within them.
+static dspark_status check_caches(const char* op, const void* k_cache, const void* v_cache, int layers, long long layer_stride,
+                                  int Hkv, int D, int num_pages, int page) {
+    DSPARK_REQUIRE(k_cache && v_cache, "%s: null cache", op);
+    DSPARK_REQUIRE(layers >= 1 && Hkv >= 1 && num_pages >= 1 && page >= 1 && D >= 8 && D <= 512 && D % 8 == 0 &&
+                       static_cast<long long>(num_pages) * page < (1ll << 31) && Hkv <= 65535 && layers <= 65535 &&
+                       static_cast<long long>(layers) * Hkv * D < (1ll << 29),
+                   "%s: bad cache (layers=%d num_pages=%d Hkv=%d page=%d D=%d)", op, layers, num_pages, Hkv, page, D);
+    // num_pages * page < 2^31, Hkv < 2^16, D < 2^10: below 2^57
+    DSPARK_REQUIRE(layer_stride % 8 == 0 && (layers == 1 || layer_stride >= static_cast<long long>(num_pages) * page * Hkv * D),
+                   "%s: the layer stride must be a multiple of 8 and at least a layer (%lld)", op, layer_stride);
+    DSPARK_REQUIRE(aligned(k_cache, 16) && aligned(v_cache, 16), "%s: the caches must be 16-byte aligned", op);
+    return DSPARK_OK;
+}
+
+dspark_status dspark_kv_compact(void* k_cache, void* v_cache, int layers, long long layer_stride, const int32_t* block_table,
+                                int max_pages, const int32_t* kv_len, const int32_t* lengths, const int32_t* path,
+                                const int32_t* num_accepted, int B, int N, int Hkv, int D, int num_pages, int page,
+                                int32_t* kv_len_out, void* workspace, size_t ws_bytes, void* stream) {
+    g_error[0] = '\0';
+    const dspark_status st = check_caches("kv_compact", k_cache, v_cache, layers, layer_stride, Hkv, D, num_pages, page);
+    if (st != DSPARK_OK) return st;
+    DSPARK_REQUIRE(block_table && kv_len && path && num_accepted && kv_len_out, "kv_compact: null pointer");
+    DSPARK_REQUIRE(kv_len_out != kv_len, "kv_compact: kv_len_out must not be kv_len");
+    DSPARK_REQUIRE(B >= 1 && N >= 1 && N <= kTreeMost, "kv_compact: bad sizes (B=%d N=%d)", B, N);
+    DSPARK_REQUIRE(max_pages >= 1 && static_cast<long long>(max_pages) * page <= (1ll << 30), "kv_compact: bad table (%d pages of %d)",
+                   max_pages, page);
+    if (bad_ws(workspace, ws_bytes, sizeof(WsHeader))) return DSPARK_ERR_INVALID_ARG;
+    DeviceInfo dev;
+    if (!current_device(&dev)) return DSPARK_ERR_UNSUPPORTED;
+    return launch_kv_compact(k_cache, v_cache, layer_stride, layers, block_table, max_pages, kv_len, lengths, path, num_accepted, B,
+                             N, Hkv, D, num_pages, page, kv_len_out, workspace, static_cast<cudaStream_t>(stream));
+}
+
+dspark_status dspark_kv_copy_pages(void* k_cache, void* v_cache, int layers, long long layer_stride, const int32_t* src,
+                                   const int32_t* dst, const int32_t* used, int M, int Hkv, int D, int num_pages, int page,
+                                   void* workspace, size_t ws_bytes, void* stream) {
+    g_error[0] = '\0';
+    const dspark_status st = check_caches("kv_copy_pages", k_cache, v_cache, layers, layer_stride, Hkv, D, num_pages, page);
+    if (st != DSPARK_OK) return st;
+    DSPARK_REQUIRE(src && dst, "kv_copy_pages: null pointer");
+    DSPARK_REQUIRE(M >= 1 && static_cast<long long>(page) * Hkv * D < (1ll << 31), "kv_copy_pages: bad sizes (M=%d, pages of %d x %d x %d)",
+                   M, Hkv, page, D);
+    if (bad_ws(workspace, ws_bytes, sizeof(WsHeader))) return DSPARK_ERR_INVALID_ARG;
+    DeviceInfo dev;
+    if (!current_device(&dev)) return DSPARK_ERR_UNSUPPORTED;
+    return launch_kv_copy_pages(k_cache, v_cache, layer_stride, layers, src, dst, used, M, Hkv, D, num_pages, page, workspace,
+                                static_cast<cudaStream_t>(stream));
 }
 
 dspark_status dspark_prompt_attention(const void* q, const void* k, const void* v, dspark_dtype dtype,

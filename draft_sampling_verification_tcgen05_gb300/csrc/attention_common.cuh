@@ -114,12 +114,12 @@ __device__ __forceinline__ bool pair_not_finite(uint32_t w, __half) {
 // blocks) before its product, which would spread them to rows that do not see them (0 * infinity is
 // NaN), and adds weight * value of each to the rows that do.  Called by 128 softmax threads together
 // (named barrier `bar`): thread `line` owns token row `line` of the tile and one output row, which
-// sees this tile's tokens [first, seen).  The rows' weights are at taddr_p, packed as the product
+// sees this tile's token t where sees(t).  The rows' weights are at taddr_p, packed as the product
 // takes them, the output row at taddr_o (complete up to the tile before); `row` and `masks` are
 // scratch in shared memory.
-template <typename T>
-__device__ __noinline__ void move_infinities(uint8_t* tile, uint32_t block_bytes, int halves, int line, int held, int first,
-                                             int seen, uint32_t taddr_p, uint32_t taddr_o, float* row, uint32_t* masks,
+template <typename T, typename Sees>
+__device__ __noinline__ void move_infinities(uint8_t* tile, uint32_t block_bytes, int halves, int line, int held, Sees sees,
+                                             uint32_t taddr_p, uint32_t taddr_o, float* row, uint32_t* masks,
                                              uint32_t bar) {
     bool bad = false;
     if (line < held) {
@@ -158,7 +158,7 @@ __device__ __noinline__ void move_infinities(uint8_t* tile, uint32_t block_bytes
             if (v == 0.0f) continue;
             const float o = __uint_as_float(tmem_ld1(taddr_o + static_cast<uint32_t>(d)));
             tmem_wait_ld();
-            tmem_st1(taddr_o + static_cast<uint32_t>(d), __float_as_uint(t >= first && t < seen ? fmaf(w, v, o) : o));
+            tmem_st1(taddr_o + static_cast<uint32_t>(d), __float_as_uint(sees(t) ? fmaf(w, v, o) : o));
             tmem_wait_st();
         }
         named_bar_sync(bar, 128);

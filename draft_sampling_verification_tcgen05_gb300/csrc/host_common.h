@@ -11,6 +11,8 @@
 
 namespace dspark {
 
+constexpr int kTreeMost = 256;             // nodes of a drafted tree
+
 struct DeviceInfo {
     int device = -1;
     int sm_count = 0;
@@ -98,6 +100,31 @@ dspark_status launch_paged_attention(const void* q, const void* k_cache, const v
                                      const int32_t* lengths, float scale, int causal, int B, int N, int Hq, int Hkv,
                                      int D, int num_pages, int page, void* out, float* lse, void* ws,
                                      cudaStream_t stream, const DeviceInfo& dev);
+
+size_t tree_attention_workspace_bytes(int B, int N, int Hq, int D);
+size_t window_attention_workspace_bytes(int B, int N, int Hq, int D);
+// parents: of a tree's nodes, or null (then causal as given)
+dspark_status launch_masked_attention(const void* q, const void* k_cache, const void* v_cache, dspark_dtype dtype,
+                                      const int32_t* block_table, int max_pages, const int32_t* kv_len,
+                                      const int32_t* lengths, const int32_t* parents, int window, int sinks, float scale,
+                                      int causal, int B, int N, int Hq, int Hkv, int D, int num_pages, int page, void* out,
+                                      float* lse, void* ws, cudaStream_t stream, const DeviceInfo& dev);
+
+dspark_status launch_verify_tree(const void* target, dspark_dtype dtype, const float* temperature, const float* u,
+                                 const int32_t* parents, const int32_t* draft_tokens, const int32_t* lengths, int B, int N,
+                                 int V, int32_t* out_tokens, int32_t* num_accepted, int32_t* path, void* ws,
+                                 cudaStream_t stream, const DeviceInfo& dev);
+dspark_status launch_verify_tree_tokens(const int32_t* target_tokens, const int32_t* parents, const int32_t* draft_tokens,
+                                        const int32_t* lengths, int B, int N, int32_t* out_tokens, int32_t* num_accepted,
+                                        int32_t* path, void* ws, cudaStream_t stream);
+
+dspark_status launch_kv_compact(void* k_cache, void* v_cache, long long layer_stride, int layers, const int32_t* block_table,
+                                int max_pages, const int32_t* kv_len, const int32_t* lengths, const int32_t* path,
+                                const int32_t* num_accepted, int B, int N, int Hkv, int D, int num_pages, int page,
+                                int32_t* kv_len_out, void* ws, cudaStream_t stream);
+dspark_status launch_kv_copy_pages(void* k_cache, void* v_cache, long long layer_stride, int layers, const int32_t* src,
+                                   const int32_t* dst, const int32_t* used, int M, int Hkv, int D, int num_pages, int page,
+                                   void* ws, cudaStream_t stream);
 
 size_t prompt_attention_workspace_bytes(int B, int T, int Hq);
 dspark_status launch_prompt_attention(const void* q, const void* k, const void* v, dspark_dtype dtype,

@@ -1,0 +1,46 @@
+// dspark_tree_attention and dspark_window_attention: arguments and launches of the kernels of paged_attention.cuh
+// with masks.  Both go through one instantiation: the masks are looked at only in the tiles that a row does not see
+// as a whole, a tree's last one to three and the two ends of a window, so a switch at run time costs nothing.
+#include "paged_attention.cuh"
+
+namespace dspark {
+
+namespace {
+
+int words_of(int N) { return (N + 31) / 32; }
+
+}  // namespace
+
+size_t tree_attention_workspace_bytes(int B, int N, int Hq, int D) {
+    if (B < 1 || N < 1 || Hq < 1 || D < 1) return 0;
+    return partials_end(N, Hq, D) + static_cast<size_t>(B) * N * (words_of(N) + 1) * sizeof(uint32_t);
+}
+
+size_t window_attention_workspace_bytes(int B, int N, int Hq, int D) {
+    if (B < 1 || N < 1 || Hq < 1 || D < 1) return 0;
+    return partials_end(N, Hq, D);
+}
+
+dspark_status launch_masked_attention(const void* q, const void* k_cache, const void* v_cache, dspark_dtype dtype,
+                                      const int32_t* block_table, int max_pages, const int32_t* kv_len,
+                                      const int32_t* lengths, const int32_t* parents, int window, int sinks, float scale,
+                                      int causal, int B, int N, int Hq, int Hkv, int D, int num_pages, int page, void* out,
+                                      float* lse, void* ws, cudaStream_t stream, const DeviceInfo& dev) {
+    if (static_cast<long long>(num_pages) * Hkv >= (1ll << 31) || static_cast<long long>(B) * N >= (1ll << 31)) {
+        set_error("%s_attention: num_pages * Hkv and B * N must be below 2^31", parents ? "tree" : "window");
+        return DSPARK_ERR_UNSUPPORTED;
+    }
+    PagedArgs a = paged_args(q, k_cache, v_cache, block_table, max_pages, kv_len, lengths, scale, causal, B, N, Hq, Hkv, D,
+                             num_pages, page, out, lse, ws);
+    a.parents = parents;
+    a.words = words_of(N);
+    a.ancestors = reinterpret_cast<uint32_t*>(static_cast<uint8_t*>(ws) + partials_end(N, Hq, D));
+    a.window = std::min(window, 1 << 30);                  // as wide as a table can be: positions stay within 32 bits
+    a.sinks = sinks;
+    const int grid = std::min(dev.sm_count, kMaxCtas);
+    if (dtype == DSPARK_BF16)
+        return D == 64 ? launch_typed<__nv_bfloat16, 64, true>(a, grid, stream) : launch_typed<__nv_bfloat16, 128, true>(a, grid, stream);
+    return D == 64 ? launch_typed<__half, 64, true>(a, grid, stream) : launch_typed<__half, 128, true>(a, grid, stream);
+}
+
+}  // namespace dspark

@@ -594,9 +594,9 @@ prompt_attention_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_co
                     if (!ok) break;
                     tc_fence_after();
                     if (part == 0) {
-                        move_infinities<T>(s.v[slot], kBlockBytes, kHalves, row, len - t * kTile, 0,
-                                           min(limit - t * kTile, kTile), tP, tO, reinterpret_cast<float*>(s.stage[8 * w]), s.masks[w],
-                                           kBarFirst + static_cast<uint32_t>(w));
+                        move_infinities<T>(s.v[slot], kBlockBytes, kHalves, row, len - t * kTile,
+                                           [=](int x) { return x < min(limit - t * kTile, kTile); }, tP, tO,
+                                           reinterpret_cast<float*>(s.stage[8 * w]), s.masks[w], kBarFirst + static_cast<uint32_t>(w));
                         fence_proxy_async_smem();
                     }
                     tc_fence_before();

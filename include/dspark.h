@@ -19,6 +19,15 @@
  *   dspark_paged_attention   a window of new tokens per request over the cache
  *   dspark_prompt_attention  attention within packed prompts
  *   dspark_sample            truncated sampling and the distributions themselves
+ *   dspark_window_attention  dspark_paged_attention with a sliding window and sinks
+ *
+ * and for trees of drafted tokens, where several candidates follow a token:
+ *
+ *   dspark_tree_attention    a tree of new tokens per request over the cache
+ *   dspark_verify_tree       the path of the tree that the target takes, from its logits
+ *   dspark_verify_tree_tokens  the same, the target's tokens given
+ *   dspark_kv_compact        the accepted path's keys and values moved together
+ *   dspark_kv_copy_pages     pages of the cache copied, for sequences that part
  *
  * Conventions shared by every call
  *   - All array arguments are DEVICE pointers on the current CUDA device,
@@ -87,7 +96,12 @@ typedef enum {
     /* 9: unused */
     DSPARK_OP_PAGED_ATTENTION = 10,
     DSPARK_OP_PROMPT_ATTENTION = 11,
-    DSPARK_OP_SAMPLE = 12
+    DSPARK_OP_SAMPLE = 12,
+    DSPARK_OP_TREE_ATTENTION = 13,
+    DSPARK_OP_WINDOW_ATTENTION = 14,
+    DSPARK_OP_VERIFY_TREE = 15,          /* dspark_verify_tree_tokens as well */
+    DSPARK_OP_KV_COMPACT = 16,
+    DSPARK_OP_KV_COPY_PAGES = 17
 } dspark_op;
 
 /*
@@ -127,6 +141,9 @@ typedef enum {
  *                           B, N as the call's, V = Hq, r = D
  *   DSPARK_OP_PROMPT_ATTENTION  the list of its work items; B as the call's, N = T, V = Hq
  *   DSPARK_OP_SAMPLE        grows with B (the rows' order); B = R, N = 1
+ *   DSPARK_OP_TREE_ATTENTION, DSPARK_OP_WINDOW_ATTENTION  as DSPARK_OP_PAGED_ATTENTION, the tree's
+ *                           with the nodes' ancestors besides
+ *   DSPARK_OP_VERIFY_TREE, DSPARK_OP_KV_COMPACT, DSPARK_OP_KV_COPY_PAGES  256 (the status word)
  * Returns 0 for an unknown op or negative sizes.
  */
 DSPARK_API size_t dspark_workspace_size(int op, int B, int N, int V, int r);
@@ -661,6 +678,160 @@ DSPARK_API dspark_status dspark_sample(const void* logits, dspark_dtype dtype, c
                                const int32_t* top_k, const float* top_p, const float* min_p,
                                const float* u, int R, int V, int32_t* tokens, float* probs,
                                void* workspace, size_t ws_bytes, void* stream);
+
+/*
+ * dspark_paged_attention with a sliding window and sinks.
+ *
+ * Layers with a window keep the cache's pages short of what any row still sees; the first tokens
+ * ("sinks") stay visible however far the window has gone.  Row i of request b's n new tokens is at
+ * position p = kv_len[b] - n + i and sees, of the tokens j <= p (causal) or j < kv_len[b] (not causal),
+ *     those with j < sinks or j > p - window.
+ * A long prompt is served in chunks: a chunk of N tokens is appended to the cache and then attended
+ * by this call.  Heads' grouping, precision, rows that see nothing, lse, and the guarantee about
+ * values that a row does not see are dspark_paged_attention's, as are all arguments but
+ *   window       >= 1
+ *   sinks        >= 0
+ * and as are the requirements and the device-side checks.  Entries of block_table for tiles of
+ * min(page, 128) tokens that no row of a request sees are not used and may be anything.
+ * workspace: >= dspark_workspace_size(DSPARK_OP_WINDOW_ATTENTION, B, N, Hq, D).
+ */
+DSPARK_API dspark_status dspark_window_attention(const void* q, const void* k_cache, const void* v_cache,
+                               dspark_dtype dtype, const int32_t* block_table, int max_pages,
+                               const int32_t* kv_len, const int32_t* lengths, int window, int sinks,
+                               float scale, int causal, int B, int N, int Hq, int Hkv, int D, int num_pages,
+                               int page, void* out, float* lse, void* workspace, size_t ws_bytes, void* stream);
+
+/*
+ * Attention of a tree of drafted tokens per request over a paged key-value cache.
+ *
+ * The target's pass over several drafted continuations at once ("Speculative decoding: from zero to
+ * DSpark" §2 scores one drafted block; here positions have more than one candidate).  The last
+ * n = lengths[b] (or N) of request b's kv_len[b] cached tokens are the nodes of its tree, in an order
+ * in which a node comes after its parent:
+ *     parents[b, i] in [0, i), or -1 for a node without one (the root; more than one may be).
+ * With base = kv_len[b] - n, row i sees
+ *     the tokens j < base; with window > 0 of those j < sinks or j > base + depth_i - window,
+ *     token base + m where m is i or an ancestor of i,
+ * depth_i being the number of i's ancestors (its position is base + depth_i, which is what
+ * dspark_kv_append rotates it by).  Everything else, and every other argument, as
+ * dspark_paged_attention.
+ *
+ *   parents      [B, N] int32, device (entries past a request's nodes are not read)
+ *   window       0 (none; sinks then count for nothing), or >= N: a node sees all its ancestors
+ *   sinks        >= 0
+ * Requirements: dspark_paged_attention's, and N <= 256.
+ * Device-side: kv_len[b] below n sets INPUT_RANGE and the request's rows are as rows that see nothing;
+ * a parent out of its range sets INPUT_RANGE and is read as -1.  With a window, entries of block_table
+ * as for dspark_window_attention.
+ * workspace: >= dspark_workspace_size(DSPARK_OP_TREE_ATTENTION, B, N, Hq, D).
+ */
+DSPARK_API dspark_status dspark_tree_attention(const void* q, const void* k_cache, const void* v_cache,
+                               dspark_dtype dtype, const int32_t* block_table, int max_pages,
+                               const int32_t* kv_len, const int32_t* lengths, const int32_t* parents,
+                               int window, int sinks, float scale, int B, int N, int Hq, int Hkv, int D,
+                               int num_pages, int page, void* out, float* lse, void* workspace,
+                               size_t ws_bytes, void* stream);
+
+/*
+ * Verification of a tree of drafted tokens from the target's logits.
+ *
+ * Node 0 is the root: the last token that was accepted before, which the target has not yet been run
+ * on.  Starting there, the target's token y of the current node is found, and the first child (the
+ * lowest index) that holds y is the next node; where no child does, y ends the output:
+ *     temperature 0:  y = argmax_v target[b, node, v], ties to the lowest v
+ *     otherwise       y drawn as dspark_sample draws it without top-k, top-p and min-p:
+ *         w_v = expf((x_v - m) * (1 / T)),  q_v = floor(w_v * 2^40),  Q = sum q_v,
+ *         t = floor(Q * U / 2^24),  U = floor(u[b, node] * 2^24),
+ *         y the smallest v whose inclusive prefix mass exceeds t.
+ * The tokens put out are the target's own, drawn one after the other, whatever the tree holds, so
+ * their law is the target's ("Speculative decoding: from zero to DSpark" §2, losslessness); the tree
+ * only decides how many of them one pass yields.  With top-k, top-p or min-p: dspark_sample draws a
+ * token for every node, and dspark_verify_tree_tokens walks.  Only the rows of the nodes on the path
+ * are read.
+ *
+ *   target       [B, N, V] dtype (fp32 or bf16), device: row i scores what follows node i
+ *   temperature  [B] fp32 >= 0, device, or NULL: 0 for all
+ *   u            [B, N] fp32 in [0, 1), device; may be NULL with temperature NULL
+ *   parents      [B, N] int32, device, as dspark_tree_attention's; node 0 has none (-1)
+ *   draft_tokens [B, N] int32 in [0, V), device; node 0's is not looked at
+ *   lengths      [B] int32 in [0, N], device, or NULL (= N): the request's nodes
+ *   out_tokens   [B, N] int32 output: accepted tokens, then the target's, then -1
+ *   num_accepted [B] int32 output: accepted tokens (the root is not counted)
+ *   path         [B, N] int32 output: node 0 and the accepted nodes, then -1
+ * A request without nodes outputs num_accepted 0 and -1 everywhere.
+ * Requirements: B >= 1, B <= 65535, 1 <= N <= 256, 1 <= V <= 2^21, target 16-byte aligned.
+ * Device-side: a length out of range sets INPUT_RANGE and the request is one without nodes; a parent
+ * out of [-1, i) or a draft token out of [0, V) sets INPUT_RANGE and the node is never reached; a u
+ * out of its range sets INPUT_RANGE and is read as the nearest value in it (NaN: 0); a temperature
+ * that is negative or not finite sets NUMERIC and is read as 0.
+ * In the rows read, -infinity is masked, NaN and +infinity are skipped and set NUMERIC, and a row
+ * without a finite entry gives token 0 and sets NUMERIC.
+ * workspace: >= dspark_workspace_size(DSPARK_OP_VERIFY_TREE, B, N, 0, 0).
+ */
+DSPARK_API dspark_status dspark_verify_tree(const void* target, dspark_dtype dtype, const float* temperature,
+                               const float* u, const int32_t* parents, const int32_t* draft_tokens,
+                               const int32_t* lengths, int B, int N, int V, int32_t* out_tokens,
+                               int32_t* num_accepted, int32_t* path, void* workspace, size_t ws_bytes,
+                               void* stream);
+
+/*
+ * dspark_verify_tree where the target's token behind every node is given:
+ *   target_tokens [B, N] int32, device (dspark_sample's output for the nodes' rows, for instance).
+ * A draft token below 0 sets INPUT_RANGE and its node is never reached; everything else as there.
+ */
+DSPARK_API dspark_status dspark_verify_tree_tokens(const int32_t* target_tokens, const int32_t* parents,
+                               const int32_t* draft_tokens, const int32_t* lengths, int B, int N,
+                               int32_t* out_tokens, int32_t* num_accepted, int32_t* path, void* workspace,
+                               size_t ws_bytes, void* stream);
+
+/*
+ * Moves the accepted path of each request's tree behind the tokens before the tree, in place and in
+ * all layers: of the last n = lengths[b] (or N) of kv_len[b] cached tokens those at
+ *     path[b, 0] < path[b, 1] < ... < path[b, num_accepted[b]]   (places in the tree, < n)
+ * are kept; with base = kv_len[b] - n, token base + path[b, i] goes to place base + i, and
+ *     kv_len_out[b] = base + num_accepted[b] + 1           (kv_len[b] where n is 0).
+ * path and num_accepted are dspark_verify_tree's.  The last token of out_tokens is not in the cache: it
+ * is the root of the next tree.  A chain's kept tokens are in place already; only kv_len changes.
+ *
+ *   k_cache, v_cache  `layers` caches [num_pages, Hkv, page, D] of 16-bit values, layer_stride values
+ *                apart, device, updated in place
+ *   block_table  [B, max_pages] int32, device, as dspark_paged_attention's; requests do not share the
+ *                pages that hold their trees
+ *   kv_len       [B] int32, device;   lengths [B] int32 in [0, N], device, or NULL (= N)
+ *   path         [B, N] int32, device;  num_accepted [B] int32 in [0, n), device (0 where n is 0)
+ *   kv_len_out   [B] int32 output; not kv_len itself
+ * Requirements: B >= 1, 1 <= N <= 256, layers, Hkv, num_pages, max_pages, page >= 1, D a multiple of 8
+ * up to 512, num_pages * page < 2^31, max_pages * page <= 2^30, layers * Hkv * D < 2^29, layer_stride a
+ * multiple of 8 and (with more than one layer) at least num_pages * Hkv * page * D; the caches 16-byte aligned.
+ * Device-side: a length, kv_len, num_accepted or path out of range sets INPUT_RANGE, nothing of the
+ * request is moved and kv_len_out[b] = kv_len[b]; a page out of [0, num_pages) sets INPUT_RANGE and
+ * its token is not moved.
+ * workspace: >= dspark_workspace_size(DSPARK_OP_KV_COMPACT, ...) bytes.
+ */
+DSPARK_API dspark_status dspark_kv_compact(void* k_cache, void* v_cache, int layers, long long layer_stride,
+                               const int32_t* block_table, int max_pages, const int32_t* kv_len,
+                               const int32_t* lengths, const int32_t* path, const int32_t* num_accepted,
+                               int B, int N, int Hkv, int D, int num_pages, int page, int32_t* kv_len_out,
+                               void* workspace, size_t ws_bytes, void* stream);
+
+/*
+ * Copies pages of a paged key-value cache within it, in all layers: page dst[m] receives the first
+ * used[m] tokens (all of them where used is NULL) of page src[m]; its other tokens stay as they are.
+ * A sequence that parts in several shares its full pages and needs a copy of its last one; a sequence
+ * can be moved to other pages.  A page may be the source of several copies; one that is a
+ * destination appears only once in the call (but for src[m] = dst[m], which does nothing): what
+ * another copy reads from it or writes to it is otherwise either's.
+ *
+ *   k_cache, v_cache, layers, layer_stride, Hkv, D, num_pages, page  as dspark_kv_compact's
+ *   src, dst     [M] int32 in [0, num_pages), device
+ *   used         [M] int32 in [0, page], device, or NULL
+ * Requirements: M >= 1, dspark_kv_compact's of the caches, and Hkv * page * D < 2^31.
+ * Device-side: an entry out of its range sets INPUT_RANGE and its page is not copied.
+ * workspace: >= dspark_workspace_size(DSPARK_OP_KV_COPY_PAGES, ...) bytes.
+ */
+DSPARK_API dspark_status dspark_kv_copy_pages(void* k_cache, void* v_cache, int layers, long long layer_stride,
+                               const int32_t* src, const int32_t* dst, const int32_t* used, int M, int Hkv,
+                               int D, int num_pages, int page, void* workspace, size_t ws_bytes, void* stream);
 
 /*
  * Synchronises `stream`, reads the status word of `workspace` written by the

@@ -38,6 +38,7 @@ from .verify_logits import verify_from_logits, draft_distributions, draft_lse, r
 from .attention import attend_row, paged_attention, prompt_attention
 from .kv_append import kv_append, rms_norm, rotate
 from .sample import sample_row, truncated_distribution, weights
+from .tree import compact, copy_pages, depths, tree_row_sees, tree_token, verify_tree, window_row_sees
 from .verify_gumbel import verify_gumbel, target_gumbel_tokens
 
 __all__ = [
@@ -50,4 +51,5 @@ __all__ = [
     "verify_gumbel", "target_gumbel_tokens",
     "attend_row", "paged_attention", "prompt_attention", "kv_append", "rms_norm", "rotate",
     "sample_row", "truncated_distribution", "weights",
+    "compact", "copy_pages", "depths", "tree_row_sees", "tree_token", "verify_tree", "window_row_sees",
 ]
