@@ -19,6 +19,12 @@ __device__ __forceinline__ uint32_t remote(const void* p, uint32_t rank) {
     asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(r) : "r"(smem_u32(p)), "r"(rank));
     return r;
 }
+// Asynchronous store there, counted in bytes on an mbarrier of the same block.
+__device__ __forceinline__ void send(uint32_t at, u64 v, uint32_t bar) {
+    asm volatile("st.async.weak.shared::cluster.mbarrier::complete_tx::bytes.b64 [%0], %1, [%2];"
+                 :: "r"(at), "l"(v), "r"(bar) : "memory");
+}
+
 // floor(total * frac / 2^24), total < 2^62, frac <= 2^24.
 __device__ __forceinline__ u64 share_of(u64 total, uint32_t frac) {
     return (total >> 24) * frac + (((total & 0xFFFFFFull) * frac) >> 24);
@@ -62,6 +68,11 @@ struct MassSum {
         lo += __float_as_uint(u.x) + __float_as_uint(u.y);
     }
     __device__ __forceinline__ void count(uint32_t k) { n += k; }             // entries that were added
+    // The warp's sum, of fewer than 128 entries in each lane (its halves then stay within 32 bits).
+    __device__ __forceinline__ u64 warp_value() const {
+        return (static_cast<u64>(__reduce_add_sync(0xFFFFFFFFu, hi - n * kHalfBias)) << 20) +
+               __reduce_add_sync(0xFFFFFFFFu, lo - n * kHalfBias);
+    }
     __device__ __forceinline__ u64 value() const {
         return (static_cast<u64>(hi - n * kHalfBias) << 20) + (lo - n * kHalfBias);
     }

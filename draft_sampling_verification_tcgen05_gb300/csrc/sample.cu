@@ -90,11 +90,7 @@ struct SampleArgs {
     int32_t* order;                        // with a queue: the rows as they are taken
 };
 
-// Asynchronous stores and an addition there, counted in bytes on an mbarrier of the same block.
-__device__ __forceinline__ void send(uint32_t at, u64 v, uint32_t bar) {
-    asm volatile("st.async.weak.shared::cluster.mbarrier::complete_tx::bytes.b64 [%0], %1, [%2];"
-                 :: "r"(at), "l"(v), "r"(bar) : "memory");
-}
+// Likewise of 32 bits, and an addition.
 __device__ __forceinline__ void send32(uint32_t at, uint32_t v, uint32_t bar) {
     asm volatile("st.async.weak.shared::cluster.mbarrier::complete_tx::bytes.b32 [%0], %1, [%2];"
                  :: "r"(at), "r"(v), "r"(bar) : "memory");
