@@ -24,6 +24,11 @@ __device__ __forceinline__ void send(uint32_t at, u64 v, uint32_t bar) {
     asm volatile("st.async.weak.shared::cluster.mbarrier::complete_tx::bytes.b64 [%0], %1, [%2];"
                  :: "r"(at), "l"(v), "r"(bar) : "memory");
 }
+// Likewise of two values that lie together, 16-byte aligned.
+__device__ __forceinline__ void send2(uint32_t at, u64 v, u64 w, uint32_t bar) {
+    asm volatile("st.async.weak.shared::cluster.mbarrier::complete_tx::bytes.v2.b64 [%0], {%1, %2}, [%3];"
+                 :: "r"(at), "l"(v), "l"(w), "r"(bar) : "memory");
+}
 
 // floor(total * frac / 2^24), total < 2^62, frac <= 2^24.
 __device__ __forceinline__ u64 share_of(u64 total, uint32_t frac) {

@@ -18,25 +18,31 @@ namespace dspark {
 namespace {
 
 constexpr int kThreads = 256;
-constexpr int kWarps = kThreads / 32;
+constexpr int kWarpBits = 3, kWarps = 1 << kWarpBits;
+static_assert(kThreads == 32 * kWarps, "warps of a block");
 constexpr int kBlocks = 4;                 // per SM
 constexpr int kClusterMost = 16;
-constexpr int kBatch = 6;                  // 16-byte pieces that a thread has under way beside those held
+constexpr int kGroup = 4;                  // rounds of 32 pieces, at least, whose sums a warp keeps apart
+constexpr int kBatch = 4;                  // 16-byte pieces that a thread looks at together
 constexpr int kHeld = 12;                  // pieces of a row that a thread holds in shared memory
 
 struct VerifyArgs {
     TreeArgs tree;
     const void* target;
     const float *temperature, *u;          // null: temperature 0
-    int cluster;
+    int cluster_bits;                      // 2^cluster_bits blocks take a request
 };
+
+constexpr int kTurns = 4;
+struct alignas(16) Pair { u64 key, sum; };
 
 struct Shared {
     uint4 held[kHeld][kThreads];
-    u64 slot[2][kClusterMost * kWarps];    // what the cluster's warps tell each other, two exchanges in turn
+    Pair pair[kTurns][kClusterMost];       // what the cluster's blocks tell each other, kTurns exchanges in turn
+    Pair warp_pair[kTurns][kWarps];
     int parent[kTreeMost], token[kTreeMost];
     int path[kTreeMost], out[kTreeMost];
-    uint64_t bar[2];
+    uint64_t bar[kTurns];
 };
 constexpr uint32_t kWaitPeer = 0xB01;
 constexpr long long kUnderWayNs = 100000;  // far more than a store into another block's shared memory takes
@@ -65,14 +71,15 @@ struct Row {
     }
     __device__ __forceinline__ int pieces() const { return (shift + V + kPer - 1) / kPer; }
     __device__ __forceinline__ int id(int piece) const { return piece * kPer - shift; }
-    __device__ __forceinline__ bool whole(int piece) const { return id(piece) >= 0 && id(piece) + kPer <= V; }
-    __device__ __forceinline__ uint4 load(int piece) const {
+    __device__ __forceinline__ int first_whole() const { return shift > 0 ? 1 : 0; }             // the pieces that lie
+    __device__ __forceinline__ int behind_whole() const { return (shift + V) / kPer; }           // within the row
+    __device__ __noinline__ uint4 edge(int piece) const {
         const int v = id(piece);
-        if (v >= 0 && v + kPer <= V) return __ldg(reinterpret_cast<const uint4*>(row + v));
-        uint4 w;
-        T* x = reinterpret_cast<T*>(&w);
+        T x[kPer];
 #pragma unroll
         for (int e = 0; e < kPer; ++e) x[e] = v + e >= 0 && v + e < V ? row[v + e] : static_cast<T>(-INFINITY);
+        uint4 w;
+        memcpy(&w, x, 16);
         return w;
     }
     static __device__ __forceinline__ uint4 nothing() {    // entries of -infinity
@@ -98,10 +105,10 @@ __global__ void __launch_bounds__(kThreads, kBlocks) verify_tree_kernel(const __
     constexpr int kPer = Row<T>::kPer;
     const TreeArgs& t = a.tree;
     const int tid = threadIdx.x, warp = static_cast<int>(warp_id()), lane = static_cast<int>(lane_id());
-    const int C = kCluster ? a.cluster : 1;
+    const int C = kCluster ? 1 << a.cluster_bits : 1, warp_bits = (kCluster ? a.cluster_bits : 0) + kWarpBits;
     const int rank = kCluster ? static_cast<int>(cluster_rank()) : 0;
-    const int b = static_cast<int>(blockIdx.x) / C;
-    const int warps = C * kWarps, self = rank * kWarps + warp;               // of the cluster, in the order of the row
+    const int b = static_cast<int>(blockIdx.x) >> (kCluster ? a.cluster_bits : 0);
+    const int self = rank * kWarps + warp;                 // among the cluster's warps, in the order of the row
     uint32_t flags = 0;
 
     const int nodes = tree_nodes(t, b);
@@ -119,27 +126,50 @@ __global__ void __launch_bounds__(kThreads, kBlocks) verify_tree_kernel(const __
     const bool greedy = T_b == 0.0f;
     const float inv = greedy ? 0.0f : fminf(1.0f / T_b, 3.402823466e38f);
 
-    // A value of every warp of the cluster for all of them; lane l then has those of warps 4 l .. 4 l + 3 (0 where
-    // there is none).  The values travel as asynchronous stores that complete on an mbarrier of the receiving block.
-    // What the next exchange but one overwrites has been read: all have answered the next one by then.  False where
-    // the wait gave up.
-    int turn = 0;                                          // exchanges so far
-    auto exchange = [&](u64 mine, u64 (&all)[4]) {
-        const int odd = turn & 1;
+    // What the blocks tell each other travels as asynchronous stores into every block, which complete on an mbarrier
+    // there.  Of any three turns at least one is an exchange of all blocks, which a block answers when all its warps
+    // have come to it, so what the turn after those overwrites has been read.
+    int turn = 0;
+    auto told = [&](uint32_t bytes) {                      // false where the wait gave up
         bool ok = true;
         if constexpr (kCluster) {
-            if (tid == 0) mbar_arrive_expect_tx(&s.bar[odd], static_cast<uint32_t>(warps) * 8u);
-            if (lane < C)
-                send(remote(&s.slot[odd][self], static_cast<uint32_t>(lane)), mine, remote(&s.bar[odd], static_cast<uint32_t>(lane)));
-            ok = mbar_wait_short(&s.bar[odd], static_cast<uint32_t>(turn >> 1) & 1u, t.ws, kDefaultTimeoutNs, kWaitPeer);
+            uint64_t* bar = &s.bar[turn % kTurns];
+            if (tid == 0) mbar_arrive_expect_tx(bar, bytes);
+            ok = mbar_wait_short(bar, static_cast<uint32_t>(turn / kTurns) & 1u, t.ws, kDefaultTimeoutNs, kWaitPeer);
             ok = __all_sync(0xFFFFFFFFu, ok);
         } else {
-            if (lane == 0) s.slot[odd][self] = mine;
             __syncthreads();
         }
         ++turn;
+        return ok;
+    };
+    // A pair of every block: the largest of the warps' `key`s and the sum of their `sum`s (added by `add`).  Lane r then has those of block r, 0 where there is none.
+    auto exchange = [&](u64 key, u64 sum, auto add, Pair& all) {
+        const int now = turn % kTurns;
+        if (lane == 0) s.warp_pair[now][warp] = Pair{key, sum};
+        __syncthreads();
+        if (warp == 0) {
+            Pair mine = s.warp_pair[now][lane % kWarps];   // every kWarps lanes come to the same
+            mine.key = warp_max_u64(mine.key);
 #pragma unroll
-        for (int x = 0; x < 4; ++x) all[x] = 4 * lane + x < warps ? s.slot[odd][4 * lane + x] : 0;
+            for (int d = kWarps / 2; d > 0; d >>= 1) mine.sum = add(mine.sum, __shfl_xor_sync(0xFFFFFFFFu, mine.sum, d));
+            if (kCluster && lane < C)
+                send2(remote(&s.pair[now][rank], static_cast<uint32_t>(lane)), mine.key, mine.sum,
+                      remote(&s.bar[now], static_cast<uint32_t>(lane)));
+            if (!kCluster && lane == 0) s.pair[now][0] = mine;
+        }
+        const bool ok = told(static_cast<uint32_t>(C) * 16u);
+        all = lane < C ? s.pair[now][lane] : Pair{0, 0};
+        return ok;
+    };
+    // A value that only one warp of the cluster has (`here`).
+    auto hear = [&](bool here, u64 mine, u64& value) {
+        const int now = turn % kTurns;
+        if (kCluster && here && lane < C)
+            send(remote(&s.pair[now][0].key, static_cast<uint32_t>(lane)), mine, remote(&s.bar[now], static_cast<uint32_t>(lane)));
+        if (!kCluster && here && lane == 0) s.pair[now][0].key = mine;
+        const bool ok = told(8u);
+        value = s.pair[now][0].key;
         return ok;
     };
     // The first child of `node` that holds token y (kTreeMost: none).
@@ -150,8 +180,7 @@ __global__ void __launch_bounds__(kThreads, kBlocks) verify_tree_kernel(const __
         return static_cast<int>(__reduce_min_sync(0xFFFFFFFFu, child));
     };
     if (kCluster && tid == 0) {
-        mbar_init(&s.bar[0], 1);
-        mbar_init(&s.bar[1], 1);
+        for (int i = 0; i < kTurns; ++i) mbar_init(&s.bar[i], 1);
         fence_mbarrier_init();
     }
     __syncthreads();
@@ -161,31 +190,55 @@ __global__ void __launch_bounds__(kThreads, kBlocks) verify_tree_kernel(const __
     }
     grid_dependency_wait();                                // the status word has been cleared
 
-    // A key's low word tells the entry by a number from 2^31 on; without that bit the warp met NaN or +infinity.
-    constexpr u64 kClean = 1ull << 31;
     int node = 0, accepted = 0;
     bool ok = true;
     for (int k = 0; k < n; ++k) {
         auto row_of = [&](int i) { return Row<T>(static_cast<const T*>(a.target) + (static_cast<long long>(b) * t.N + i) * t.V, t.V); };
         const Row<T> row = row_of(node);
         // this warp's pieces, in rounds of 32; the first kHeld rounds stay in shared memory
-        auto first_piece = [&](const Row<T>& r, int w) { return static_cast<int>(static_cast<long long>(r.pieces()) * w / warps); };
+        auto first_piece = [&](const Row<T>& r, int w) { return static_cast<int>((static_cast<long long>(r.pieces()) * w) >> warp_bits); };
         const int lo = first_piece(row, self), hi = first_piece(row, self + 1);
         const int rounds = (hi - lo + 31) / 32;
         const int held = min(rounds, kHeld);
         auto piece_of = [&](int x) { return lo + 32 * x + lane; };
         const uint4 nothing = Row<T>::nothing();           // where the last round has no piece for a lane
-
-        // ---- the largest entry, the first of equal ones ----
+        const int whole0 = row.first_whole(), whole1 = row.behind_whole();
+        auto load = [&](int j) {
+            if (j >= whole0 && j < min(hi, whole1)) return __ldg(reinterpret_cast<const uint4*>(row.row + row.id(j)));
+            return j < hi ? row.edge(j) : nothing;
+        };
 #pragma unroll 4
         for (int x = 0; x < held; ++x) {
             const int j = piece_of(x);
-            if (j < hi && row.whole(j)) copy_async(&s.held[x][tid], row.row + row.id(j));
-            else s.held[x][tid] = j < hi ? row.load(j) : nothing;
+            if (j >= whole0 && j < min(hi, whole1)) copy_async(&s.held[x][tid], row.row + row.id(j));
+            else s.held[x][tid] = j < hi ? row.edge(j) : nothing;
         }
-        float best = -INFINITY;
+        auto piece = [&](int x) { return x < kHeld ? s.held[x][tid] : load(piece_of(x)); };
+
+        // ---- one pass: the largest entry, the first of equal ones; without greed sums of weights for a first answer ----
+        // These weights are relative to `ref`, the largest of the row's first pieces, which all warps look at.
+        float ref = 0.0f;
+        if (!greedy) {
+            float v[kPer], top = -INFINITY;
+            Row<T>::unpack(lane >= whole0 && lane < whole1 ? __ldg(reinterpret_cast<const uint4*>(row.row + row.id(lane)))
+                           : lane < row.pieces()           ? row.edge(lane)
+                                                           : nothing,
+                           v);
+#pragma unroll
+            for (int e = 0; e < kPer; ++e) top = fmaxf(top, v[e]);
+            top = float_from_order_bits(__reduce_max_sync(0xFFFFFFFFu, float_order_bits(top)));
+            if (top > -INFINITY && top < INFINITY) ref = top;
+        }
+        const float2 slope2 = make_float2(inv * kLog2e, inv * kLog2e), shift2 = make_float2(-ref * slope2.x, -ref * slope2.x);
+        auto quick = [&](const float* v, int e) {          // 2^((v - ref) / T * log2 e), two at once
+            const float2 z = __ffma2_rn(make_float2(v[e], v[e + 1]), slope2, shift2);
+            return make_float2(exp2_approx(z.x), exp2_approx(z.y));
+        };
+        const int per = max(kGroup, (rounds + 31) / 32);   // rounds of a group; lane g keeps the sum of the g-th
+        float2 sum2[2] = {};
+        float group_sum = 0.0f, warp_sum = 0.0f;
+        float best = -INFINITY, odd_value = -INFINITY;     // odd_value: NaN where one is met
         int best_piece = -1;
-        bool clean = true;                                 // no NaN, no +infinity
         auto look = [&](const uint4& raw, int j) {
             float v[kPer];
             Row<T>::unpack(raw, v);
@@ -197,214 +250,244 @@ __global__ void __launch_bounds__(kThreads, kBlocks) verify_tree_kernel(const __
                 top = max3_nan(top, v[5], v[6]);
                 top = max3_nan(top, v[7], v[7]);
             }
-            if (!(top < INFINITY)) {
-                clean = false;
-                top = -INFINITY;
-#pragma unroll
-                for (int e = 0; e < kPer; ++e)
-                    if (v[e] < INFINITY) top = fmaxf(top, v[e]);
-            }
+            odd_value = max3_nan(odd_value, top, top);
             if (top > best) {
                 best = top;
                 best_piece = j;
             }
+            if (!greedy) {
+#pragma unroll
+                for (int e = 0; e < kPer; e += 2) sum2[(e >> 1) & 1] = __fadd2_rn(sum2[(e >> 1) & 1], quick(v, e));
+            }
         };
-        for (int x0 = kHeld; x0 < rounds; x0 += kBatch) {
-            uint4 raw[kBatch];
-#pragma unroll
-            for (int x = 0; x < kBatch; ++x) raw[x] = piece_of(x0 + x) < hi ? row.load(piece_of(x0 + x)) : nothing;
-#pragma unroll
-            for (int x = 0; x < kBatch; ++x) look(raw[x], piece_of(x0 + x));
-        }
-        // the pieces held come before the others
-        const float later = best;
-        const int later_piece = best_piece;
-        best = -INFINITY;
-        best_piece = -1;
         copy_wait();
-#pragma unroll 4
-        for (int x = 0; x < held; ++x) look(s.held[x][tid], piece_of(x));
-        if (later > best) {
-            best = later;
-            best_piece = later_piece;
+        for (int g = 0; g * per < rounds; ++g) {
+            const int end = min((g + 1) * per, rounds);
+            for (int x0 = g * per; x0 < end; x0 += kBatch) {
+                uint4 raw[kBatch];
+#pragma unroll
+                for (int x = 0; x < kBatch; ++x) raw[x] = x0 + x < end ? piece(x0 + x) : nothing;
+#pragma unroll
+                for (int x = 0; x < kBatch; ++x) look(raw[x], piece_of(x0 + x));
+            }
+            if (!greedy) {
+                float sum = (sum2[0].x + sum2[0].y) + (sum2[1].x + sum2[1].y);
+                for (int d = 16; d > 0; d >>= 1) sum += __shfl_xor_sync(0xFFFFFFFFu, sum, d);
+                if (lane == g) group_sum = sum;
+                warp_sum += sum;
+                sum2[0] = sum2[1] = make_float2(0.0f, 0.0f);
+            }
+        }
+        bool clean = __all_sync(0xFFFFFFFFu, odd_value < INFINITY);           // no NaN, no +infinity
+        if (!clean) {                                      // once more without them
+            best = -INFINITY;
+            best_piece = -1;
+            for (int x = 0; x < rounds; ++x) {
+                float v[kPer];
+                Row<T>::unpack(piece(x), v);
+#pragma unroll
+                for (int e = 0; e < kPer; ++e)
+                    if (v[e] < INFINITY && v[e] > best) {
+                        best = v[e];
+                        best_piece = piece_of(x);
+                    }
+            }
         }
         u64 key = 0;                                       // 0: nothing finite
         if (best_piece >= 0) {
-            const int x = (best_piece - lo) / 32;
             float v[kPer];
-            Row<T>::unpack(x < kHeld ? s.held[x][tid] : row.load(best_piece), v);
+            Row<T>::unpack(piece((best_piece - lo) >> 5), v);
 #pragma unroll
             for (int e = kPer - 1; e >= 0; --e)
                 if (v[e] == best) key = argmax_key(best, static_cast<uint32_t>(row.id(best_piece) + e));
         }
-        key = warp_max_u64(key) | kClean;
-        if (!__all_sync(0xFFFFFFFFu, clean)) key &= ~kClean;
-        u64 all[4];
-        ok = exchange(key, all);
-        if (!ok) break;
-        clean = true;
-        key = 0;
-#pragma unroll
-        for (int x = 0; x < 4; ++x) {
-            if (4 * lane + x < warps && !(all[x] & kClean)) clean = false;
-            key = max(key, all[x] | kClean);
-        }
-        clean = __all_sync(0xFFFFFFFFu, clean);
         key = warp_max_u64(key);
-        if (key >> 32 == 0) key = 0;
-        if (!clean) flags |= DSPARK_STATUS_NUMERIC;
+        auto add_floats = [](u64 x, u64 y) {
+            return static_cast<u64>(__float_as_uint(__uint_as_float(static_cast<uint32_t>(x)) + __uint_as_float(static_cast<uint32_t>(y))));
+        };
+        Pair all;
+        // a block that met NaN or +infinity says so by a sum of NaN; a sum that is not a number by itself (a slope that
+        // overflows) counts as infinite
+        ok = exchange(key, __float_as_uint(!clean ? NAN : warp_sum == warp_sum ? warp_sum : INFINITY), add_floats, all);
+        if (!ok) break;
+        const float block_sum = __uint_as_float(static_cast<uint32_t>(all.sum));
+        clean = __all_sync(0xFFFFFFFFu, block_sum == block_sum);
+        key = warp_max_u64(all.key);
+        if (!clean || key == 0) flags |= DSPARK_STATUS_NUMERIC;
         int y = key != 0 ? static_cast<int>(key_index(key)) : 0;
-        if (key == 0) flags |= DSPARK_STATUS_NUMERIC;
         int child = child_of(node, y);
 
         if (!greedy && key != 0) {
             if (child < n) {                               // the likeliest next row is under way to the L2 cache meanwhile
                 const Row<T> next = row_of(child);
-                const int to = first_piece(next, self + 1);
-                for (int j = first_piece(next, self) + 8 * lane; j < to; j += 8 * 32)
-                    if (next.whole(j)) prefetch_l2(next.row + next.id(j));
+                const int to = min(first_piece(next, self + 1), next.behind_whole());
+                for (int j = max(first_piece(next, self), next.first_whole()) + 8 * lane; j < to; j += 8 * 32)
+                    prefetch_l2(next.row + next.id(j));
             }
-            // ---- masses: lane g keeps the sum of the warp's g-th group of rounds ----
             const float m = float_from_order_bits(static_cast<uint32_t>(key >> 32));
-            const float2 shift = make_float2(-m, -m), slope = make_float2(inv, inv);
-            auto weights = [&](const uint4& raw, float* w, bool filter) {  // the roundings of (x - m) * inv, two at once
-                Row<T>::unpack(raw, w);
-                if (filter)
-#pragma unroll
-                    for (int e = 0; e < kPer; ++e) w[e] = w[e] < INFINITY ? w[e] : -INFINITY;
-#pragma unroll
-                for (int e = 0; e < kPer; e += 2) {
-                    const float2 z = __fmul2_rn(__fadd2_rn(make_float2(w[e], w[e + 1]), shift), slope);
-                    w[e] = expf(z.x);
-                    w[e + 1] = expf(z.y);
-                }
-            };
-            // A round's masses: fewer than 2^27 in each half, so the halves' sums over a group of up to 16 stay within 32 bits.
-            auto add_round = [&](MassSum& sum, const uint4& raw, bool filter) {
-                float w[kPer];
-                weights(raw, w, filter);
-#pragma unroll
-                for (int e = 0; e < kPer; e += 2) sum.add(make_float2(w[e], w[e + 1]));
-                sum.count(kPer);
-            };
-            auto piece = [&](int x) { return piece_of(x) < hi ? row.load(piece_of(x)) : nothing; };
-            const int per = (rounds + 31) / 32;            // rounds of a group
-            u64 kept = 0;
-            auto sum_groups = [&](bool filter) {
-                if (per == 1) {
-#pragma unroll 4
-                    for (int x = 0; x < held; ++x) {
-                        MassSum sum;
-                        add_round(sum, s.held[x][tid], filter);
-                        const u64 q = sum.warp_value();
-                        if (lane == x) kept = q;
-                    }
-                }
-                for (int g = per == 1 ? held : 0; g * per < rounds; ) {
-                    // kBatch rounds' loads ahead: as many groups, or part of one
-                    uint4 raw[kBatch];
-                    if (per == 1) {
-#pragma unroll
-                        for (int x = 0; x < kBatch; ++x) raw[x] = g + x < rounds ? piece(g + x) : nothing;
-#pragma unroll
-                        for (int x = 0; x < kBatch; ++x) {
-                            MassSum sum;
-                            add_round(sum, raw[x], filter);
-                            const u64 q = sum.warp_value();
-                            if (lane == g + x) kept = q;
-                        }
-                        g += kBatch;
-                    } else {
-                        u64 q = 0;
-                        for (int x0 = g * per; x0 < min((g + 1) * per, rounds); x0 += kBatch) {
-                            const int end = min((g + 1) * per, rounds);
-#pragma unroll
-                            for (int x = 0; x < kBatch; ++x)
-                                raw[x] = x0 + x >= end ? nothing : x0 + x < kHeld ? s.held[x0 + x][tid] : piece(x0 + x);
-                            MassSum sum;
-#pragma unroll
-                            for (int x = 0; x < kBatch; ++x) add_round(sum, raw[x], filter);
-                            q += sum.warp_value();
-                        }
-                        if (lane == g) kept = q;
-                        ++g;
-                    }
-                }
-            };
-            if (clean) sum_groups(false);
-            else sum_groups(true);
-            u64 q[4];
-            ok = exchange(warp_sum_u64(kept), q);
-            if (!ok) break;
-            const u64 mine = (q[0] + q[1]) + (q[2] + q[3]);
-            u64 before = mine;                             // inclusive, then ahead of this lane's warps
-            for (int d = 1; d < 32; d <<= 1) {
-                const u64 o = __shfl_up_sync(0xFFFFFFFFu, before, d);
-                if (lane >= d) before += o;
-            }
-            const u64 total = __shfl_sync(0xFFFFFFFFu, before, 31);
-            before -= mine;
             float u = a.u[static_cast<long long>(b) * t.N + node];
             if (!(u >= 0.0f && u < 1.0f)) {
                 flags |= DSPARK_STATUS_INPUT_RANGE;
                 u = u >= 1.0f ? 0x1.fffffep-1f : 0.0f;
             }
-            const u64 want = share_of(total, static_cast<uint32_t>(u * 0x1p24f));  // exact: a power of two, then the floor
-            // the warp whose part holds the share, and the mass ahead of it there
-            int owner = -1;
-            u64 rest = 0;
-#pragma unroll
-            for (int x = 0; x < 4; ++x) {
-                if (before <= want && want < before + q[x]) {
-                    owner = 4 * lane + x;
-                    rest = want - before;
-                }
-                before += q[x];
-            }
-            const int at = __ffs(__ballot_sync(0xFFFFFFFFu, owner >= 0)) - 1;      // some lane: want < total
-            owner = __shfl_sync(0xFFFFFFFFu, owner, at);
-            rest = __shfl_sync(0xFFFFFFFFu, rest, at);
-            u64 found = 0;                                 // the entry's id + 1, in the one warp that finds it
-            if (owner == self) {
-                u64 incl = kept;
+            const uint32_t share = static_cast<uint32_t>(u * 0x1p24f);        // exact: a power of two, then the floor
+            // Which of the lanes' values q, end to end, holds `rest`; leaves in `rest` what is behind its beginning (-1: none).
+            auto locate = [&](u64 q, u64& rest) {
+                u64 in = q;
                 for (int d = 1; d < 32; d <<= 1) {
-                    const u64 o = __shfl_up_sync(0xFFFFFFFFu, incl, d);
-                    if (lane >= d) incl += o;
+                    const u64 o = __shfl_up_sync(0xFFFFFFFFu, in, d);
+                    if (lane >= d) in += o;
                 }
-                const int g = __ffs(__ballot_sync(0xFFFFFFFFu, incl > rest)) - 1;
-                rest -= __shfl_sync(0xFFFFFFFFu, incl - kept, g);
-                for (int x = g * per; x < rounds; ++x) {
-                    float w[kPer];
-                    u64 sum = 0;
-                    weights(x < kHeld ? s.held[x][tid] : piece(x), w, !clean);
+                const uint32_t over = __ballot_sync(0xFFFFFFFFu, in > rest);
+                const int at = __ffs(over) - 1;
+                rest -= __shfl_sync(0xFFFFFFFFu, in - q, max(at, 0));
+                return at;
+            };
+            // The warp that holds the drawn share of the total of the blocks' sums; `of_warp` gives a warp's of this block.
+            auto owns = [&](u64 q, auto of_warp, u64& total, u64& rest) {
+                total = warp_sum_u64(q);
+                rest = share_of(total, share);
+                if (locate(q, rest) != rank) return false;
+                const int w = locate(lane < kWarps ? of_warp(lane) : 0, rest);
+                return (w < 0 ? kWarps - 1 : w) == warp;   // -1: behind all by a rounding; one has to answer
+            };
+
+            // ---- the first answer: from the fp32 sums, where their error cannot reach the entry's ends ----
+            // With r_v the real weight: the exact mass differs from 2^40 r_v by the roundings of (x - m) * inv, 2^-23 of
+            // up to 28 (what is smaller has no mass), expf's 2 ulp and the floor; the quick weight by those of the
+            // slope, 1.5 * 2^-24 of up to 41 in log2 units, of the multiply-add, 2^-24 of its result, and ex2's 2 ulp
+            // (a common factor counts for nothing); the sums by 2^-24 a step.  `slack` is more than all that.
+            const float far = (m - ref) * slope2.x;
+            const float reach = far >= 0.0f ? fmaxf(41.0f, far) : 41.0f - far;
+            const float eps = 7e-6f + 5e-8f * reach + 6e-8f * static_cast<float>(rounds * (kPer / 4) + 64) + 2e-12f * static_cast<float>(t.V);
+            const float most = float_from_order_bits(__reduce_max_sync(0xFFFFFFFFu, float_order_bits(block_sum)));
+            u64 found = 0;                                 // the entry's id + 1
+            if (clean && most >= 0x1p-60f && most < 0x1p60f) {
+                // fixed point, the largest sum between 2^53 and 2^54
+                const float unit = __uint_as_float((127u + 53u + 127u - (__float_as_uint(most) >> 23)) << 23);
+                auto fixed = [&](float x) { return __float2ull_rz(x * unit); };
+                const int last = (turn - 1) % kTurns;
+                u64 total, rest;
+                const bool here = owns(fixed(block_sum),
+                                       [&](int w) { return fixed(__uint_as_float(static_cast<uint32_t>(s.warp_pair[last][w].sum))); },
+                                       total, rest);
+                if (here) {
+                    const u64 slack = __float2ull_rz(eps * __ull2float_rn(total)) + 4096;
+                    const int g = locate(fixed(group_sum), rest);
+                    for (int x0 = g * per; g >= 0 && x0 < min((g + 1) * per, rounds); x0 += kGroup) {
+                        u64 part = 0;                      // lane x: the x-th round's
 #pragma unroll
-                    for (int e = 0; e < kPer; ++e) sum += mass_of(w[e]);
-                    u64 in = sum;
-                    for (int d = 1; d < 32; d <<= 1) {
-                        const u64 o = __shfl_up_sync(0xFFFFFFFFu, in, d);
-                        if (lane >= d) in += o;
+                        for (int x = 0; x < kGroup; ++x) {
+                            float v[kPer];
+                            Row<T>::unpack(x0 + x < rounds ? piece(x0 + x) : nothing, v);
+                            float2 w = quick(v, 0);
+#pragma unroll
+                            for (int e = 2; e < kPer; e += 2) w = __fadd2_rn(w, quick(v, e));
+                            float sum = w.x + w.y;
+                            for (int d = 16; d > 0; d >>= 1) sum += __shfl_xor_sync(0xFFFFFFFFu, sum, d);
+                            if (lane == x) part = fixed(sum);
+                        }
+                        const u64 before = rest;
+                        const int x = locate(part, rest);
+                        if (x < 0) {                       // in a later round
+                            rest = before - warp_sum_u64(part);
+                            continue;
+                        }
+                        float v[kPer];
+                        u64 w[kPer], sum = 0;
+                        Row<T>::unpack(x0 + x < rounds ? piece(x0 + x) : nothing, v);
+#pragma unroll
+                        for (int e = 0; e < kPer; e += 2) {
+                            const float2 z = quick(v, e);
+                            w[e] = fixed(z.x);
+                            w[e + 1] = fixed(z.y);
+                            sum += w[e] + w[e + 1];
+                        }
+                        const int l = locate(sum, rest);
+                        u64 from = 0;
+#pragma unroll
+                        for (int e = 0; e < kPer; ++e) {
+                            if (lane == l && rest >= from + slack && rest + slack < from + w[e])
+                                found = static_cast<u64>(row.id(piece_of(x0 + x)) + e) + 1;
+                            from += w[e];
+                        }
+                        found = warp_max_u64(found);
+                        break;
                     }
-                    const uint32_t over = __ballot_sync(0xFFFFFFFFu, in > rest);
-                    if (over == 0) {
-                        rest -= __shfl_sync(0xFFFFFFFFu, in, 31);
-                        continue;
+                }
+                ok = hear(here, found, found);
+                if (!ok) break;
+            }
+
+            if (found == 0) {
+                // ---- exact masses ----
+                const float2 shift = make_float2(-m, -m), slope = make_float2(inv, inv);
+                auto weights = [&](const uint4& raw, float* w) {   // the roundings of (x - m) * inv, two at once
+                    Row<T>::unpack(raw, w);
+#pragma unroll
+                    for (int e = 0; e < kPer; ++e) w[e] = w[e] < INFINITY ? w[e] : -INFINITY;
+#pragma unroll
+                    for (int e = 0; e < kPer; e += 2) {
+                        const float2 z = __fmul2_rn(__fadd2_rn(make_float2(w[e], w[e + 1]), shift), slope);
+                        w[e] = expf(z.x);
+                        w[e + 1] = expf(z.y);
                     }
-                    if (lane == __ffs(over) - 1) {
-                        u64 ahead = in - sum;
+                };
+                u64 kept = 0;
+                for (int g = 0; g * per < rounds; ++g) {
+                    const int end = min((g + 1) * per, rounds);
+                    u64 q = 0;
+                    for (int x0 = g * per; x0 < end; x0 += kBatch) {
+                        uint4 raw[kBatch];
+#pragma unroll
+                        for (int x = 0; x < kBatch; ++x) raw[x] = x0 + x < end ? piece(x0 + x) : nothing;
+                        MassSum sum;
+#pragma unroll
+                        for (int x = 0; x < kBatch; ++x) {
+                            float w[kPer];
+                            weights(raw[x], w);
+#pragma unroll
+                            for (int e = 0; e < kPer; e += 2) sum.add(make_float2(w[e], w[e + 1]));
+                            sum.count(kPer);
+                        }
+                        q += sum.warp_value();
+                    }
+                    if (lane == g) kept = q;
+                }
+                ok = exchange(0, warp_sum_u64(kept), [](u64 x, u64 y) { return x + y; }, all);
+                if (!ok) break;
+                const int last = (turn - 1) % kTurns;
+                u64 total, rest;
+                const bool here = owns(all.sum, [&](int w) { return s.warp_pair[last][w].sum; }, total, rest);
+                if (here) {
+                    const int g = locate(kept, rest);
+                    for (int x = g * per; x < rounds; ++x) {
+                        float w[kPer];
+                        u64 sum = 0;
+                        weights(piece(x), w);
+#pragma unroll
+                        for (int e = 0; e < kPer; ++e) sum += mass_of(w[e]);
+                        const u64 before = rest;
+                        const int l = locate(sum, rest);
+                        if (l < 0) {
+                            rest = before - warp_sum_u64(sum);
+                            continue;
+                        }
+                        u64 ahead = 0;
 #pragma unroll
                         for (int e = 0; e < kPer; ++e) {
                             const u64 qe = mass_of(w[e]);
-                            if (found == 0 && ahead + qe > rest) found = static_cast<u64>(row.id(piece_of(x)) + e) + 1;
+                            if (lane == l && found == 0 && ahead + qe > rest) found = static_cast<u64>(row.id(piece_of(x)) + e) + 1;
                             ahead += qe;
                         }
+                        found = warp_max_u64(found);
+                        break;
                     }
-                    found = __shfl_sync(0xFFFFFFFFu, found, __ffs(over) - 1);
-                    break;
                 }
+                ok = hear(here, found, found);
+                if (!ok) break;
             }
-            ok = exchange(found, all);
-            if (!ok) break;
-            y = static_cast<int>(warp_max_u64(max(max(all[0], all[1]), max(all[2], all[3])))) - 1;
+            y = static_cast<int>(found) - 1;
             child = child_of(node, y);
         }
 
@@ -496,7 +579,7 @@ __global__ void __launch_bounds__(32 * kWalkWarps) walk_tree_kernel(const __grid
 template <typename T>
 dspark_status launch_typed(const VerifyArgs& a, cudaStream_t stream) {
     cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3(static_cast<unsigned>(a.tree.B) * static_cast<unsigned>(a.cluster));
+    cfg.gridDim = dim3(static_cast<unsigned>(a.tree.B) << a.cluster_bits);
     cfg.blockDim = dim3(kThreads);
     cfg.dynamicSmemBytes = sizeof(Shared);
     cfg.stream = stream;
@@ -504,14 +587,14 @@ dspark_status launch_typed(const VerifyArgs& a, cudaStream_t stream) {
     at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
     at[0].val.programmaticStreamSerializationAllowed = 1;
     at[1].id = cudaLaunchAttributeClusterDimension;
-    at[1].val.clusterDim.x = static_cast<unsigned>(a.cluster);
+    at[1].val.clusterDim.x = 1u << a.cluster_bits;
     at[1].val.clusterDim.y = 1;
     at[1].val.clusterDim.z = 1;
     cfg.attrs = at;
-    cfg.numAttrs = a.cluster > 1 ? 2 : 1;
-    const auto kernel = a.cluster > 1 ? verify_tree_kernel<T, true> : verify_tree_kernel<T, false>;
+    cfg.numAttrs = a.cluster_bits > 0 ? 2 : 1;
+    const auto kernel = a.cluster_bits > 0 ? verify_tree_kernel<T, true> : verify_tree_kernel<T, false>;
     cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(sizeof(Shared)));
-    if (e == cudaSuccess && a.cluster > 8) e = cudaFuncSetAttribute(kernel, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
+    if (e == cudaSuccess && a.cluster_bits > 3) e = cudaFuncSetAttribute(kernel, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
     if (e == cudaSuccess) e = cudaLaunchKernelEx(&cfg, kernel, a);
     if (e != cudaSuccess) return cuda_error(e, "launch(verify_tree)");
     return DSPARK_OK;
@@ -529,10 +612,9 @@ dspark_status launch_verify_tree(const void* target, dspark_dtype dtype, const f
     a.temperature = temperature;
     a.u = u;
     // As many blocks per request as the SMs hold, while a block's part of a row stays worth an exchange.
-    a.cluster = 1;
-    while (a.cluster < kClusterMost && 2ll * a.cluster * B <= static_cast<long long>(kBlocks) * dev.sm_count &&
-           V / (2 * a.cluster) >= 4 * kThreads)
-        a.cluster *= 2;
+    while ((2 << a.cluster_bits) <= kClusterMost && static_cast<long long>(B) * (2 << a.cluster_bits) <= static_cast<long long>(kBlocks) * dev.sm_count &&
+           V / (2 << a.cluster_bits) >= 4 * kThreads)
+        ++a.cluster_bits;
     const dspark_status st = clear_header(ws, stream);
     if (st != DSPARK_OK) return st;
     return dtype == DSPARK_F32 ? launch_typed<float>(a, stream) : launch_typed<__nv_bfloat16>(a, stream);
