@@ -24,7 +24,7 @@ constexpr int kBlocks = 4;                 // per SM
 constexpr int kClusterMost = 16;
 constexpr int kGroup = 4;                  // rounds of 32 pieces, at least, whose sums a warp keeps apart
 constexpr int kBatch = 4;                  // 16-byte pieces that a thread looks at together
-constexpr int kHeld = 12;                  // pieces of a row that a thread holds in shared memory
+constexpr int kHeldGroups = 3, kHeld = kHeldGroups * kGroup;          // pieces of a row that a thread holds in shared memory
 
 struct VerifyArgs {
     TreeArgs tree;
@@ -207,8 +207,9 @@ __global__ void __launch_bounds__(kThreads, kBlocks) verify_tree_kernel(const __
             if (j >= whole0 && j < min(hi, whole1)) return __ldg(reinterpret_cast<const uint4*>(row.row + row.id(j)));
             return j < hi ? row.edge(j) : nothing;
         };
+        const float drawn = greedy ? 0.0f : a.u[static_cast<long long>(b) * t.N + node];
 #pragma unroll 4
-        for (int x = 0; x < held; ++x) {
+        for (int x = 0; x < (held + kGroup - 1) / kGroup * kGroup; ++x) {      // whole groups, with nothing behind the last round
             const int j = piece_of(x);
             if (j >= whole0 && j < min(hi, whole1)) copy_async(&s.held[x][tid], row.row + row.id(j));
             else s.held[x][tid] = j < hi ? row.edge(j) : nothing;
@@ -234,9 +235,12 @@ __global__ void __launch_bounds__(kThreads, kBlocks) verify_tree_kernel(const __
             const float2 z = __ffma2_rn(make_float2(v[e], v[e + 1]), slope2, shift2);
             return make_float2(exp2_approx(z.x), exp2_approx(z.y));
         };
-        const int per = max(kGroup, (rounds + 31) / 32);   // rounds of a group; lane g keeps the sum of the g-th
+        // Groups of rounds, whose sums lane g keeps of the g-th: kGroup rounds of those held, then `per` of the others.
+        const int per = max(kGroup, (rounds - kHeld + 31 - kHeldGroups) / (32 - kHeldGroups));
+        auto group_begin = [&](int g) { return g < kHeldGroups ? g * kGroup : kHeld + (g - kHeldGroups) * per; };
+        auto group_end = [&](int g) { return min(group_begin(g + 1), rounds); };
         float2 sum2[2] = {};
-        float group_sum = 0.0f, warp_sum = 0.0f;
+        float group_sum = 0.0f;
         float best = -INFINITY, odd_value = -INFINITY;     // odd_value: NaN where one is met
         int best_piece = -1;
         auto look = [&](const uint4& raw, int j) {
@@ -260,24 +264,47 @@ __global__ void __launch_bounds__(kThreads, kBlocks) verify_tree_kernel(const __
                 for (int e = 0; e < kPer; e += 2) sum2[(e >> 1) & 1] = __fadd2_rn(sum2[(e >> 1) & 1], quick(v, e));
             }
         };
+        auto lane_sum = [&]() {                            // of the group that has been looked at
+            const float sum = (sum2[0].x + sum2[0].y) + (sum2[1].x + sum2[1].y);
+            sum2[0] = sum2[1] = make_float2(0.0f, 0.0f);
+            return sum;
+        };
         copy_wait();
-        for (int g = 0; g * per < rounds; ++g) {
-            const int end = min((g + 1) * per, rounds);
-            for (int x0 = g * per; x0 < end; x0 += kBatch) {
+        float held_sum[kHeldGroups];
+#pragma unroll
+        for (int g = 0; g < kHeldGroups; ++g) {
+            held_sum[g] = 0.0f;
+            if (g * kGroup >= rounds) continue;
+#pragma unroll
+            for (int x = 0; x < kGroup; ++x) look(s.held[g * kGroup + x][tid], piece_of(g * kGroup + x));
+            held_sum[g] = lane_sum();
+        }
+        if (!greedy) {
+#pragma unroll
+            for (int d = 16; d > 0; d >>= 1)
+#pragma unroll
+                for (int g = 0; g < kHeldGroups; ++g) held_sum[g] += __shfl_xor_sync(0xFFFFFFFFu, held_sum[g], d);
+#pragma unroll
+            for (int g = 0; g < kHeldGroups; ++g)
+                if (lane == g) group_sum = held_sum[g];
+        }
+        for (int g = kHeldGroups; group_begin(g) < rounds; ++g) {
+            const int end = group_end(g);
+            for (int x0 = group_begin(g); x0 < end; x0 += kBatch) {
                 uint4 raw[kBatch];
 #pragma unroll
-                for (int x = 0; x < kBatch; ++x) raw[x] = x0 + x < end ? piece(x0 + x) : nothing;
+                for (int x = 0; x < kBatch; ++x) raw[x] = x0 + x < end ? load(piece_of(x0 + x)) : nothing;
 #pragma unroll
                 for (int x = 0; x < kBatch; ++x) look(raw[x], piece_of(x0 + x));
             }
-            if (!greedy) {
-                float sum = (sum2[0].x + sum2[0].y) + (sum2[1].x + sum2[1].y);
-                for (int d = 16; d > 0; d >>= 1) sum += __shfl_xor_sync(0xFFFFFFFFu, sum, d);
-                if (lane == g) group_sum = sum;
-                warp_sum += sum;
-                sum2[0] = sum2[1] = make_float2(0.0f, 0.0f);
-            }
+            if (greedy) continue;
+            float sum = lane_sum();
+            for (int d = 16; d > 0; d >>= 1) sum += __shfl_xor_sync(0xFFFFFFFFu, sum, d);
+            if (lane == g) group_sum = sum;
         }
+        float warp_sum = group_sum;
+        if (!greedy)
+            for (int d = 16; d > 0; d >>= 1) warp_sum += __shfl_xor_sync(0xFFFFFFFFu, warp_sum, d);
         bool clean = __all_sync(0xFFFFFFFFu, odd_value < INFINITY);           // no NaN, no +infinity
         if (!clean) {                                      // once more without them
             best = -INFINITY;
@@ -325,31 +352,31 @@ __global__ void __launch_bounds__(kThreads, kBlocks) verify_tree_kernel(const __
                     prefetch_l2(next.row + next.id(j));
             }
             const float m = float_from_order_bits(static_cast<uint32_t>(key >> 32));
-            float u = a.u[static_cast<long long>(b) * t.N + node];
+            float u = drawn;
             if (!(u >= 0.0f && u < 1.0f)) {
                 flags |= DSPARK_STATUS_INPUT_RANGE;
                 u = u >= 1.0f ? 0x1.fffffep-1f : 0.0f;
             }
             const uint32_t share = static_cast<uint32_t>(u * 0x1p24f);        // exact: a power of two, then the floor
             // Which of the lanes' values q, end to end, holds `rest`; leaves in `rest` what is behind its beginning (-1: none).
-            auto locate = [&](u64 q, u64& rest) {
-                u64 in = q;
+            auto locate = [&](auto q, auto& rest) {
+                auto in = q;
+#pragma unroll
                 for (int d = 1; d < 32; d <<= 1) {
-                    const u64 o = __shfl_up_sync(0xFFFFFFFFu, in, d);
+                    const auto o = __shfl_up_sync(0xFFFFFFFFu, in, d);
                     if (lane >= d) in += o;
                 }
-                const uint32_t over = __ballot_sync(0xFFFFFFFFu, in > rest);
-                const int at = __ffs(over) - 1;
-                rest -= __shfl_sync(0xFFFFFFFFu, in - q, max(at, 0));
+                const int at = __ffs(__ballot_sync(0xFFFFFFFFu, in > rest)) - 1;
+                if (at > 0) rest -= __shfl_sync(0xFFFFFFFFu, in, at - 1);
                 return at;
             };
-            // The warp that holds the drawn share of the total of the blocks' sums; `of_warp` gives a warp's of this block.
-            auto owns = [&](u64 q, auto of_warp, u64& total, u64& rest) {
-                total = warp_sum_u64(q);
-                rest = share_of(total, share);
-                if (locate(q, rest) != rank) return false;
-                const int w = locate(lane < kWarps ? of_warp(lane) : 0, rest);
-                return (w < 0 ? kWarps - 1 : w) == warp;   // -1: behind all by a rounding; one has to answer
+            // Whether this warp holds `rest`, given the blocks' values and the warps' of this block; exactly one does (where
+            // a rounding leaves it behind all, the last).
+            auto owns = [&](auto of_blocks, auto of_warps, auto& rest) {
+                const int r = locate(of_blocks, rest);
+                if ((r < 0 ? C - 1 : r) != rank) return false;
+                const int w = locate(of_warps, rest);
+                return (w < 0 ? kWarps - 1 : w) == warp;
             };
 
             // ---- the first answer: from the fp32 sums, where their error cannot reach the entry's ends ----
@@ -360,22 +387,18 @@ __global__ void __launch_bounds__(kThreads, kBlocks) verify_tree_kernel(const __
             const float far = (m - ref) * slope2.x;
             const float reach = far >= 0.0f ? fmaxf(41.0f, far) : 41.0f - far;
             const float eps = 7e-6f + 5e-8f * reach + 6e-8f * static_cast<float>(rounds * (kPer / 4) + 64) + 2e-12f * static_cast<float>(t.V);
-            const float most = float_from_order_bits(__reduce_max_sync(0xFFFFFFFFu, float_order_bits(block_sum)));
+            float total = block_sum;
+            for (int d = 16; d > 0; d >>= 1) total += __shfl_xor_sync(0xFFFFFFFFu, total, d);
             u64 found = 0;                                 // the entry's id + 1
-            if (clean && most >= 0x1p-60f && most < 0x1p60f) {
-                // fixed point, the largest sum between 2^53 and 2^54
-                const float unit = __uint_as_float((127u + 53u + 127u - (__float_as_uint(most) >> 23)) << 23);
-                auto fixed = [&](float x) { return __float2ull_rz(x * unit); };
+            if (clean && total > 0x1p-60f && total < 0x1p100f) {
                 const int last = (turn - 1) % kTurns;
-                u64 total, rest;
-                const bool here = owns(fixed(block_sum),
-                                       [&](int w) { return fixed(__uint_as_float(static_cast<uint32_t>(s.warp_pair[last][w].sum))); },
-                                       total, rest);
+                float rest = total * u;
+                const bool here = owns(block_sum, lane < kWarps ? __uint_as_float(static_cast<uint32_t>(s.warp_pair[last][lane].sum)) : 0.0f, rest);
                 if (here) {
-                    const u64 slack = __float2ull_rz(eps * __ull2float_rn(total)) + 4096;
-                    const int g = locate(fixed(group_sum), rest);
-                    for (int x0 = g * per; g >= 0 && x0 < min((g + 1) * per, rounds); x0 += kGroup) {
-                        u64 part = 0;                      // lane x: the x-th round's
+                    const float slack = eps * total;
+                    const int g = locate(group_sum, rest);
+                    for (int x0 = group_begin(g); g >= 0 && x0 < group_end(g); x0 += kGroup) {
+                        float part[kGroup];
 #pragma unroll
                         for (int x = 0; x < kGroup; ++x) {
                             float v[kPer];
@@ -383,35 +406,41 @@ __global__ void __launch_bounds__(kThreads, kBlocks) verify_tree_kernel(const __
                             float2 w = quick(v, 0);
 #pragma unroll
                             for (int e = 2; e < kPer; e += 2) w = __fadd2_rn(w, quick(v, e));
-                            float sum = w.x + w.y;
-                            for (int d = 16; d > 0; d >>= 1) sum += __shfl_xor_sync(0xFFFFFFFFu, sum, d);
-                            if (lane == x) part = fixed(sum);
+                            part[x] = w.x + w.y;
                         }
-                        const u64 before = rest;
-                        const int x = locate(part, rest);
-                        if (x < 0) {                       // in a later round
-                            rest = before - warp_sum_u64(part);
-                            continue;
+#pragma unroll
+                        for (int d = 1; d < 32; d <<= 1)                      // inclusive sums over the lanes, round by round
+#pragma unroll
+                            for (int x = 0; x < kGroup; ++x) {
+                                const float o = __shfl_up_sync(0xFFFFFFFFu, part[x], d);
+                                if (lane >= d) part[x] += o;
+                            }
+                        int at = -1;
+                        uint32_t over = 0;
+#pragma unroll
+                        for (int x = 0; x < kGroup; ++x) {
+                            if (at >= 0) continue;
+                            over = __ballot_sync(0xFFFFFFFFu, part[x] > rest);
+                            if (over != 0) {
+                                at = x;
+                                if (over & 1u) continue;
+                                rest -= __shfl_sync(0xFFFFFFFFu, part[x], __ffs(over) - 2);
+                            } else {
+                                rest -= __shfl_sync(0xFFFFFFFFu, part[x], 31);
+                            }
                         }
-                        float v[kPer];
-                        u64 w[kPer], sum = 0;
-                        Row<T>::unpack(x0 + x < rounds ? piece(x0 + x) : nothing, v);
+                        if (at < 0) continue;              // in a later round
+                        float v[kPer], from = 0.0f;
+                        Row<T>::unpack(piece(x0 + at), v);
 #pragma unroll
                         for (int e = 0; e < kPer; e += 2) {
-                            const float2 z = quick(v, e);
-                            w[e] = fixed(z.x);
-                            w[e + 1] = fixed(z.y);
-                            sum += w[e] + w[e + 1];
+                            const float2 w = quick(v, e);
+                            if (rest >= from + slack && rest + slack < from + w.x) found = static_cast<u64>(row.id(piece_of(x0 + at)) + e) + 1;
+                            from += w.x;
+                            if (rest >= from + slack && rest + slack < from + w.y) found = static_cast<u64>(row.id(piece_of(x0 + at)) + e) + 2;
+                            from += w.y;
                         }
-                        const int l = locate(sum, rest);
-                        u64 from = 0;
-#pragma unroll
-                        for (int e = 0; e < kPer; ++e) {
-                            if (lane == l && rest >= from + slack && rest + slack < from + w[e])
-                                found = static_cast<u64>(row.id(piece_of(x0 + x)) + e) + 1;
-                            from += w[e];
-                        }
-                        found = warp_max_u64(found);
+                        found = __shfl_sync(0xFFFFFFFFu, found, __ffs(over) - 1);
                         break;
                     }
                 }
@@ -434,10 +463,10 @@ __global__ void __launch_bounds__(kThreads, kBlocks) verify_tree_kernel(const __
                     }
                 };
                 u64 kept = 0;
-                for (int g = 0; g * per < rounds; ++g) {
-                    const int end = min((g + 1) * per, rounds);
+                for (int g = 0; group_begin(g) < rounds; ++g) {
+                    const int end = group_end(g);
                     u64 q = 0;
-                    for (int x0 = g * per; x0 < end; x0 += kBatch) {
+                    for (int x0 = group_begin(g); x0 < end; x0 += kBatch) {
                         uint4 raw[kBatch];
 #pragma unroll
                         for (int x = 0; x < kBatch; ++x) raw[x] = x0 + x < end ? piece(x0 + x) : nothing;
@@ -457,20 +486,19 @@ __global__ void __launch_bounds__(kThreads, kBlocks) verify_tree_kernel(const __
                 ok = exchange(0, warp_sum_u64(kept), [](u64 x, u64 y) { return x + y; }, all);
                 if (!ok) break;
                 const int last = (turn - 1) % kTurns;
-                u64 total, rest;
-                const bool here = owns(all.sum, [&](int w) { return s.warp_pair[last][w].sum; }, total, rest);
+                u64 rest = share_of(warp_sum_u64(all.sum), share);
+                const bool here = owns(all.sum, lane < kWarps ? s.warp_pair[last][lane].sum : 0, rest);
                 if (here) {
                     const int g = locate(kept, rest);
-                    for (int x = g * per; x < rounds; ++x) {
+                    for (int x = group_begin(g); x < rounds; ++x) {
                         float w[kPer];
                         u64 sum = 0;
                         weights(piece(x), w);
 #pragma unroll
                         for (int e = 0; e < kPer; ++e) sum += mass_of(w[e]);
-                        const u64 before = rest;
                         const int l = locate(sum, rest);
                         if (l < 0) {
-                            rest = before - warp_sum_u64(sum);
+                            rest -= warp_sum_u64(sum);
                             continue;
                         }
                         u64 ahead = 0;
@@ -487,8 +515,10 @@ __global__ void __launch_bounds__(kThreads, kBlocks) verify_tree_kernel(const __
                 ok = hear(here, found, found);
                 if (!ok) break;
             }
-            y = static_cast<int>(found) - 1;
-            child = child_of(node, y);
+            if (static_cast<int>(found) - 1 != y) {
+                y = static_cast<int>(found) - 1;
+                child = child_of(node, y);
+            }
         }
 
         if (tid == 0) {
