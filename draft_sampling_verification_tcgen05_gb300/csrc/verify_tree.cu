@@ -22,9 +22,8 @@ constexpr int kWarpBits = 3, kWarps = 1 << kWarpBits;
 static_assert(kThreads == 32 * kWarps, "warps of a block");
 constexpr int kBlocks = 4;                 // per SM
 constexpr int kClusterMost = 16;
-constexpr int kGroup = 4;                  // rounds of 32 pieces, at least, whose sums a warp keeps apart
-constexpr int kBatch = 4;                  // 16-byte pieces that a thread looks at together
-constexpr int kHeldGroups = 3, kHeld = kHeldGroups * kGroup;          // pieces of a row that a thread holds in shared memory
+constexpr int kGroup = 4;                  // rounds of 32 pieces that are loaded and looked at together
+constexpr int kHeld = 3;                   // groups in shared memory: under way, or the last ones
 
 struct VerifyArgs {
     TreeArgs tree;
@@ -37,7 +36,7 @@ constexpr int kTurns = 4;
 struct alignas(16) Pair { u64 key, sum; };
 
 struct Shared {
-    uint4 held[kHeld][kThreads];
+    uint4 held[kHeld][kGroup][kThreads];
     Pair pair[kTurns][kClusterMost];       // what the cluster's blocks tell each other, kTurns exchanges in turn
     Pair warp_pair[kTurns][kWarps];
     int parent[kTreeMost], token[kTreeMost];
@@ -50,7 +49,9 @@ constexpr long long kUnderWayNs = 100000;  // far more than a store into another
 __device__ __forceinline__ void copy_async(void* to, const void* from) {
     asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" :: "r"(smem_u32(to)), "l"(from) : "memory");
 }
-__device__ __forceinline__ void copy_wait() { asm volatile("cp.async.wait_all;" ::: "memory"); }
+__device__ __forceinline__ void copy_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int kLeft>
+__device__ __forceinline__ void copy_wait() { asm volatile("cp.async.wait_group %0;" :: "n"(kLeft) : "memory"); }
 
 // The largest of three; NaN where one is NaN.
 __device__ __forceinline__ float max3_nan(float x, float y, float z) {
@@ -195,26 +196,35 @@ __global__ void __launch_bounds__(kThreads, kBlocks) verify_tree_kernel(const __
     for (int k = 0; k < n; ++k) {
         auto row_of = [&](int i) { return Row<T>(static_cast<const T*>(a.target) + (static_cast<long long>(b) * t.N + i) * t.V, t.V); };
         const Row<T> row = row_of(node);
-        // this warp's pieces, in rounds of 32; the first kHeld rounds stay in shared memory
+        // this warp's pieces, in rounds of 32 and groups of rounds
         auto first_piece = [&](const Row<T>& r, int w) { return static_cast<int>((static_cast<long long>(r.pieces()) * w) >> warp_bits); };
         const int lo = first_piece(row, self), hi = first_piece(row, self + 1);
-        const int rounds = (hi - lo + 31) / 32;
-        const int held = min(rounds, kHeld);
+        const int rounds = (hi - lo + 31) / 32, groups = (rounds + kGroup - 1) / kGroup;
         auto piece_of = [&](int x) { return lo + 32 * x + lane; };
-        const uint4 nothing = Row<T>::nothing();           // where the last round has no piece for a lane
+        const uint4 nothing = Row<T>::nothing();           // behind the last piece
         const int whole0 = row.first_whole(), whole1 = row.behind_whole();
-        auto load = [&](int j) {
+        auto start = [&](int g) {                          // a group's loads; an empty one behind the last keeps the count
+            if (g < groups) {
+#pragma unroll
+                for (int x = 0; x < kGroup; ++x) {
+                    const int j = piece_of(g * kGroup + x);
+                    uint4* to = &s.held[g % kHeld][x][tid];
+                    if (j >= whole0 && j < min(hi, whole1)) copy_async(to, row.row + row.id(j));
+                    else *to = j < hi ? row.edge(j) : nothing;
+                }
+            }
+            copy_commit();
+        };
+        // a round again, after the pass: from shared memory, or from the L2 cache
+        auto piece = [&](int x) {
+            const int j = piece_of(x);
+            if (x / kGroup >= groups - kHeld) return s.held[x / kGroup % kHeld][x % kGroup][tid];
             if (j >= whole0 && j < min(hi, whole1)) return __ldg(reinterpret_cast<const uint4*>(row.row + row.id(j)));
             return j < hi ? row.edge(j) : nothing;
         };
         const float drawn = greedy ? 0.0f : a.u[static_cast<long long>(b) * t.N + node];
-#pragma unroll 4
-        for (int x = 0; x < (held + kGroup - 1) / kGroup * kGroup; ++x) {      // whole groups, with nothing behind the last round
-            const int j = piece_of(x);
-            if (j >= whole0 && j < min(hi, whole1)) copy_async(&s.held[x][tid], row.row + row.id(j));
-            else s.held[x][tid] = j < hi ? row.edge(j) : nothing;
-        }
-        auto piece = [&](int x) { return x < kHeld ? s.held[x][tid] : load(piece_of(x)); };
+#pragma unroll
+        for (int g = 0; g < kHeld; ++g) start(g);
 
         // ---- one pass: the largest entry, the first of equal ones; without greed sums of weights for a first answer ----
         // These weights are relative to `ref`, the largest of the row's first pieces, which all warps look at.
@@ -235,14 +245,12 @@ __global__ void __launch_bounds__(kThreads, kBlocks) verify_tree_kernel(const __
             const float2 z = __ffma2_rn(make_float2(v[e], v[e + 1]), slope2, shift2);
             return make_float2(exp2_approx(z.x), exp2_approx(z.y));
         };
-        // Groups of rounds, whose sums lane g keeps of the g-th: kGroup rounds of those held, then `per` of the others.
-        const int per = max(kGroup, (rounds - kHeld + 31 - kHeldGroups) / (32 - kHeldGroups));
-        auto group_begin = [&](int g) { return g < kHeldGroups ? g * kGroup : kHeld + (g - kHeldGroups) * per; };
-        auto group_end = [&](int g) { return min(group_begin(g + 1), rounds); };
+        const int per = (groups + 31) / 32;                // lane l keeps the sums of `per` groups together, the l-th such
         float2 sum2[2] = {};
         float group_sum = 0.0f;
         float best = -INFINITY, odd_value = -INFINITY;     // odd_value: NaN where one is met
-        int best_piece = -1;
+        int best_piece = lo;
+        uint4 best_raw = nothing;
         auto look = [&](const uint4& raw, int j) {
             float v[kPer];
             Row<T>::unpack(raw, v);
@@ -258,6 +266,7 @@ __global__ void __launch_bounds__(kThreads, kBlocks) verify_tree_kernel(const __
             if (top > best) {
                 best = top;
                 best_piece = j;
+                best_raw = raw;
             }
             if (!greedy) {
 #pragma unroll
@@ -269,38 +278,26 @@ __global__ void __launch_bounds__(kThreads, kBlocks) verify_tree_kernel(const __
             sum2[0] = sum2[1] = make_float2(0.0f, 0.0f);
             return sum;
         };
-        copy_wait();
-        float held_sum[kHeldGroups];
+        for (int g0 = 0; g0 < groups; g0 += kHeld) {
+            float sum[kHeld];
 #pragma unroll
-        for (int g = 0; g < kHeldGroups; ++g) {
-            held_sum[g] = 0.0f;
-            if (g * kGroup >= rounds) continue;
+            for (int g = 0; g < kHeld; ++g) {
+                sum[g] = 0.0f;
+                if (g0 + g >= groups) continue;
+                copy_wait<kHeld - 1>();
 #pragma unroll
-            for (int x = 0; x < kGroup; ++x) look(s.held[g * kGroup + x][tid], piece_of(g * kGroup + x));
-            held_sum[g] = lane_sum();
-        }
-        if (!greedy) {
+                for (int x = 0; x < kGroup; ++x) look(s.held[g][x][tid], piece_of((g0 + g) * kGroup + x));
+                sum[g] = lane_sum();
+                start(g0 + g + kHeld);
+            }
+            if (greedy) continue;
 #pragma unroll
             for (int d = 16; d > 0; d >>= 1)
 #pragma unroll
-                for (int g = 0; g < kHeldGroups; ++g) held_sum[g] += __shfl_xor_sync(0xFFFFFFFFu, held_sum[g], d);
+                for (int g = 0; g < kHeld; ++g) sum[g] += __shfl_xor_sync(0xFFFFFFFFu, sum[g], d);
 #pragma unroll
-            for (int g = 0; g < kHeldGroups; ++g)
-                if (lane == g) group_sum = held_sum[g];
-        }
-        for (int g = kHeldGroups; group_begin(g) < rounds; ++g) {
-            const int end = group_end(g);
-            for (int x0 = group_begin(g); x0 < end; x0 += kBatch) {
-                uint4 raw[kBatch];
-#pragma unroll
-                for (int x = 0; x < kBatch; ++x) raw[x] = x0 + x < end ? load(piece_of(x0 + x)) : nothing;
-#pragma unroll
-                for (int x = 0; x < kBatch; ++x) look(raw[x], piece_of(x0 + x));
-            }
-            if (greedy) continue;
-            float sum = lane_sum();
-            for (int d = 16; d > 0; d >>= 1) sum += __shfl_xor_sync(0xFFFFFFFFu, sum, d);
-            if (lane == g) group_sum = sum;
+            for (int g = 0; g < kHeld; ++g)
+                if (lane == (per == 1 ? g0 + g : (g0 + g) / per)) group_sum += sum[g];
         }
         float warp_sum = group_sum;
         if (!greedy)
@@ -308,22 +305,25 @@ __global__ void __launch_bounds__(kThreads, kBlocks) verify_tree_kernel(const __
         bool clean = __all_sync(0xFFFFFFFFu, odd_value < INFINITY);           // no NaN, no +infinity
         if (!clean) {                                      // once more without them
             best = -INFINITY;
-            best_piece = -1;
             for (int x = 0; x < rounds; ++x) {
                 float v[kPer];
-                Row<T>::unpack(piece(x), v);
+                const uint4 raw = piece(x);
+                Row<T>::unpack(raw, v);
+                float top = -INFINITY;
 #pragma unroll
                 for (int e = 0; e < kPer; ++e)
-                    if (v[e] < INFINITY && v[e] > best) {
-                        best = v[e];
-                        best_piece = piece_of(x);
-                    }
+                    if (v[e] < INFINITY) top = fmaxf(top, v[e]);
+                if (top > best) {
+                    best = top;
+                    best_piece = piece_of(x);
+                    best_raw = raw;
+                }
             }
         }
         u64 key = 0;                                       // 0: nothing finite
-        if (best_piece >= 0) {
+        if (best > -INFINITY) {
             float v[kPer];
-            Row<T>::unpack(piece((best_piece - lo) >> 5), v);
+            Row<T>::unpack(best_raw, v);
 #pragma unroll
             for (int e = kPer - 1; e >= 0; --e)
                 if (v[e] == best) key = argmax_key(best, static_cast<uint32_t>(row.id(best_piece) + e));
@@ -396,8 +396,8 @@ __global__ void __launch_bounds__(kThreads, kBlocks) verify_tree_kernel(const __
                 const bool here = owns(block_sum, lane < kWarps ? __uint_as_float(static_cast<uint32_t>(s.warp_pair[last][lane].sum)) : 0.0f, rest);
                 if (here) {
                     const float slack = eps * total;
-                    const int g = locate(group_sum, rest);
-                    for (int x0 = group_begin(g); g >= 0 && x0 < group_end(g); x0 += kGroup) {
+                    const int l = locate(group_sum, rest);
+                    for (int x0 = l * per * kGroup; l >= 0 && x0 < min((l + 1) * per * kGroup, rounds); x0 += kGroup) {
                         float part[kGroup];
 #pragma unroll
                         for (int x = 0; x < kGroup; ++x) {
@@ -463,25 +463,21 @@ __global__ void __launch_bounds__(kThreads, kBlocks) verify_tree_kernel(const __
                     }
                 };
                 u64 kept = 0;
-                for (int g = 0; group_begin(g) < rounds; ++g) {
-                    const int end = group_end(g);
-                    u64 q = 0;
-                    for (int x0 = group_begin(g); x0 < end; x0 += kBatch) {
-                        uint4 raw[kBatch];
+                for (int g = 0; g < groups; ++g) {
+                    uint4 raw[kGroup];
 #pragma unroll
-                        for (int x = 0; x < kBatch; ++x) raw[x] = x0 + x < end ? piece(x0 + x) : nothing;
-                        MassSum sum;
+                    for (int x = 0; x < kGroup; ++x) raw[x] = piece(g * kGroup + x);
+                    MassSum sum;
 #pragma unroll
-                        for (int x = 0; x < kBatch; ++x) {
-                            float w[kPer];
-                            weights(raw[x], w);
+                    for (int x = 0; x < kGroup; ++x) {
+                        float w[kPer];
+                        weights(raw[x], w);
 #pragma unroll
-                            for (int e = 0; e < kPer; e += 2) sum.add(make_float2(w[e], w[e + 1]));
-                            sum.count(kPer);
-                        }
-                        q += sum.warp_value();
+                        for (int e = 0; e < kPer; e += 2) sum.add(make_float2(w[e], w[e + 1]));
+                        sum.count(kPer);
                     }
-                    if (lane == g) kept = q;
+                    const u64 q = sum.warp_value();
+                    if (lane == (per == 1 ? g : g / per)) kept += q;
                 }
                 ok = exchange(0, warp_sum_u64(kept), [](u64 x, u64 y) { return x + y; }, all);
                 if (!ok) break;
@@ -489,8 +485,7 @@ __global__ void __launch_bounds__(kThreads, kBlocks) verify_tree_kernel(const __
                 u64 rest = share_of(warp_sum_u64(all.sum), share);
                 const bool here = owns(all.sum, lane < kWarps ? s.warp_pair[last][lane].sum : 0, rest);
                 if (here) {
-                    const int g = locate(kept, rest);
-                    for (int x = group_begin(g); x < rounds; ++x) {
+                    for (int x = locate(kept, rest) * per * kGroup; x < rounds; ++x) {
                         float w[kPer];
                         u64 sum = 0;
                         weights(piece(x), w);
@@ -532,7 +527,7 @@ __global__ void __launch_bounds__(kThreads, kBlocks) verify_tree_kernel(const __
 
     if constexpr (kCluster) {                              // no block ends while another still stores into it
         if (!ok) {
-            copy_wait();
+            copy_wait<0>();
             const long long t0 = global_ns();
             while (global_ns() - t0 < kUnderWayNs) {
             }
