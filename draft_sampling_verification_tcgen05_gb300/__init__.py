@@ -718,29 +718,33 @@ def dspark_tree_attention(q, k_cache, v_cache, block_table, kv_len, parents, sca
     return out
 
 
+def _given(t, name, like_shape):
+    """An int32 output that the caller has given."""
+    _need(t, name, (_torch().int32,))
+    if t.shape != like_shape:
+        raise ValueError(f"{name} must be {list(like_shape)}")
+    return t
+
+
 def _tree(parents, draft_tokens, lengths, out_tokens, num_accepted, path):
     """Checks a tree and its outputs; returns (out_tokens, num_accepted, path)."""
     torch = _torch()
     i32 = (torch.int32,)
     _need(draft_tokens, "draft_tokens", i32, 2)
     _need(parents, "parents", i32, 2)
-    B, N = draft_tokens.shape
-    if parents.shape != (B, N):
+    shape = draft_tokens.shape
+    if parents.shape != shape:
         raise ValueError("parents and draft_tokens must be [B, N]")
     if lengths is not None:
         _need(lengths, "lengths", i32, 1)
-        if len(lengths) != B:
+        if lengths.shape[0] != shape[0]:
             raise ValueError("lengths must be [B]")
-    out = []
-    for t, name, shape in ((out_tokens, "out_tokens", (B, N)), (num_accepted, "num_accepted", (B,)), (path, "path", (B, N))):
-        if t is None:
-            t = torch.empty(shape, dtype=torch.int32, device=draft_tokens.device)
-        else:
-            _need(t, name, i32, len(shape))
-            if t.shape != shape:
-                raise ValueError(f"{name} must be {list(shape)}")
-        out.append(t)
-    return out
+    if num_accepted is None:
+        num_accepted = torch.empty(shape[0], dtype=torch.int32, device=draft_tokens.device)
+    else:
+        _given(num_accepted, "num_accepted", shape[:1])
+    return (torch.empty_like(draft_tokens) if out_tokens is None else _given(out_tokens, "out_tokens", shape), num_accepted,
+            torch.empty_like(draft_tokens) if path is None else _given(path, "path", shape))
 
 
 @_on_its_stream
@@ -764,13 +768,13 @@ def dspark_verify_tree(target, parents, draft_tokens, temperature=None, u=None, 
         if u is None:
             raise ValueError("temperatures need the uniforms u [B, N]")
         _need(u, "u", (torch.float32,), 2)
-        if len(temperature) != B or u.shape != (B, N):
+        if temperature.shape[0] != B or u.shape != draft_tokens.shape:
             raise ValueError("temperature must be [B] and u [B, N]")
     ws = workspace if workspace is not None else Workspace(OP_VERIFY_TREE, B, N, device=target.device)
     _check(lib().dspark_verify_tree(_ptr(target), _dt(target), _ptr(temperature), _ptr(u), _ptr(parents), _ptr(draft_tokens),
                                     _ptr(lengths), B, N, V, _ptr(outs[0]), _ptr(outs[1]), _ptr(outs[2]), ws.address, ws.nbytes,
                                     _stream(stream)), "dspark_verify_tree")
-    return tuple(outs)
+    return outs
 
 
 @_on_its_stream
@@ -787,7 +791,7 @@ def dspark_verify_tree_tokens(target_tokens, parents, draft_tokens, lengths=None
     _check(lib().dspark_verify_tree_tokens(_ptr(target_tokens), _ptr(parents), _ptr(draft_tokens), _ptr(lengths), B, N,
                                            _ptr(outs[0]), _ptr(outs[1]), _ptr(outs[2]), ws.address, ws.nbytes,
                                            _stream(stream)), "dspark_verify_tree_tokens")
-    return tuple(outs)
+    return outs
 
 
 def _caches(k_cache, v_cache):
@@ -799,16 +803,17 @@ def _caches(k_cache, v_cache):
             raise TypeError(f"{name} must be a CUDA tensor")
         if t.dtype != torch.bfloat16 and t.dtype != torch.float16:
             raise TypeError(f"{name} has dtype {t.dtype}, expected torch.bfloat16 or torch.float16")
-        if t.dim() not in (4, 5) or t.numel() == 0 or not t[(0,) * (t.dim() - 4)].is_contiguous():
+        if t.ndim not in (4, 5) or not (t.is_contiguous() or (t.ndim == 5 and t.shape[0] > 0 and t[0].is_contiguous())):
             raise ValueError(f"{name} must be [num_pages, Hkv, page_size, D], or [layers, ...] of such, contiguous within a layer")
-    if v_cache.shape != k_cache.shape or v_cache.dtype != k_cache.dtype:
+    shape = k_cache.shape
+    if v_cache.shape != shape or v_cache.dtype != k_cache.dtype:
         raise ValueError("k_cache and v_cache must have the same shape and dtype")
-    shape = tuple(k_cache.shape[-4:])
-    layers = k_cache.shape[0] if k_cache.dim() == 5 else 1
-    stride = k_cache.stride(0) if layers > 1 else shape[0] * shape[1] * shape[2] * shape[3]
-    if layers > 1 and v_cache.stride(0) != stride:
+    if k_cache.ndim == 4:
+        return (1, 0, *shape)
+    stride = k_cache.stride(0)
+    if shape[0] > 1 and v_cache.stride(0) != stride:
         raise ValueError("k_cache and v_cache must have the same layer stride")
-    return (layers, stride) + shape
+    return (shape[0], stride if shape[0] > 1 else 0, *shape[1:])
 
 
 @_on_its_stream
@@ -825,18 +830,13 @@ def dspark_kv_compact(k_cache, v_cache, block_table, kv_len, path, num_accepted,
     _need(path, "path", i32, 2)
     _need(num_accepted, "num_accepted", i32, 1)
     B, N = path.shape
-    if block_table.shape[0] != B or len(kv_len) != B or len(num_accepted) != B:
+    if block_table.shape[0] != B or kv_len.shape[0] != B or num_accepted.shape[0] != B:
         raise ValueError("shapes: block_table [B, max_pages], kv_len / num_accepted [B], path [B, N]")
     if lengths is not None:
         _need(lengths, "lengths", i32, 1)
-        if len(lengths) != B:
+        if lengths.shape[0] != B:
             raise ValueError("lengths must be [B]")
-    if kv_len_out is None:
-        kv_len_out = torch.empty_like(kv_len)
-    else:
-        _need(kv_len_out, "kv_len_out", i32, 1)
-        if len(kv_len_out) != B:
-            raise ValueError("kv_len_out must be [B]")
+    kv_len_out = torch.empty_like(kv_len) if kv_len_out is None else _given(kv_len_out, "kv_len_out", kv_len.shape)
     ws = workspace if workspace is not None else Workspace(OP_KV_COMPACT, device=k_cache.device)
     _check(lib().dspark_kv_compact(_ptr(k_cache), _ptr(v_cache), layers, stride, _ptr(block_table), block_table.shape[1],
                                    _ptr(kv_len), _ptr(lengths), _ptr(path), _ptr(num_accepted), B, N, Hkv, D, num_pages, page,
@@ -853,10 +853,10 @@ def dspark_kv_copy_pages(k_cache, v_cache, src, dst, used=None, workspace=None, 
     layers, stride, num_pages, Hkv, page, D = _caches(k_cache, v_cache)
     _need(src, "src", i32, 1)
     _need(dst, "dst", i32, 1)
-    M = len(src)
+    M = src.shape[0]
     if used is not None:
         _need(used, "used", i32, 1)
-    if len(dst) != M or (used is not None and len(used) != M):
+    if dst.shape[0] != M or (used is not None and used.shape[0] != M):
         raise ValueError("src, dst and used must be [M]")
     ws = workspace if workspace is not None else Workspace(OP_KV_COPY_PAGES, device=k_cache.device)
     _check(lib().dspark_kv_copy_pages(_ptr(k_cache), _ptr(v_cache), layers, stride, _ptr(src), _ptr(dst), _ptr(used), M, Hkv, D,
