@@ -1,24 +1,33 @@
-// dspark_tree_attention and dspark_window_attention: arguments and launches of the kernels of paged_attention.cuh
-// with masks.  Both go through one instantiation: the masks are looked at only in the tiles that a row does not see
-// as a whole, a tree's last one to three and the two ends of a window, so a switch at run time costs nothing.
-#include "paged_attention.cuh"
+// dspark_tree_attention and dspark_window_attention: arguments and launches of the kernels of paged_attention.cuh and
+// wide_attention.cuh with masks.  Both go through one instantiation: the masks are looked at only in the tiles that a
+// row does not see as a whole, a tree's last one to three and the two ends of a window, so a switch at run time costs
+// nothing.
+#include "wide_attention.cuh"
 
 namespace dspark {
 
 namespace {
 
 int words_of(int N) { return (N + 31) / 32; }
+int wide_cap_of(int N, int heads) { return static_cast<int>(std::min<long long>(2 * kTile, static_cast<long long>(N) * heads)); }
+
+template <typename T, int D>
+dspark_status launch(PagedArgs& a, int grid, cudaStream_t stream) {
+    // More rows than a tile holds: two tiles against one stream of keys and values.
+    if (a.N > a.tile_tokens) return launch_wide<T, D>(a, grid, stream);
+    return launch_typed<T, D, true>(a, grid, stream);
+}
 
 }  // namespace
 
 size_t tree_attention_workspace_bytes(int B, int N, int Hq, int D) {
     if (B < 1 || N < 1 || Hq < 1 || D < 1) return 0;
-    return partials_end(N, Hq, D) + static_cast<size_t>(B) * N * (words_of(N) + 1) * sizeof(uint32_t);
+    return partials_end(wide_cap_of(N, Hq), D) + static_cast<size_t>(B) * N * (words_of(N) + 1) * sizeof(uint32_t);
 }
 
 size_t window_attention_workspace_bytes(int B, int N, int Hq, int D) {
     if (B < 1 || N < 1 || Hq < 1 || D < 1) return 0;
-    return partials_end(N, Hq, D);
+    return partials_end(wide_cap_of(N, Hq), D);
 }
 
 dspark_status launch_masked_attention(const void* q, const void* k_cache, const void* v_cache, dspark_dtype dtype,
@@ -32,15 +41,16 @@ dspark_status launch_masked_attention(const void* q, const void* k_cache, const 
     }
     PagedArgs a = paged_args(q, k_cache, v_cache, block_table, max_pages, kv_len, lengths, scale, causal, B, N, Hq, Hkv, D,
                              num_pages, page, out, lse, ws);
+    a.rows_cap = wide_cap_of(N, Hq);
+    set_partials(a);
     a.parents = parents;
     a.words = words_of(N);
-    a.ancestors = reinterpret_cast<uint32_t*>(static_cast<uint8_t*>(ws) + partials_end(N, Hq, D));
+    a.ancestors = reinterpret_cast<uint32_t*>(static_cast<uint8_t*>(ws) + partials_end(a.rows_cap, D));
     a.window = std::min(window, 1 << 30);                  // as wide as a table can be: positions stay within 32 bits
     a.sinks = sinks;
     const int grid = std::min(dev.sm_count, kMaxCtas);
-    if (dtype == DSPARK_BF16)
-        return D == 64 ? launch_typed<__nv_bfloat16, 64, true>(a, grid, stream) : launch_typed<__nv_bfloat16, 128, true>(a, grid, stream);
-    return D == 64 ? launch_typed<__half, 64, true>(a, grid, stream) : launch_typed<__half, 128, true>(a, grid, stream);
+    if (dtype == DSPARK_BF16) return D == 64 ? launch<__nv_bfloat16, 64>(a, grid, stream) : launch<__nv_bfloat16, 128>(a, grid, stream);
+    return D == 64 ? launch<__half, 64>(a, grid, stream) : launch<__half, 128>(a, grid, stream);
 }
 
 }  // namespace dspark

@@ -5,7 +5,7 @@ namespace dspark {
 
 size_t paged_attention_workspace_bytes(int B, int N, int Hq, int D) {
     if (B < 1 || N < 1 || Hq < 1 || D < 1) return 0;
-    return partials_end(N, Hq, D);
+    return partials_end(rows_cap_of(N, Hq), D);
 }
 
 dspark_status launch_paged_attention(const void* q, const void* k_cache, const void* v_cache, dspark_dtype dtype,

@@ -51,6 +51,7 @@
 #include "host_common.h"
 
 #include <algorithm>
+#include <type_traits>
 
 namespace dspark {
 namespace {
@@ -86,6 +87,7 @@ struct PagedArgs {
     int max_pages, causal, B, N, Hq, Hkv, group, num_pages, page;
     int box_rows;                          // tokens of one TMA box: min(page, 128)
     int tile_tokens;                       // window tokens per row tile
+    int unit_tokens;                       // window tokens per unit: one row tile's, or two tiles' (wide_attention.cuh)
     int rows_cap;                          // rows of one partial result
     float scale;
     void* out;
@@ -112,7 +114,7 @@ __device__ __forceinline__ bool request(const PagedArgs& a, int b, int& kv, int&
 }
 
 __device__ __forceinline__ int tiles_of(int kv) { return (kv + kTile - 1) / kTile; }
-__device__ __forceinline__ int row_tiles_of(const PagedArgs& a, int n) { return (n + a.tile_tokens - 1) / a.tile_tokens; }
+__device__ __forceinline__ int row_tiles_of(const PagedArgs& a, int n) { return (n + a.unit_tokens - 1) / a.unit_tokens; }
 
 // The cache's tiles that row tile rt of a request reads (kMasked): the first `lead` of them (sinks), then those
 // from `first` on, `count` in all, at least one.  Tile t of the row tile is cache tile place(t).
@@ -122,9 +124,9 @@ struct Span {
     __device__ __forceinline__ int place(int t) const { return t < lead ? t : first + (t - lead); }
 };
 __device__ __forceinline__ Span span_of(const PagedArgs& a, int kv, int n, int rt) {
-    const int base = kv - n, i0 = rt * a.tile_tokens;
+    const int base = kv - n, i0 = rt * a.unit_tokens;
     Span s;
-    s.high = a.causal ? min(kv, base + min(n, i0 + a.tile_tokens)) : kv;
+    s.high = a.causal ? min(kv, base + min(n, i0 + a.unit_tokens)) : kv;
     // a tree's row may be as shallow as the root
     s.low = a.window > 0 ? max(0, base + (a.parents ? 0 : i0) - a.window + 1) : 0;
     s.first = s.low / kTile;
@@ -138,7 +140,7 @@ template <bool kMasked>
 __device__ __forceinline__ int unit_tiles(const PagedArgs& a, int kv, int n) {
     const int tiles = tiles_of(kv);
     if (!kMasked || a.window == 0) return tiles;
-    const long long width = static_cast<long long>(a.window) - 1 + (a.causal && !a.parents ? min(n, a.tile_tokens) : n);
+    const long long width = static_cast<long long>(a.window) - 1 + (a.causal && !a.parents ? min(n, a.unit_tokens) : n);
     // `width` tokens reach into (width - 2) / kTile + 2 tiles at most
     return static_cast<int>(min(static_cast<long long>(tiles), (width + kTile - 2) / kTile + 1 + tiles_of(min(a.sinks, kv))));
 }
@@ -1065,7 +1067,7 @@ paged_attention_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_con
 // ---------------------------------------------------------------------------
 constexpr int kJoinRows = 4;
 
-template <typename T, int D, bool kMasked>
+template <typename T, int D>
 __global__ void __launch_bounds__(kJoinRows * D) paged_join_kernel(const __grid_constant__ PagedArgs a) {
     __shared__ float s_f[kJoinRows][kMaxCtas], s_inv[kJoinRows];      // factor of each partial result, 1 / sum
     const int r = static_cast<int>(threadIdx.x) / D, col = static_cast<int>(threadIdx.x) % D;
@@ -1076,11 +1078,11 @@ __global__ void __launch_bounds__(kJoinRows * D) paged_join_kernel(const __grid_
     const int row = static_cast<int>(blockIdx.y) * kJoinRows + r;
     const int n = at.n, rt = at.rt, h = at.h, b = at.b;
     const int count = c < a.plan->ctas ? at.joined : 0;
-    const bool active = count > 0 && row < min(a.tile_tokens, n - rt * a.tile_tokens) * a.group;
+    const bool active = count > 0 && row < min(a.unit_tokens, n - rt * a.unit_tokens) * a.group;
     // the row's k-th partial result: CTA c - 1 opened the unit, the others went on with it
     const long long first = static_cast<long long>(2 * (c - 1) + 1) * a.rows_cap + row;
     const long long step = 2ll * a.rows_cap;
-    const int tok = rt * a.tile_tokens + row / a.group, head = h * a.group + row % a.group;
+    const int tok = rt * a.unit_tokens + row / a.group, head = h * a.group + row % a.group;
     const long long to = (static_cast<long long>(b) * a.N + tok) * a.Hq + head;
     // the first values are under way while the factors are found
     constexpr int kFirst = 8;
@@ -1134,7 +1136,86 @@ __global__ void __launch_bounds__(kJoinRows * D) paged_join_kernel(const __grid_
          w < static_cast<long long>(a.B) * a.N; w += warps) {
         const int rb = static_cast<int>(quotient(w, a.N)), i = static_cast<int>(w - static_cast<long long>(rb) * a.N);
         int kv, m;
-        request<kMasked>(a, rb, kv, m);
+        request<false>(a, rb, kv, m);
+        if (i < m) continue;
+        uint4* dst = reinterpret_cast<uint4*>(static_cast<T*>(a.out) + w * a.Hq * D);
+        for (int x = lane; x < a.Hq * (D / 8); x += 32) dst[x] = make_uint4(0u, 0u, 0u, 0u);
+        if (a.lse)
+            for (int x = lane; x < a.Hq; x += 32) a.lse[w * a.Hq + x] = -INFINITY;
+    }
+}
+
+// ---------------------------------------------------------------------------
+// Join with kMasked, whose units have up to 256 rows: a warp adds a row over the unit's partial results in order, a
+// lane D / 32 columns.  Block (c, y) takes every (gridDim.y)-th eight rows of the unit that CTA c's run begins inside
+// of.  (paged_join_kernel's block for every four rows took 45 us for two partial results of each of 38000 rows.)
+// ---------------------------------------------------------------------------
+constexpr int kRowJoinWarps = 8, kRowJoinHigh = 8;
+
+template <typename T, int D>
+__global__ void __launch_bounds__(32 * kRowJoinWarps) row_join_kernel(const __grid_constant__ PagedArgs a) {
+    constexpr int kCols = D / 32, kFirst = 8;
+    using Part = typename std::conditional<kCols == 4, float4, float2>::type;
+    const int lane = static_cast<int>(lane_id()), warp = static_cast<int>(warp_id());
+    grid_dependency_wait();
+    const int c = static_cast<int>(blockIdx.x) + 1;
+    const PlanEntry& at = a.plan->entry[c < kMaxCtas ? c : 0];
+    const int count = c < a.plan->ctas ? at.joined : 0;
+    const int rows = count > 0 ? min(a.unit_tokens, at.n - at.rt * a.unit_tokens) * a.group : 0;
+    for (int row = static_cast<int>(blockIdx.y) * kRowJoinWarps + warp; row < rows; row += static_cast<int>(gridDim.y) * kRowJoinWarps) {
+        // the row's k-th partial result: CTA c - 1 opened the unit, the others went on with it
+        auto place = [&](int k) { return static_cast<long long>(2 * (c - 1 + k) + (k == 0 ? 1 : 0)) * a.rows_cap + row; };
+        auto part = [&](int k) { return reinterpret_cast<const Part*>(a.part_o + place(k) * D)[lane]; };
+        Part v[kFirst];                                       // under way while the factors are found
+#pragma unroll
+        for (int k = 0; k < kFirst; ++k)
+            if (k < count) v[k] = part(k);
+        float top = -INFINITY;
+        for (int k = lane; k < count; k += 32) top = fmaxf(top, reinterpret_cast<const float2*>(a.part_ml)[place(k)].x);
+        for (int d = 16; d > 0; d >>= 1) top = fmaxf(top, __shfl_xor_sync(0xFFFFFFFFu, top, d));
+        float o[kCols] = {}, sum = 0.0f;
+        auto add = [&](const Part& p, float f) {
+            const float* x = reinterpret_cast<const float*>(&p);
+#pragma unroll
+            for (int e = 0; e < kCols; ++e) o[e] = fmaf(f, x[e], o[e]);
+        };
+        for (int k0 = 0; k0 < count; k0 += 32) {
+            float2 ml = make_float2(-INFINITY, 0.0f);
+            if (k0 + lane < count) ml = reinterpret_cast<const float2*>(a.part_ml)[place(k0 + lane)];
+            const bool none = ml.x == -INFINITY;              // its sum is then 0, or NaN
+            const float f = none ? ml.y : exp2_approx(ml.x - top);
+            float part_sum = none ? ml.y : ml.y * f;
+            for (int d = 16; d > 0; d >>= 1) part_sum += __shfl_xor_sync(0xFFFFFFFFu, part_sum, d);
+            sum += part_sum;
+            if (k0 == 0) {
+#pragma unroll
+                for (int k = 0; k < kFirst; ++k) {
+                    const float fk = __shfl_sync(0xFFFFFFFFu, f, k);
+                    if (k < count) add(v[k], fk);
+                }
+            }
+#pragma unroll 4
+            for (int k = k0 == 0 ? kFirst : 0; k < min(32, count - k0); ++k) add(part(k0 + k), __shfl_sync(0xFFFFFFFFu, f, k));
+        }
+        const float inv = sum != 0.0f ? 1.0f / sum : 0.0f;
+        const int rt = row / a.group;
+        const long long to = (static_cast<long long>(at.b) * a.N + at.rt * a.unit_tokens + rt) * a.Hq + at.h * a.group + (row - rt * a.group);
+        uint32_t packed[kCols / 2];
+#pragma unroll
+        for (int e = 0; e < kCols / 2; ++e) packed[e] = pack2(o[2 * e] * inv, o[2 * e + 1] * inv, T{});
+        uint32_t* dst = reinterpret_cast<uint32_t*>(static_cast<T*>(a.out) + to * D) + lane * (kCols / 2);
+        if constexpr (kCols == 4) *reinterpret_cast<uint2*>(dst) = make_uint2(packed[0], packed[1]);
+        else *dst = packed[0];
+        if (lane == 0 && a.lse) a.lse[to] = lse_of(top, sum);
+    }
+
+    // rows without a request or window token, a warp each
+    const long long warps = static_cast<long long>(gridDim.x) * gridDim.y * kRowJoinWarps;
+    for (long long w = (static_cast<long long>(blockIdx.y) * gridDim.x + blockIdx.x) * kRowJoinWarps + warp;
+         w < static_cast<long long>(a.B) * a.N; w += warps) {
+        const int rb = static_cast<int>(quotient(w, a.N)), i = static_cast<int>(w - static_cast<long long>(rb) * a.N);
+        int kv, m;
+        request<true>(a, rb, kv, m);
         if (i < m) continue;
         uint4* dst = reinterpret_cast<uint4*>(static_cast<T*>(a.out) + w * a.Hq * D);
         for (int x = lane; x < a.Hq * (D / 8); x += 32) dst[x] = make_uint4(0u, 0u, 0u, 0u);
@@ -1159,10 +1240,12 @@ cudaError_t launch_parts(const CUtensorMap& q, const CUtensorMap& k, const CUten
     return launch_dependent(paged_attention_kernel<T, D, kParts, kMasked>, dim3(grid), dim3(PagedCfg<D, kParts>::kThreads), kSmem, stream, q, k, v, a);
 }
 
-template <typename T, int D, bool kMasked>
-dspark_status launch_typed(PagedArgs a, int grid, cudaStream_t stream) {
+// Tensor maps of the queries (a row tile of one key head's) and of the caches (a page, or 128 tokens of one).
+struct PagedMaps { CUtensorMap q, k, v; };
+
+template <typename T, int D>
+bool make_maps(const PagedArgs& a, PagedMaps& m) {
     const uint64_t e = sizeof(T);
-    CUtensorMap q, k, v;
     const uint64_t qd[3] = {static_cast<uint64_t>(D), static_cast<uint64_t>(a.Hq), static_cast<uint64_t>(a.B) * a.N};
     const uint64_t qs[2] = {D * e, static_cast<uint64_t>(a.Hq) * D * e};
     const uint32_t qb[3] = {64, static_cast<uint32_t>(a.group), static_cast<uint32_t>(a.tile_tokens)};
@@ -1170,28 +1253,51 @@ dspark_status launch_typed(PagedArgs a, int grid, cudaStream_t stream) {
                             static_cast<uint64_t>(a.num_pages) * a.Hkv};
     const uint64_t ks[2] = {D * e, static_cast<uint64_t>(a.page) * D * e};
     const uint32_t kb[3] = {64, static_cast<uint32_t>(a.box_rows), 1};
-    if (!make_tensor_map(&q, HalfType<T>::kMapType, 3, a.q, qd, qs, qb, CU_TENSOR_MAP_SWIZZLE_128B) ||
-        !make_tensor_map(&k, HalfType<T>::kMapType, 3, a.k_cache, kd, ks, kb, CU_TENSOR_MAP_SWIZZLE_128B) ||
-        !make_tensor_map(&v, HalfType<T>::kMapType, 3, a.v_cache, kd, ks, kb, CU_TENSOR_MAP_SWIZZLE_128B))
-        return DSPARK_ERR_CUDA;
+    return make_tensor_map(&m.q, HalfType<T>::kMapType, 3, a.q, qd, qs, qb, CU_TENSOR_MAP_SWIZZLE_128B) &&
+           make_tensor_map(&m.k, HalfType<T>::kMapType, 3, a.k_cache, kd, ks, kb, CU_TENSOR_MAP_SWIZZLE_128B) &&
+           make_tensor_map(&m.v, HalfType<T>::kMapType, 3, a.v_cache, kd, ks, kb, CU_TENSOR_MAP_SWIZZLE_128B);
+}
+
+template <bool kMasked>
+dspark_status launch_plan(const PagedArgs& a, int grid, cudaStream_t stream) {
     const int trees = kMasked && a.parents ? a.B : 0;
     paged_plan_kernel<kMasked><<<1 + trees, kPlanThreads, 0, stream>>>(a, grid);
-    cudaError_t err = cudaGetLastError();
-    if (err != cudaSuccess) return cuda_error(err, "launch(paged_attention plan)");
+    const cudaError_t err = cudaGetLastError();
+    return err == cudaSuccess ? DSPARK_OK : cuda_error(err, "launch(paged_attention plan)");
+}
+
+template <typename T, int D, bool kMasked>
+dspark_status launch_join(const PagedArgs& a, int grid, cudaStream_t stream) {
+    const int rows = a.unit_tokens * a.group;
+    cudaError_t err;
+    if constexpr (kMasked)
+        err = launch_dependent(row_join_kernel<T, D>, dim3(grid, std::min(kRowJoinHigh, (rows + kRowJoinWarps - 1) / kRowJoinWarps)),
+                               dim3(32 * kRowJoinWarps), 0, stream, a);
+    else
+        err = launch_dependent(paged_join_kernel<T, D>, dim3(grid, (rows + kJoinRows - 1) / kJoinRows), dim3(kJoinRows * D), 0, stream, a);
+    return err == cudaSuccess ? DSPARK_OK : cuda_error(err, "launch(paged_attention join)");
+}
+
+template <typename T, int D, bool kMasked>
+dspark_status launch_typed(const PagedArgs& a, int grid, cudaStream_t stream) {
+    PagedMaps m;
+    if (!make_maps<T, D>(a, m)) return DSPARK_ERR_CUDA;
+    const dspark_status st = launch_plan<kMasked>(a, grid, stream);
+    if (st != DSPARK_OK) return st;
     const int rows = a.tile_tokens * a.group;
-    err = rows <= 32   ? launch_parts<T, D, 4, kMasked>(q, k, v, a, grid, stream)
-          : rows <= 64 ? launch_parts<T, D, 2, kMasked>(q, k, v, a, grid, stream)
-                       : launch_parts<T, D, 1, kMasked>(q, k, v, a, grid, stream);
+    const cudaError_t err = rows <= 32   ? launch_parts<T, D, 4, kMasked>(m.q, m.k, m.v, a, grid, stream)
+                            : rows <= 64 ? launch_parts<T, D, 2, kMasked>(m.q, m.k, m.v, a, grid, stream)
+                                         : launch_parts<T, D, 1, kMasked>(m.q, m.k, m.v, a, grid, stream);
     if (err != cudaSuccess) return cuda_error(err, "launch(paged_attention)");
-    err = launch_dependent(paged_join_kernel<T, D, kMasked>, dim3(grid, (rows + kJoinRows - 1) / kJoinRows), dim3(kJoinRows * D),
-                           0, stream, a);
-    if (err != cudaSuccess) return cuda_error(err, "launch(paged_attention join)");
-    return DSPARK_OK;
+    return launch_join<T, D, kMasked>(a, grid, stream);
 }
 
 // Bytes of the plan and the partial results behind it.
-size_t partials_end(int N, int Hq, int D) {
-    return sizeof(Plan) + 2ull * kMaxCtas * rows_cap_of(N, Hq) * (2ull + D) * sizeof(float);
+size_t partials_end(int rows_cap, int D) { return sizeof(Plan) + 2ull * kMaxCtas * rows_cap * (2ull + D) * sizeof(float); }
+
+void set_partials(PagedArgs& a) {
+    a.part_ml = reinterpret_cast<float*>(reinterpret_cast<uint8_t*>(a.plan) + sizeof(Plan));
+    a.part_o = a.part_ml + 2ull * kMaxCtas * a.rows_cap * 2;
 }
 
 PagedArgs paged_args(const void* q, const void* k_cache, const void* v_cache, const int32_t* block_table, int max_pages,
@@ -1214,14 +1320,13 @@ PagedArgs paged_args(const void* q, const void* k_cache, const void* v_cache, co
     a.num_pages = num_pages;
     a.page = page;
     a.box_rows = std::min(page, kTile);
-    a.tile_tokens = std::min(N, kTile / a.group);
+    a.tile_tokens = a.unit_tokens = std::min(N, kTile / a.group);
     a.rows_cap = rows_cap_of(N, Hq);
     a.scale = scale;
     a.out = out;
     a.lse = lse;
     a.plan = static_cast<Plan*>(ws);
-    a.part_ml = reinterpret_cast<float*>(static_cast<uint8_t*>(ws) + sizeof(Plan));
-    a.part_o = a.part_ml + 2ull * kMaxCtas * a.rows_cap * 2;
+    set_partials(a);
     a.timeout_ns = kDefaultTimeoutNs;
     return a;
 }

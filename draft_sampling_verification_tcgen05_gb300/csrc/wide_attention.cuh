@@ -1,0 +1,590 @@
+// Masked attention over a paged cache where the rows of a key head fill more than one tile (a tree of 64 nodes with four
+// query heads to a key head, a chunk of a prompt): a unit is two row tiles of 128 rows, so keys and values are loaded
+// once for 256 rows, and while one tile's scores go through the softmax, the tensor cores work for the other.  Units,
+// runs, partial results, plan and join are those of paged_attention.cuh.
+//
+//   warps 0-7, 8-15  softmax and results of one row tile each: two threads per row, 64 of a key tile's tokens each
+//   warp 16          walks the run's segments and loads (TMA) queries, and page by page keys and values
+//   warps 17, 18     issue S = Q K^T and O += P V of one row tile each on tcgen05 (M = 128, fp32 in tensor memory; P
+//                    replaces half of S)
+//
+// Maxima, rounding and infinities are handled as in paged_attention.cuh; where a result is not finite, the CTA goes
+// through its run again, once for each row tile, as the values' infinities are taken out for its rows.
+#pragma once
+
+#include "paged_attention.cuh"
+
+namespace dspark {
+namespace {
+
+namespace wide {
+
+constexpr int kThreads = 608;
+constexpr int kRowThreads = 256;           // softmax threads of a row tile: two to a row, 64 of a key tile's tokens each
+constexpr int kAhead = 4;                  // segments between the loads and the results
+constexpr int kSlots = 2;                  // key tiles, and value tiles, in flight
+constexpr uint32_t kColS = 0, kColP = 64, kColO = 256, kTmemCols = 512;    // S and O of tile 1: + 128
+constexpr uint32_t kWarpLoad = 16, kWarpMma = 17;
+// named barriers: + row tile; + 4 * row tile + quadrant, the two warps of the same rows; + row tile
+constexpr uint32_t kBarTile = 1, kBarRows = 3, kBarFirst = 11;
+constexpr uint32_t kWaitLoad = 0x811, kWaitMma = 0x812, kWaitSoftmax = 0x813;
+
+// A segment as the roles see it: n key tiles for each row tile that takes part (t0 = t1: the end of a pass).
+struct Item {
+    Segment<true> g;
+    int n[2];
+};
+
+template <int D>
+struct Smem {
+    static constexpr int kHalves = D / 64;                        // 128-byte column blocks
+    static constexpr uint32_t kBlockBytes = kTile * 128;
+    static constexpr uint32_t kTileBytes = kHalves * kBlockBytes;
+    alignas(1024) uint8_t q[2][kTileBytes];
+    alignas(1024) uint8_t k[kSlots][kTileBytes];
+    alignas(1024) uint8_t v[kSlots][kTileBytes];
+    alignas(1024) uint4 stage[16][128];                           // 32 columns of a warp's rows; a row of values in a later pass
+    Item item[kAhead];
+    float half[2][2][kTile];                                      // by row tile and half of the key tiles: a row's largest score, or sum
+    uint32_t masks[2][4];
+    uint32_t again, failed;                                       // further passes are needed / a wait gave up
+    uint64_t item_full[kAhead], item_empty[kAhead];
+    uint64_t q_full[2], q_empty[2];
+    uint64_t k_full[kSlots], k_empty[kSlots], v_full[kSlots], v_empty[kSlots];
+    uint64_t s_full[2], p_first[2], p_last[2], pv_done[2], o_empty[2], turn[2], drain;
+    uint32_t tmem_base;
+};
+
+}  // namespace wide
+
+template <typename T, int D>
+__global__ void __launch_bounds__(wide::kThreads, 1)
+wide_attention_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmK,
+                      const __grid_constant__ CUtensorMap tmV, const __grid_constant__ PagedArgs a) {
+    using namespace wide;
+    using Smem = wide::Smem<D>;
+    constexpr int kHalves = Smem::kHalves;
+    constexpr uint32_t kBlockBytes = Smem::kBlockBytes, kTileBytes = Smem::kTileBytes;
+    extern __shared__ __align__(1024) uint8_t smem_raw[];
+    Smem& s = *reinterpret_cast<Smem*>(smem_raw);
+    const uint32_t warp = warp_id(), lane = lane_id();
+    WsHeader* ws = &a.plan->header;
+
+    if (threadIdx.x == 0) {
+        for (int i = 0; i < wide::kAhead; ++i) {
+            mbar_init(&s.item_full[i], 1);
+            mbar_init(&s.item_empty[i], 2 * wide::kRowThreads + 2);
+        }
+        for (int i = 0; i < 2; ++i) {
+            mbar_init(&s.q_full[i], 1);
+            mbar_init(&s.q_empty[i], 1);
+            mbar_init(&s.s_full[i], 1);
+            mbar_init(&s.turn[i], 1);
+            mbar_init(&s.p_first[i], wide::kRowThreads);
+            mbar_init(&s.p_last[i], wide::kRowThreads);
+            mbar_init(&s.pv_done[i], 1);
+            mbar_init(&s.o_empty[i], wide::kRowThreads);
+        }
+        for (int i = 0; i < kSlots; ++i) {
+            mbar_init(&s.k_full[i], 1);
+            mbar_init(&s.k_empty[i], 2);
+            mbar_init(&s.v_full[i], 1);
+            mbar_init(&s.v_empty[i], 2);
+        }
+        mbar_init(&s.drain, 2);
+        s.again = s.failed = 0u;
+        fence_mbarrier_init();
+        prefetch_tensormap(&tmQ);
+        prefetch_tensormap(&tmK);
+        prefetch_tensormap(&tmV);
+    }
+    if (warp == kWarpMma) {
+        tmem_alloc(&s.tmem_base, wide::kTmemCols);
+        tmem_relinquish();
+    }
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tmem = s.tmem_base;
+    grid_dependency_wait();
+
+    bool ok = true;
+    auto all = [&](bool x) { return __all_sync(0xFFFFFFFFu, x); };
+    auto wait = [&](uint64_t& bar, int use, uint32_t where) {            // use: how often it completed before
+        return mbar_wait_short(&bar, static_cast<uint32_t>(use) & 1u, ws, a.timeout_ns, where);
+    };
+    // Carried from pass to pass, each role for itself: items, key tiles, own key tiles, own row tiles, turns.
+    int count = 0, kt = 0, i = 0, used = 0, turn = 0, qt[2] = {0, 0};
+    // Pass 0 is all there is, as a rule; passes 1 and 2 take one row tile each.
+    for (int pass = 0;; ++pass) {
+        if (warp == kWarpLoad) {
+            // ---------------- segments and loads ----------------
+            const uint64_t keep = l2_policy_evict_last();
+            const int page_bits = __ffs(a.page) - 1;
+            const int boxes = kTile / a.box_rows * kHalves;
+            const int box = static_cast<int>(lane) / kHalves, half = static_cast<int>(lane) % kHalves;
+            const uint32_t box_bytes = static_cast<uint32_t>(a.box_rows) * 128u;
+            const uint32_t box_at = static_cast<uint32_t>(half) * kBlockBytes + static_cast<uint32_t>(box) * box_bytes;
+            // this lane's box of tile t: its page (looked at only when it is used), -2: none, or -3: seen by no row
+            auto lookup = [&](const Segment<true>& g, int t) {
+                const int j = g.place(t) * kTile + box * a.box_rows;
+                if (static_cast<int>(lane) >= boxes || j >= g.kv) return -2;
+                if (g.skipped(a, j, j + a.box_rows)) return -3;
+                return max(-1, a.block_table[static_cast<long long>(g.b) * a.max_pages + (j >> page_bits)]);
+            };
+            Walker<true> walk(a);
+            Segment<true> g{};
+            while (ok) {
+                const bool more = walk.next(g);
+                int n[2];
+                for (int x = 0; x < 2; ++x)
+                    n[x] = more && g.rt * a.unit_tokens + x * a.tile_tokens < g.n && (pass == 0 || pass == x + 1) ? g.t1 - g.t0 : 0;
+                if (more && n[0] + n[1] == 0) continue;
+                ok = all(wait(s.item_empty[count % wide::kAhead], count / wide::kAhead + 1, wide::kWaitLoad));
+                if (!ok) break;
+                if (lane == 0) {
+                    Item& it = s.item[count % wide::kAhead];
+                    it.g = g;
+                    if (!more) it.g.t0 = it.g.t1 = 0;
+                    it.n[0] = n[0];
+                    it.n[1] = n[1];
+                    mbar_arrive(&s.item_full[count % wide::kAhead]);
+                }
+                __syncwarp();
+                ++count;
+                if (!more) break;
+                for (int x = 0; ok && x < 2; ++x) {
+                    if (n[x] == 0) continue;
+                    ok = all(wait(s.q_empty[x], qt[x] + 1, wide::kWaitLoad));
+                    if (!ok) break;
+                    if (lane == 0) {
+                        mbar_arrive_expect_tx(&s.q_full[x], static_cast<uint32_t>(a.tile_tokens * a.group) * 128u * kHalves);
+                        for (int y = 0; y < kHalves; ++y)
+                            tma_load_3d(s.q[x] + y * kBlockBytes, &tmQ, y * 64, g.h * a.group,
+                                        g.b * a.N + g.rt * a.unit_tokens + x * a.tile_tokens, &s.q_full[x], keep);
+                    }
+                    __syncwarp();
+                    ++qt[x];
+                }
+                int page = lookup(g, g.t0);
+                for (int t = g.t0; ok && t < g.t1; ++t, ++kt) {
+                    const int next = t + 1 < g.t1 ? lookup(g, t + 1) : -2;
+                    const int slot = kt % kSlots;
+                    const uint32_t bytes = __popc(__ballot_sync(0xFFFFFFFFu, page != -2)) * box_bytes;
+                    const int y = (g.place(t) * kTile + box * a.box_rows) & (a.page - 1);
+                    int z = page * a.Hkv + g.h;
+                    if (page == -3) {
+                        z = a.num_pages * a.Hkv;              // outside the map: reads zeros
+                    } else if (page != -2 && (page < 0 || page >= a.num_pages)) {
+                        flag_input_index(ws);
+                        z = g.h;
+                    }
+                    for (int x = 0; x < 2; ++x) {             // keys, values
+                        uint64_t* full = x == 0 ? s.k_full : s.v_full;
+                        ok = all(wait(x == 0 ? s.k_empty[slot] : s.v_empty[slot], kt / kSlots + 1, wide::kWaitLoad));
+                        if (!ok) break;
+                        if (lane == 0) mbar_arrive_expect_tx(&full[slot], bytes);
+                        __syncwarp();
+                        if (page != -2)
+                            tma_load_3d((x == 0 ? s.k[slot] : s.v[slot]) + box_at, x == 0 ? &tmK : &tmV, half * 64, y, z, &full[slot], keep);
+                    }
+                    page = next;
+                }
+            }
+            grid_dependency_launch();
+            if (!ok) {
+                // give copies in flight time to land before the block exits
+                const long long t0 = global_ns();
+                while (global_ns() - t0 < a.timeout_ns) {
+                }
+            }
+        } else if (warp >= kWarpMma) {
+            // ---------------- products of row tile w: the whole warp waits, one lane issues ----------------
+            // The tensor cores run one tile's products in the order of issue, so S may be written as soon as the
+            // product that read P (in S) has been issued.  The tiles take turns with the end of a product and the
+            // next scores: then one tile's products run while the other is in its softmax.  The waits of a turn are
+            // done before it, since one takes about as long as the tensor cores' queue lasts.
+            const int w = static_cast<int>(warp - kWarpMma);
+            constexpr uint32_t kIdescS = attn_idesc<T, false>(kTile, kTile);
+            constexpr uint32_t kIdescO = attn_idesc<T, true>(kTile, D);
+            constexpr uint32_t kStep = kTileBytes >> 4;           // a tile, in descriptor units
+            const uint64_t q_desc = sw128_kmajor_desc(smem_u32(s.q[w]));
+            const uint64_t k_desc = sw128_kmajor_desc(smem_u32(s.k[0]));
+            const uint64_t v_desc = sw128_token_rows_desc(smem_u32(s.v[0]), kBlockBytes);
+            const uint32_t tS = tmem + wide::kColS + w * 128u, tP = tmem + wide::kColP + w * 128u, tO = tmem + wide::kColO + w * 128u;
+            auto take_turn = [&] {
+                const bool mine = w == 0 ? turn == 0 || wait(s.turn[0], turn - 1, wide::kWaitMma) : wait(s.turn[1], turn, wide::kWaitMma);
+                ++turn;
+                return all(mine);
+            };
+            while (ok) {
+                ok = all(wait(s.item_full[count % wide::kAhead], count / wide::kAhead, wide::kWaitMma));
+                if (!ok) break;
+                const Item& it = s.item[count % wide::kAhead];
+                const int n = __shfl_sync(0xFFFFFFFFu, it.n[w], 0), other = __shfl_sync(0xFFFFFFFFu, it.n[1 - w], 0);
+                // tokens that the request holds from the segment's last tile on
+                const int held = __shfl_sync(0xFFFFFFFFu, it.g.kv - it.g.place(it.g.t1 - 1) * kTile, 0);
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&s.item_empty[count % wide::kAhead]);
+                ++count;
+                const int most = max(n, other);
+                if (most == 0) break;
+                // turn t: the end of the product of key tile t - 1 and the scores of key tile t
+                for (int t = 0; t <= most; ++t) {
+                    const uint64_t v = v_desc + static_cast<uint32_t>((kt + t - 1) % kSlots) * kStep;
+                    const uint64_t k = k_desc + static_cast<uint32_t>((kt + t) % kSlots) * kStep;
+                    // what is usually there comes first, the weights last
+                    if (t < most) ok = all(wait(s.k_full[(kt + t) % kSlots], (kt + t) / kSlots, wide::kWaitMma));
+                    if (ok && t == 0 && n > 0) ok = all(wait(s.q_full[w], used, wide::kWaitMma));
+                    if (!ok) break;
+                    if (t > 0) {
+                        const int slot = (kt + t - 1) % kSlots;
+                        ok = all(wait(s.v_full[slot], (kt + t - 1) / kSlots, wide::kWaitMma));
+                        if (!ok) break;
+                        if (t <= n) {
+                            if (t == most && held < kTile) {      // behind the request's end nothing may count
+                                const int pieces = (kTile - held) * 8;    // of 16 bytes, per block
+                                for (int y = 0; y < kHalves; ++y)
+                                    for (int x = static_cast<int>(lane); x < pieces; x += 32)
+                                        *reinterpret_cast<uint4*>(s.v[slot] + y * kBlockBytes + held * 128 + x * 16) =
+                                            make_uint4(0u, 0u, 0u, 0u);
+                                fence_proxy_async_smem();
+                                __syncwarp();
+                            }
+                            ok = all(wait(s.p_first[w], i, wide::kWaitMma) && (t > 1 || used == 0 || wait(s.o_empty[w], used - 1, wide::kWaitMma)));
+                            if (!ok) break;
+                            tc_fence_after();
+                            const uint32_t onto = t == 1 && pass == 0 ? 0u : 1u;   // later, O starts from what is there
+                            // 16 tokens a product; of each half of the tile, the first 32 tokens' weights are ready first
+                            if (elect_one()) {
+#pragma unroll
+                                for (int z = 0; z < 4; ++z) {
+                                    const int y = z + (z & 2);
+                                    mma_issue_ta(tO, tP + y * 8, v + y * 128, kIdescO, z == 0 ? onto : 1u);
+                                }
+                            }
+                            __syncwarp();
+                        }
+                    }
+                    ok = take_turn();
+                    if (ok && t > 0 && t <= n) ok = all(wait(s.p_last[w], i++, wide::kWaitMma));
+                    if (!ok) break;
+                    tc_fence_after();
+                    if (elect_one()) {
+                        if (t > 0 && t <= n) {
+#pragma unroll
+                            for (int z = 0; z < 4; ++z) {
+                                const int y = 2 + z + (z & 2);
+                                mma_issue_ta(tO, tP + y * 8, v + y * 128, kIdescO, 1u);
+                            }
+                            mma_commit(&s.pv_done[w]);
+                        }
+                        if (t < n) {
+#pragma unroll
+                            for (int d = 0; d < D / 16; ++d) {
+                                const uint64_t off = (static_cast<uint32_t>(d / 4) * kBlockBytes + (d % 4) * 32) >> 4;
+                                mma_issue<false>(tS, q_desc + off, k + off, kIdescS, d != 0 ? 1u : 0u);
+                            }
+                            mma_commit(&s.s_full[w]);
+                        }
+                        mbar_arrive(&s.turn[1 - w]);
+                        if (t + 1 == n) mma_commit(&s.q_empty[w]);
+                        if (t > 0) mma_commit(&s.v_empty[(kt + t - 1) % kSlots]);
+                        if (t < most) mma_commit(&s.k_empty[(kt + t) % kSlots]);
+                    }
+                    __syncwarp();
+                }
+                if (!ok) break;
+                kt += most;
+                used += n > 0 ? 1 : 0;
+            }
+            if (elect_one()) mma_commit(&s.drain);
+            __syncwarp();
+            const long long t0 = global_ns();
+            while (!mbar_try_wait(&s.drain, pass & 1) && global_ns() - t0 < a.timeout_ns) {
+            }
+            __syncwarp();
+        } else {
+            // ---------------- softmax and results of row tile w ----------------
+            const int w = static_cast<int>(warp >> 3);
+            const int part = static_cast<int>(warp >> 2) & 1;  // 64 of the key tile's tokens, half of the output's columns
+            const uint32_t quad = warp & 3u;
+            const uint32_t bar_tile = kBarTile + static_cast<uint32_t>(w), bar_rows = kBarRows + 4u * static_cast<uint32_t>(w) + quad;
+            const uint32_t lanes = (quad * 32u) << 16;
+            const uint32_t tS = tmem + lanes + wide::kColS + w * 128u + part * 64u, tP = tmem + lanes + wide::kColP + w * 128u + part * 32u;
+            const uint32_t tO = tmem + lanes + wide::kColO + w * 128u + part * (D / 2u);
+            const int row = static_cast<int>(quad * 32u + lane);
+            const int row_tok = row / a.group;
+            const bool row_used = row < a.tile_tokens * a.group;
+            const float sl2 = a.scale * kLog2e;
+            const bool falling = sl2 < 0.0f;                          // the largest score is the smallest product
+            const float none = falling ? INFINITY : -INFINITY;
+            // A masked score is infinite and gets no weight by that, for which the slope must not be 0: the smallest step above
+            // it (no product of finite values then reaches 2^-20) stands for a scale of 0.
+            const float steep = sl2 == 0.0f ? 0x1p-149f : sl2;
+            const bool redo = pass != 0;
+            while (true) {
+                ok = named_bar_and(bar_tile, wide::kRowThreads, wait(s.item_full[count % wide::kAhead], count / wide::kAhead, wide::kWaitSoftmax));
+                if (!ok) break;
+                const Item& it = s.item[count % wide::kAhead];
+                const int n = it.n[w];
+                if (n == 0) {
+                    const int other = it.n[1 - w];
+                    kt += other;
+                    mbar_arrive(&s.item_empty[count++ % wide::kAhead]);
+                    if (other == 0) break;
+                    continue;
+                }
+                const Segment<true>& g = it.g;
+                const int first = g.rt * a.unit_tokens + w * a.tile_tokens;   // the tile's first window token
+                const int tok = first + row_tok;
+                const bool valid = row_used && tok < g.n;
+                // tokens that every row of the tile sees: [from, to), and those below `sinks` as far as `to`
+                const int base = g.kv - g.n, last = min(g.n, first + a.tile_tokens) - 1;
+                const int to = a.parents ? base : a.causal ? base + first + 1 : g.kv;
+                const int from = a.window > 0 ? base + (a.parents ? g.n - 1 : last) - a.window + 1 : 0;
+                const int sinks = a.window > 0 ? a.sinks : 0;
+                float m2 = -INFINITY, l = 0.0f;
+                for (int t = 0; t < n; ++t, ++i) {
+                    bool go = wait(s.s_full[w], i, wide::kWaitSoftmax);
+                    if (redo) go = named_bar_and(bar_tile, wide::kRowThreads, go);  // these meet in barriers below
+                    go = all(go);
+                    // 64 scores in registers
+                    uint32_t r[2][32];
+                    const int j = g.place(g.t0 + t) * kTile;
+                    const bool masked = j + kTile > to || (j < from && j + kTile > sinks);
+                    tc_fence_after();
+                    tmem_ld32(tS, r[0]);
+                    tmem_ld32(tS + 32, r[1]);
+                    tmem_wait_ld32(r[0]);
+                    tmem_wait_ld32(r[1]);
+                    if (masked) {                             // an infinite score has no weight
+                        SeenBits<64> sees;
+                        RowMask<true>(a, g, tok, valid).get(a, j + part * 64, sees);
+#pragma unroll
+                        for (int c = 0; c < 64; ++c)
+                            if (!sees.has(c)) r[c >> 5][c & 31] = __float_as_uint(none);
+                    }
+                    float best[4] = {none, none, none, none};
+                    if (!falling) {
+#pragma unroll
+                        for (int c = 0; c < 64; c += 8)
+#pragma unroll
+                            for (int e = 0; e < 4; ++e)
+                                best[e] = max3(best[e], __uint_as_float(r[c >> 5][(c & 31) + e]),
+                                               __uint_as_float(r[c >> 5][(c & 31) + 4 + e]));
+                    } else {
+#pragma unroll
+                        for (int c = 0; c < 64; ++c) best[c & 3] = fminf(best[c & 3], __uint_as_float(r[c >> 5][c & 31]));
+                    }
+                    const float top = falling ? fminf(fminf(best[0], best[1]), fminf(best[2], best[3]))
+                                              : fmaxf(fmaxf(best[0], best[1]), fmaxf(best[2], best[3]));
+                    float mt = top == none ? -INFINITY : top * sl2 - HalfType<T>::kHeadroom;
+                    // The two threads of a row meet: P may then replace the scores, and if either finds the maximum
+                    // too low (or has given up) they exchange theirs.
+                    bool raise = t == 0 || !go || (valid && mt > m2 + kRaise);
+                    if (t > 0) raise = !named_bar_and(bar_rows, 64, !raise);
+                    ok = go;
+                    if (raise) {
+                        s.half[w][part][row] = mt;
+                        if (t > 0) go = go && all(wait(s.pv_done[w], i - 1, wide::kWaitSoftmax));
+                        ok = named_bar_and(bar_rows, 64, go);
+                        if (!ok && !redo) break;                          // else at the vote below
+                        mt = fmaxf(mt, s.half[w][1 - part][row]);
+                        if (t == 0) {
+                            m2 = mt;
+                        } else if (ok) {
+                            tc_fence_after();
+                            const bool up = valid && mt > m2 + kRaise;
+                            const float f = up ? exp2_approx(m2 - mt) : 1.0f;
+                            if (up) {
+                                l *= f;
+                                m2 = mt;
+                            }
+#pragma unroll 1
+                            for (uint32_t c = 0; c < D / 2; c += 16) {
+                                uint32_t o[16];
+                                tmem_ld16(tO + c, o);
+                                tmem_wait_ld();
+#pragma unroll
+                                for (int x = 0; x < 16; ++x) o[x] = __float_as_uint(__uint_as_float(o[x]) * f);
+                                tmem_st16(tO + c, o);
+                            }
+                            tmem_wait_st();
+                        }
+                    }
+                    const float ref = m2 == -INFINITY ? 0.0f : m2;
+                    float2 sum[2] = {};
+                    const float2 slope = make_float2(steep, steep), shift = make_float2(-ref, -ref);
+                    // 32 weights, to P: one straight piece of code, for which the compiler finds an order that keeps the
+                    // exponential's unit (4 cycles a warp) at work.
+                    auto weigh = [&](int x) {
+                        uint32_t p[16];
+#pragma unroll
+                        for (int c = 0; c < 32; c += 2) {
+                            const float2 y = __ffma2_rn(make_float2(__uint_as_float(r[x][c]), __uint_as_float(r[x][c + 1])), slope, shift);
+                            const float2 e = make_float2(exp2_approx(y.x), exp2_approx(y.y));
+                            sum[(c >> 1) & 1] = __fadd2_rn(sum[(c >> 1) & 1], e);
+                            p[c >> 1] = pack2(e.x, e.y, T{});
+                        }
+                        tmem_st16(tP + x * 16, p);
+                        tmem_wait_st();
+                    };
+                    weigh(0);
+                    if (!redo) {
+                        tc_fence_before();
+                        mbar_arrive(&s.p_first[w]);
+                    }
+                    weigh(1);
+                    l += (sum[0].x + sum[0].y) + (sum[1].x + sum[1].y);
+                    if (redo) {
+                        const int slot = (kt + t) % kSlots;
+                        bool there = ok && wait(s.v_full[slot], (kt + t) / kSlots, wide::kWaitSoftmax);
+                        // O is about to be changed here: the products before must be complete
+                        if (there && t > 0) there = wait(s.pv_done[w], i - 1, wide::kWaitSoftmax);
+                        there = all(there);
+                        if (there && t == 0) {
+                            uint32_t zero[16];
+#pragma unroll
+                            for (int c = 0; c < 16; ++c) zero[c] = 0u;
+                            for (uint32_t c = 0; c < D / 2; c += 16) tmem_st16(tO + c, zero);
+                            tmem_wait_st();
+                        }
+                        tc_fence_before();
+                        ok = named_bar_and(bar_tile, wide::kRowThreads, there);     // P and O of both halves are in place
+                        if (!ok) break;
+                        tc_fence_after();
+                        if (part == 0) {
+                            // the row's mask over the whole tile: this thread has its first half
+                            SeenBits<128> whole;
+                            whole.all();
+                            if (masked) {
+                                const RowMask<true> mask(a, g, tok, valid);
+                                mask.get(a, j, whole);
+                            }
+                            move_infinities<T>(s.v[slot], kBlockBytes, kHalves, row, g.kv - j, [=](int x) { return whole.at(x); }, tP, tO,
+                                               reinterpret_cast<float*>(s.stage[8 * w]), s.masks[w], kBarFirst + static_cast<uint32_t>(w));
+                            fence_proxy_async_smem();
+                        }
+                        tc_fence_before();
+                        mbar_arrive(&s.p_first[w]);
+                    }
+                    tc_fence_before();
+                    mbar_arrive(&s.p_last[w]);
+                }
+                kt += max(n, it.n[1 - w]);
+
+                // ---------------- the tile's rows ----------------
+                if (ok) ok = all(wait(s.pv_done[w], i - 1, wide::kWaitSoftmax));
+                s.half[w][part][row] = l;
+                ok = named_bar_and(bar_tile, wide::kRowThreads, ok);      // the warps meet again: give up together
+                if (!ok) break;
+                tc_fence_after();
+                l = s.half[w][0][row] + s.half[w][1][row];
+                const bool whole = g.t0 == 0 && g.t1 == g.tiles;
+                const float f = whole ? (l != 0.0f ? 1.0f / l : 0.0f) : 1.0f;
+                float check[4] = {l * 0.0f, 0.0f, 0.0f, 0.0f};            // 0, or NaN
+                uint4* stage = s.stage[warp];
+                const int rows = min(a.tile_tokens, g.n - first) * a.group;
+                const long long row0 = (static_cast<long long>(g.b) * a.N + first) * a.Hq + g.h * a.group;
+                const long long part_base = static_cast<long long>(2 * blockIdx.x + (g.t0 == 0 ? 1 : 0)) * a.rows_cap + w * a.tile_tokens * a.group;
+                // through shared memory, so that four lanes write a row's piece together: 32 columns of the output, or 16
+                // of a partial result, at a time
+                const int piece = static_cast<int>(lane) & 3;
+                long long to_row[4];                                      // this lane's four rows (-1: none)
+#pragma unroll
+                for (int y = 0; y < 4; ++y) {
+                    const int rr = static_cast<int>(quad) * 32 + y * 8 + (static_cast<int>(lane) >> 2);
+                    const int rt = rr / a.group;
+                    to_row[y] = rr >= rows ? -1 : whole ? row0 + static_cast<long long>(rt) * a.Hq + (rr - rt * a.group) : part_base + rr;
+                }
+#pragma unroll 1
+                for (int c = 0; c < D / 2; c += 32) {
+                    float o[32];
+                    tmem_ld32(tO + c, reinterpret_cast<uint32_t*>(o));
+                    tmem_wait_ld32(reinterpret_cast<uint32_t*>(o));
+                    if (c + 32 == D / 2) {
+                        tc_fence_before();
+                        mbar_arrive(&s.o_empty[w]);
+                    }
+#pragma unroll
+                    for (int x = 0; x < 32; ++x) {
+                        check[x & 3] = fmaf(o[x], 0.0f, check[x & 3]);
+                        o[x] *= f;
+                    }
+                    const int col = part * (D / 2) + c;
+                    if (whole) {
+                        __syncwarp();                                     // the columns before have been read
+#pragma unroll
+                        for (int x = 0; x < 4; ++x) stage[lane * 4 + (x ^ ((lane >> 1) & 3))] = pack8(o + 8 * x, T{});
+                        __syncwarp();
+#pragma unroll
+                        for (int y = 0; y < 4; ++y) {
+                            const int at = y * 8 + (static_cast<int>(lane) >> 2);
+                            if (to_row[y] >= 0)
+                                *reinterpret_cast<uint4*>(static_cast<T*>(a.out) + to_row[y] * D + col + piece * 8) =
+                                    stage[at * 4 + (piece ^ ((at >> 1) & 3))];
+                        }
+                    } else {
+#pragma unroll
+                        for (int z = 0; z < 2; ++z) {
+                            __syncwarp();
+#pragma unroll
+                            for (int x = 0; x < 4; ++x)
+                                stage[lane * 4 + (x ^ ((lane >> 1) & 3))] =
+                                    make_uint4(__float_as_uint(o[16 * z + 4 * x]), __float_as_uint(o[16 * z + 4 * x + 1]),
+                                               __float_as_uint(o[16 * z + 4 * x + 2]), __float_as_uint(o[16 * z + 4 * x + 3]));
+                            __syncwarp();
+#pragma unroll
+                            for (int y = 0; y < 4; ++y) {
+                                const int at = y * 8 + (static_cast<int>(lane) >> 2);
+                                if (to_row[y] >= 0)
+                                    *reinterpret_cast<uint4*>(a.part_o + to_row[y] * D + col + 16 * z + piece * 4) =
+                                        stage[at * 4 + (piece ^ ((at >> 1) & 3))];
+                            }
+                        }
+                    }
+                }
+                if (valid && part == 0) {
+                    if (!whole) reinterpret_cast<float2*>(a.part_ml)[part_base + row] = make_float2(m2, l);
+                    else if (a.lse) a.lse[(static_cast<long long>(g.b) * a.N + tok) * a.Hq + g.h * a.group + (row - row_tok * a.group)] = lse_of(m2, l);
+                }
+                if (pass == 0 && valid && check[0] + check[1] + check[2] + check[3] != 0.0f) s.again = 1u;
+                __syncwarp();
+                mbar_arrive(&s.item_empty[count++ % wide::kAhead]);
+            }
+        }
+        if (!ok) s.failed = 1u;
+        __syncthreads();
+        const bool stop = pass == 2 || s.again == 0u || s.failed != 0u;
+        __syncthreads();                       // everyone has read them before the next pass may write them
+        if (stop) break;
+    }
+
+    tc_fence_before();
+    __syncthreads();
+    if (warp == kWarpMma) {
+        __syncwarp();
+        tc_fence_after();
+        tmem_dealloc(tmem, wide::kTmemCols);
+    }
+}
+
+template <typename T, int D>
+dspark_status launch_wide(PagedArgs& a, int grid, cudaStream_t stream) {
+    constexpr size_t kSmem = sizeof(wide::Smem<D>);
+    static_assert(kSmem <= 227 * 1024, "shared memory of one SM");
+    a.unit_tokens = std::min(a.N, 2 * a.tile_tokens);
+    PagedMaps m;
+    if (!make_maps<T, D>(a, m)) return DSPARK_ERR_CUDA;
+    const dspark_status st = launch_plan<true>(a, grid, stream);
+    if (st != DSPARK_OK) return st;
+    cudaError_t err = cudaFuncSetAttribute(wide_attention_kernel<T, D>, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(kSmem));
+    if (err == cudaSuccess)
+        err = launch_dependent(wide_attention_kernel<T, D>, dim3(grid), dim3(wide::kThreads), kSmem, stream, m.q, m.k, m.v, a);
+    if (err != cudaSuccess) return cuda_error(err, "launch(wide_attention)");
+    return launch_join<T, D, true>(a, grid, stream);
+}
+
+}  // namespace
+}  // namespace dspark

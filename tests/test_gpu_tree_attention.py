@@ -94,7 +94,7 @@ def test_many_requests_of_mixed_lengths(cuda_lib, B):
 
 @pytest.mark.parametrize("dtype", ["bf16", "f16"])
 @pytest.mark.parametrize("bad", [math.nan, math.inf, -math.inf])
-@pytest.mark.parametrize("N,G", [(5, 2), (12, 4), (20, 5)])
+@pytest.mark.parametrize("N,G", [(5, 2), (12, 4), (20, 5), (40, 4), (61, 5)])
 def test_infinities_and_nan_reach_only_rows_that_see_them(cuda_lib, dtype, bad, N, G):
     import torch
     lens = [200, 131, 64]

@@ -97,7 +97,7 @@ def test_scores_that_grow_scales_below_zero_and_of_zero(cuda_lib):
 
 @pytest.mark.parametrize("dtype", ["bf16", "f16"])
 @pytest.mark.parametrize("bad", [math.nan, math.inf, -math.inf])
-@pytest.mark.parametrize("N,G", [(3, 2), (12, 4), (20, 5)])
+@pytest.mark.parametrize("N,G", [(3, 2), (12, 4), (20, 5), (40, 4), (61, 5)])
 def test_infinities_and_nan_reach_only_rows_that_see_them(cuda_lib, dtype, bad, N, G):
     """A value in the tile where the window begins: the first rows see it, the later ones do not."""
     import torch
