@@ -1147,56 +1147,76 @@ __global__ void __launch_bounds__(kJoinRows * D) paged_join_kernel(const __grid_
 
 // ---------------------------------------------------------------------------
 // Join with kMasked, whose units have up to 256 rows: a warp adds a row over the unit's partial results in order, a
-// lane D / 32 columns.  Block (c, y) takes every (gridDim.y)-th eight rows of the unit that CTA c's run begins inside
-// of.  (paged_join_kernel's block for every four rows took 45 us for two partial results of each of 38000 rows.)
+// lane D / 32 columns.  Block (c, y) takes eight rows at a time of the unit that CTA c's run begins inside of; the last
+// kClearBlocks columns of blocks clear the rows that see nothing because their request or window token does not exist.
+// The loops are not unrolled further than their loads need: the instructions come from memory each time.
+// (paged_join_kernel's block for every four rows took 45 us for two partial results of each of 38000 rows.)
 // ---------------------------------------------------------------------------
-constexpr int kRowJoinWarps = 8, kRowJoinHigh = 8;
+constexpr int kRowJoinWarps = 8, kRowJoinHigh = 32, kClearBlocks = 16;
 
 template <typename T, int D>
 __global__ void __launch_bounds__(32 * kRowJoinWarps) row_join_kernel(const __grid_constant__ PagedArgs a) {
-    constexpr int kCols = D / 32, kFirst = 8;
+    constexpr int kCols = D / 32, kFirst = 4;
     using Part = typename std::conditional<kCols == 4, float4, float2>::type;
-    const int lane = static_cast<int>(lane_id()), warp = static_cast<int>(warp_id());
+    const uint32_t lane = lane_id(), warp = warp_id();
     grid_dependency_wait();
+    const uint32_t starts = gridDim.x - kClearBlocks;
+    if (blockIdx.x >= starts) {
+        // rows without a request or window token, a warp each
+        const uint32_t warps = kClearBlocks * gridDim.y * kRowJoinWarps, all = static_cast<uint32_t>(a.B) * static_cast<uint32_t>(a.N);
+#pragma unroll 1
+        for (uint32_t w = ((blockIdx.x - starts) * gridDim.y + blockIdx.y) * kRowJoinWarps + warp; w < all; w += warps) {
+            const uint32_t rb = w / static_cast<uint32_t>(a.N);
+            int kv, m;
+            request<true>(a, static_cast<int>(rb), kv, m);
+            if (static_cast<int>(w - rb * static_cast<uint32_t>(a.N)) < m) continue;
+            uint4* dst = reinterpret_cast<uint4*>(static_cast<T*>(a.out) + static_cast<long long>(w) * a.Hq * D);
+#pragma unroll 1
+            for (uint32_t x = lane; x < static_cast<uint32_t>(a.Hq) * (D / 8); x += 32) dst[x] = make_uint4(0u, 0u, 0u, 0u);
+#pragma unroll 1
+            for (uint32_t x = lane; a.lse && x < static_cast<uint32_t>(a.Hq); x += 32)
+                a.lse[static_cast<long long>(w) * a.Hq + x] = -INFINITY;
+        }
+        return;
+    }
     const int c = static_cast<int>(blockIdx.x) + 1;
     const PlanEntry& at = a.plan->entry[c < kMaxCtas ? c : 0];
     const int count = c < a.plan->ctas ? at.joined : 0;
     const int rows = count > 0 ? min(a.unit_tokens, at.n - at.rt * a.unit_tokens) * a.group : 0;
-    for (int row = static_cast<int>(blockIdx.y) * kRowJoinWarps + warp; row < rows; row += static_cast<int>(gridDim.y) * kRowJoinWarps) {
+#pragma unroll 1
+    for (int row = static_cast<int>(blockIdx.y * kRowJoinWarps + warp); row < rows; row += static_cast<int>(gridDim.y) * kRowJoinWarps) {
         // the row's k-th partial result: CTA c - 1 opened the unit, the others went on with it
-        auto place = [&](int k) { return static_cast<long long>(2 * (c - 1 + k) + (k == 0 ? 1 : 0)) * a.rows_cap + row; };
+        auto place = [&](int k) { return static_cast<size_t>((2 * (c - 1 + k) + (k == 0 ? 1 : 0)) * a.rows_cap + row); };
         auto part = [&](int k) { return reinterpret_cast<const Part*>(a.part_o + place(k) * D)[lane]; };
+        const float2* stats = reinterpret_cast<const float2*>(a.part_ml);
         Part v[kFirst];                                       // under way while the factors are found
 #pragma unroll
         for (int k = 0; k < kFirst; ++k)
             if (k < count) v[k] = part(k);
         float top = -INFINITY;
-        for (int k = lane; k < count; k += 32) top = fmaxf(top, reinterpret_cast<const float2*>(a.part_ml)[place(k)].x);
-        for (int d = 16; d > 0; d >>= 1) top = fmaxf(top, __shfl_xor_sync(0xFFFFFFFFu, top, d));
+#pragma unroll 1
+        for (int k = static_cast<int>(lane); k < count; k += 32) top = fmaxf(top, stats[place(k)].x);
+        top = float_from_order_bits(__reduce_max_sync(0xFFFFFFFFu, float_order_bits(top)));
         float o[kCols] = {}, sum = 0.0f;
-        auto add = [&](const Part& p, float f) {
-            const float* x = reinterpret_cast<const float*>(&p);
-#pragma unroll
-            for (int e = 0; e < kCols; ++e) o[e] = fmaf(f, x[e], o[e]);
-        };
+#pragma unroll 1
         for (int k0 = 0; k0 < count; k0 += 32) {
-            float2 ml = make_float2(-INFINITY, 0.0f);
-            if (k0 + lane < count) ml = reinterpret_cast<const float2*>(a.part_ml)[place(k0 + lane)];
+            const int mine = k0 + static_cast<int>(lane);     // this lane finds the factor of this one
+            const float2 ml = mine < count ? stats[place(mine)] : make_float2(-INFINITY, 0.0f);
             const bool none = ml.x == -INFINITY;              // its sum is then 0, or NaN
             const float f = none ? ml.y : exp2_approx(ml.x - top);
-            float part_sum = none ? ml.y : ml.y * f;
-            for (int d = 16; d > 0; d >>= 1) part_sum += __shfl_xor_sync(0xFFFFFFFFu, part_sum, d);
-            sum += part_sum;
-            if (k0 == 0) {
+            sum += none ? ml.y : ml.y * f;
+#pragma unroll 1
+            for (int k = k0; k < min(count, k0 + 32); ++k) {
+                const float fk = __shfl_sync(0xFFFFFFFFu, f, k - k0);
+                const float* x = reinterpret_cast<const float*>(&v[0]);
 #pragma unroll
-                for (int k = 0; k < kFirst; ++k) {
-                    const float fk = __shfl_sync(0xFFFFFFFFu, f, k);
-                    if (k < count) add(v[k], fk);
-                }
+                for (int e = 0; e < kCols; ++e) o[e] = fmaf(fk, x[e], o[e]);
+#pragma unroll
+                for (int y = 0; y + 1 < kFirst; ++y) v[y] = v[y + 1];
+                if (k + kFirst < count) v[kFirst - 1] = part(k + kFirst);
             }
-#pragma unroll 4
-            for (int k = k0 == 0 ? kFirst : 0; k < min(32, count - k0); ++k) add(part(k0 + k), __shfl_sync(0xFFFFFFFFu, f, k));
         }
+        for (int d = 16; d > 0; d >>= 1) sum += __shfl_xor_sync(0xFFFFFFFFu, sum, d);
         const float inv = sum != 0.0f ? 1.0f / sum : 0.0f;
         const int rt = row / a.group;
         const long long to = (static_cast<long long>(at.b) * a.N + at.rt * a.unit_tokens + rt) * a.Hq + at.h * a.group + (row - rt * a.group);
@@ -1207,20 +1227,6 @@ __global__ void __launch_bounds__(32 * kRowJoinWarps) row_join_kernel(const __gr
         if constexpr (kCols == 4) *reinterpret_cast<uint2*>(dst) = make_uint2(packed[0], packed[1]);
         else *dst = packed[0];
         if (lane == 0 && a.lse) a.lse[to] = lse_of(top, sum);
-    }
-
-    // rows without a request or window token, a warp each
-    const long long warps = static_cast<long long>(gridDim.x) * gridDim.y * kRowJoinWarps;
-    for (long long w = (static_cast<long long>(blockIdx.y) * gridDim.x + blockIdx.x) * kRowJoinWarps + warp;
-         w < static_cast<long long>(a.B) * a.N; w += warps) {
-        const int rb = static_cast<int>(quotient(w, a.N)), i = static_cast<int>(w - static_cast<long long>(rb) * a.N);
-        int kv, m;
-        request<true>(a, rb, kv, m);
-        if (i < m) continue;
-        uint4* dst = reinterpret_cast<uint4*>(static_cast<T*>(a.out) + w * a.Hq * D);
-        for (int x = lane; x < a.Hq * (D / 8); x += 32) dst[x] = make_uint4(0u, 0u, 0u, 0u);
-        if (a.lse)
-            for (int x = lane; x < a.Hq; x += 32) a.lse[w * a.Hq + x] = -INFINITY;
     }
 }
 
@@ -1271,7 +1277,7 @@ dspark_status launch_join(const PagedArgs& a, int grid, cudaStream_t stream) {
     const int rows = a.unit_tokens * a.group;
     cudaError_t err;
     if constexpr (kMasked)
-        err = launch_dependent(row_join_kernel<T, D>, dim3(grid, std::min(kRowJoinHigh, (rows + kRowJoinWarps - 1) / kRowJoinWarps)),
+        err = launch_dependent(row_join_kernel<T, D>, dim3(grid + kClearBlocks, std::min(kRowJoinHigh, (rows + kRowJoinWarps - 1) / kRowJoinWarps)),
                                dim3(32 * kRowJoinWarps), 0, stream, a);
     else
         err = launch_dependent(paged_join_kernel<T, D>, dim3(grid, (rows + kJoinRows - 1) / kJoinRows), dim3(kJoinRows * D), 0, stream, a);

@@ -46,6 +46,7 @@ struct Smem {
     alignas(1024) uint4 stage[16][128];                           // 32 columns of a warp's rows; a row of values in a later pass
     Item item[kAhead];
     float half[2][2][kTile];                                      // by row tile and half of the key tiles: a row's largest score, or sum
+    uint8_t token_of[kTile];                                      // of a row tile's rows
     uint32_t masks[2][4];
     uint32_t again, failed;                                       // further passes are needed / a wait gave up
     uint64_t item_full[kAhead], item_empty[kAhead];
@@ -54,6 +55,14 @@ struct Smem {
     uint64_t s_full[2], p_first[2], p_last[2], pv_done[2], o_empty[2], turn[2], drain;
     uint32_t tmem_base;
 };
+
+// Which of the 64 tokens from j on row `tok` sees.  Out of line, and called where little else is alive: it is needed in few
+// tiles, and the softmax has no registers to spare.
+inline __device__ __noinline__ uint2 row_bits(const PagedArgs& a, const Segment<true>& g, int tok, bool valid, int j) {
+    SeenBits<64> sees;
+    RowMask<true>(a, g, tok, valid).get(a, j, sees);
+    return make_uint2(sees.word[0], sees.word[1]);
+}
 
 }  // namespace wide
 
@@ -98,6 +107,7 @@ wide_attention_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_cons
         prefetch_tensormap(&tmK);
         prefetch_tensormap(&tmV);
     }
+    if (threadIdx.x < kTile) s.token_of[threadIdx.x] = static_cast<uint8_t>(threadIdx.x / a.group);
     if (warp == kWarpMma) {
         tmem_alloc(&s.tmem_base, wide::kTmemCols);
         tmem_relinquish();
@@ -137,9 +147,15 @@ wide_attention_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_cons
             while (ok) {
                 const bool more = walk.next(g);
                 int n[2];
-                for (int x = 0; x < 2; ++x)
-                    n[x] = more && g.rt * a.unit_tokens + x * a.tile_tokens < g.n && (pass == 0 || pass == x + 1) ? g.t1 - g.t0 : 0;
+                for (int x = 0; x < 2; ++x) {
+                    const int first = g.rt * a.unit_tokens + x * a.tile_tokens;
+                    n[x] = more && first < g.n && (pass == 0 || pass == x + 1) ? g.t1 - g.t0 : 0;
+                    // tiles behind what the row tile's last row sees are for the other alone; one is always there
+                    if (n[x] > 0 && a.causal && (x == 0 || pass == 0))
+                        while (n[x] > 1 && g.place(g.t0 + n[x] - 1) * kTile >= g.kv - g.n + min(g.n, first + a.tile_tokens)) --n[x];
+                }
                 if (more && n[0] + n[1] == 0) continue;
+                const int t1 = g.t0 + max(n[0], n[1]);
                 ok = all(wait(s.item_empty[count % wide::kAhead], count / wide::kAhead + 1, wide::kWaitLoad));
                 if (!ok) break;
                 if (lane == 0) {
@@ -167,8 +183,8 @@ wide_attention_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_cons
                     ++qt[x];
                 }
                 int page = lookup(g, g.t0);
-                for (int t = g.t0; ok && t < g.t1; ++t, ++kt) {
-                    const int next = t + 1 < g.t1 ? lookup(g, t + 1) : -2;
+                for (int t = g.t0; ok && t < t1; ++t, ++kt) {
+                    const int next = t + 1 < t1 ? lookup(g, t + 1) : -2;
                     const int slot = kt % kSlots;
                     const uint32_t bytes = __popc(__ballot_sync(0xFFFFFFFFu, page != -2)) * box_bytes;
                     const int y = (g.place(t) * kTile + box * a.box_rows) & (a.page - 1);
@@ -222,8 +238,8 @@ wide_attention_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_cons
                 if (!ok) break;
                 const Item& it = s.item[count % wide::kAhead];
                 const int n = __shfl_sync(0xFFFFFFFFu, it.n[w], 0), other = __shfl_sync(0xFFFFFFFFu, it.n[1 - w], 0);
-                // tokens that the request holds from the segment's last tile on
-                const int held = __shfl_sync(0xFFFFFFFFu, it.g.kv - it.g.place(it.g.t1 - 1) * kTile, 0);
+                // tokens that the request holds from the last of these tiles on
+                const int held = __shfl_sync(0xFFFFFFFFu, it.g.kv - it.g.place(it.g.t0 + max(it.n[0], it.n[1]) - 1) * kTile, 0);
                 __syncwarp();
                 if (lane == 0) mbar_arrive(&s.item_empty[count % wide::kAhead]);
                 ++count;
@@ -322,7 +338,8 @@ wide_attention_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_cons
             // A masked score is infinite and gets no weight by that, for which the slope must not be 0: the smallest step above
             // it (no product of finite values then reaches 2^-20) stands for a scale of 0.
             const float steep = sl2 == 0.0f ? 0x1p-149f : sl2;
-            const bool redo = pass != 0;
+            auto rows_of_pass = [&](auto later) {
+            constexpr bool redo = decltype(later)::value;
             while (true) {
                 ok = named_bar_and(bar_tile, wide::kRowThreads, wait(s.item_full[count % wide::kAhead], count / wide::kAhead, wide::kWaitSoftmax));
                 if (!ok) break;
@@ -346,24 +363,24 @@ wide_attention_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_cons
                 const int sinks = a.window > 0 ? a.sinks : 0;
                 float m2 = -INFINITY, l = 0.0f;
                 for (int t = 0; t < n; ++t, ++i) {
+                    const int j = g.place(g.t0 + t) * kTile;
+                    const bool masked = j + kTile > to || (j < from && j + kTile > sinks);
+                    uint2 sees = make_uint2(0xFFFFFFFFu, 0xFFFFFFFFu);
+                    if (masked) sees = row_bits(a, g, tok, valid, j + part * 64);
                     bool go = wait(s.s_full[w], i, wide::kWaitSoftmax);
                     if (redo) go = named_bar_and(bar_tile, wide::kRowThreads, go);  // these meet in barriers below
                     go = all(go);
                     // 64 scores in registers
                     uint32_t r[2][32];
-                    const int j = g.place(g.t0 + t) * kTile;
-                    const bool masked = j + kTile > to || (j < from && j + kTile > sinks);
                     tc_fence_after();
                     tmem_ld32(tS, r[0]);
                     tmem_ld32(tS + 32, r[1]);
                     tmem_wait_ld32(r[0]);
                     tmem_wait_ld32(r[1]);
                     if (masked) {                             // an infinite score has no weight
-                        SeenBits<64> sees;
-                        RowMask<true>(a, g, tok, valid).get(a, j + part * 64, sees);
 #pragma unroll
                         for (int c = 0; c < 64; ++c)
-                            if (!sees.has(c)) r[c >> 5][c & 31] = __float_as_uint(none);
+                            if (!(((c < 32 ? sees.x : sees.y) >> (c & 31)) & 1u)) r[c >> 5][c & 31] = __float_as_uint(none);
                     }
                     float best[4] = {none, none, none, none};
                     if (!falling) {
@@ -459,8 +476,11 @@ wide_attention_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_cons
                             SeenBits<128> whole;
                             whole.all();
                             if (masked) {
-                                const RowMask<true> mask(a, g, tok, valid);
-                                mask.get(a, j, whole);
+                                const uint2 other = row_bits(a, g, tok, valid, j + 64);
+                                whole.word[0] = sees.x;
+                                whole.word[1] = sees.y;
+                                whole.word[2] = other.x;
+                                whole.word[3] = other.y;
                             }
                             move_infinities<T>(s.v[slot], kBlockBytes, kHalves, row, g.kv - j, [=](int x) { return whole.at(x); }, tP, tO,
                                                reinterpret_cast<float*>(s.stage[8 * w]), s.masks[w], kBarFirst + static_cast<uint32_t>(w));
@@ -488,60 +508,45 @@ wide_attention_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_cons
                 const int rows = min(a.tile_tokens, g.n - first) * a.group;
                 const long long row0 = (static_cast<long long>(g.b) * a.N + first) * a.Hq + g.h * a.group;
                 const long long part_base = static_cast<long long>(2 * blockIdx.x + (g.t0 == 0 ? 1 : 0)) * a.rows_cap + w * a.tile_tokens * a.group;
-                // through shared memory, so that four lanes write a row's piece together: 32 columns of the output, or 16
-                // of a partial result, at a time
-                const int piece = static_cast<int>(lane) & 3;
-                long long to_row[4];                                      // this lane's four rows (-1: none)
-#pragma unroll
-                for (int y = 0; y < 4; ++y) {
-                    const int rr = static_cast<int>(quad) * 32 + y * 8 + (static_cast<int>(lane) >> 2);
-                    const int rt = rr / a.group;
-                    to_row[y] = rr >= rows ? -1 : whole ? row0 + static_cast<long long>(rt) * a.Hq + (rr - rt * a.group) : part_base + rr;
-                }
+                // 16 columns at a time through shared memory, so that the lanes write pieces of a row together.  Short code
+                // counts here: it is run once per unit, and its instructions come from the L2 cache each time.
+                const int pieces = whole ? 2 : 4;                         // of 16 bytes, in 16 columns of a row
 #pragma unroll 1
-                for (int c = 0; c < D / 2; c += 32) {
-                    float o[32];
-                    tmem_ld32(tO + c, reinterpret_cast<uint32_t*>(o));
-                    tmem_wait_ld32(reinterpret_cast<uint32_t*>(o));
-                    if (c + 32 == D / 2) {
+                for (int c = 0; c < D / 2; c += 16) {
+                    uint32_t o[16];
+                    tmem_ld16(tO + c, o);
+                    tmem_wait_ld();
+                    if (c + 16 == D / 2) {
                         tc_fence_before();
                         mbar_arrive(&s.o_empty[w]);
                     }
+                    __syncwarp();                                         // the columns before have been read
 #pragma unroll
-                    for (int x = 0; x < 32; ++x) {
-                        check[x & 3] = fmaf(o[x], 0.0f, check[x & 3]);
-                        o[x] *= f;
+                    for (int x = 0; x < 16; ++x) {
+                        check[x & 3] = fmaf(__uint_as_float(o[x]), 0.0f, check[x & 3]);
+                        o[x] = __float_as_uint(__uint_as_float(o[x]) * f);
                     }
-                    const int col = part * (D / 2) + c;
                     if (whole) {
-                        __syncwarp();                                     // the columns before have been read
 #pragma unroll
-                        for (int x = 0; x < 4; ++x) stage[lane * 4 + (x ^ ((lane >> 1) & 3))] = pack8(o + 8 * x, T{});
-                        __syncwarp();
-#pragma unroll
-                        for (int y = 0; y < 4; ++y) {
-                            const int at = y * 8 + (static_cast<int>(lane) >> 2);
-                            if (to_row[y] >= 0)
-                                *reinterpret_cast<uint4*>(static_cast<T*>(a.out) + to_row[y] * D + col + piece * 8) =
-                                    stage[at * 4 + (piece ^ ((at >> 1) & 3))];
-                        }
+                        for (int x = 0; x < 2; ++x)
+                            stage[(lane * 2 + x) ^ ((lane >> 2) & 1)] = pack8(reinterpret_cast<const float*>(o) + 8 * x, T{});
                     } else {
 #pragma unroll
-                        for (int z = 0; z < 2; ++z) {
-                            __syncwarp();
-#pragma unroll
-                            for (int x = 0; x < 4; ++x)
-                                stage[lane * 4 + (x ^ ((lane >> 1) & 3))] =
-                                    make_uint4(__float_as_uint(o[16 * z + 4 * x]), __float_as_uint(o[16 * z + 4 * x + 1]),
-                                               __float_as_uint(o[16 * z + 4 * x + 2]), __float_as_uint(o[16 * z + 4 * x + 3]));
-                            __syncwarp();
-#pragma unroll
-                            for (int y = 0; y < 4; ++y) {
-                                const int at = y * 8 + (static_cast<int>(lane) >> 2);
-                                if (to_row[y] >= 0)
-                                    *reinterpret_cast<uint4*>(a.part_o + to_row[y] * D + col + 16 * z + piece * 4) =
-                                        stage[at * 4 + (piece ^ ((at >> 1) & 3))];
-                            }
+                        for (int x = 0; x < 4; ++x)
+                            stage[lane * 4 + (x ^ ((lane >> 1) & 3))] = make_uint4(o[4 * x], o[4 * x + 1], o[4 * x + 2], o[4 * x + 3]);
+                    }
+                    __syncwarp();
+                    const int col = part * (D / 2) + c;
+#pragma unroll 1
+                    for (int x = static_cast<int>(lane); x < 32 * pieces; x += 32) {
+                        const int at = x / pieces, piece = x - at * pieces, rr = static_cast<int>(quad) * 32 + at;
+                        if (rr >= rows) break;
+                        if (whole) {
+                            const int rt = s.token_of[rr];
+                            const long long to_row = row0 + static_cast<long long>(rt) * a.Hq + (rr - rt * a.group);
+                            *reinterpret_cast<uint4*>(static_cast<T*>(a.out) + to_row * D + col + piece * 8) = stage[(at * 2 + piece) ^ ((at >> 2) & 1)];
+                        } else {
+                            *reinterpret_cast<uint4*>(a.part_o + (part_base + rr) * D + col + piece * 4) = stage[at * 4 + (piece ^ ((at >> 1) & 3))];
                         }
                     }
                 }
@@ -549,10 +554,13 @@ wide_attention_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_cons
                     if (!whole) reinterpret_cast<float2*>(a.part_ml)[part_base + row] = make_float2(m2, l);
                     else if (a.lse) a.lse[(static_cast<long long>(g.b) * a.N + tok) * a.Hq + g.h * a.group + (row - row_tok * a.group)] = lse_of(m2, l);
                 }
-                if (pass == 0 && valid && check[0] + check[1] + check[2] + check[3] != 0.0f) s.again = 1u;
+                if (!redo && valid && check[0] + check[1] + check[2] + check[3] != 0.0f) s.again = 1u;
                 __syncwarp();
                 mbar_arrive(&s.item_empty[count++ % wide::kAhead]);
             }
+            };
+            if (pass == 0) rows_of_pass(std::false_type{});
+            else rows_of_pass(std::true_type{});
         }
         if (!ok) s.failed = 1u;
         __syncthreads();
