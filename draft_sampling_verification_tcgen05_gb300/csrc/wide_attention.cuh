@@ -4,7 +4,9 @@
 // runs, partial results, plan and join are those of paged_attention.cuh.
 //
 //   warps 0-7, 8-15  softmax and results of one row tile each: two threads per row, 64 of a key tile's tokens each
-//   warp 16          walks the run's segments and loads (TMA) queries, and page by page keys and values
+//   warp 16          walks the run's segments and loads (TMA) queries, and page by page keys
+//   warp 19          loads the values (with pages of 16 a tile is 16 boxes, whose issue takes 1300 cycles: one warp for both
+//                    loads was slower than the products, 77 us for 16 trees of 64 nodes over 500 to 8000 tokens)
 //   warps 17, 18     issue S = Q K^T and O += P V of one row tile each on tcgen05 (M = 128, fp32 in tensor memory; P
 //                    replaces half of S)
 //
@@ -19,12 +21,12 @@ namespace {
 
 namespace wide {
 
-constexpr int kThreads = 608;
+constexpr int kThreads = 640;
 constexpr int kRowThreads = 256;           // softmax threads of a row tile: two to a row, 64 of a key tile's tokens each
 constexpr int kAhead = 4;                  // segments between the loads and the results
 constexpr int kSlots = 2;                  // key tiles, and value tiles, in flight
 constexpr uint32_t kColS = 0, kColP = 64, kColO = 256, kTmemCols = 512;    // S and O of tile 1: + 128
-constexpr uint32_t kWarpLoad = 16, kWarpMma = 17;
+constexpr uint32_t kWarpLoad = 16, kWarpMma = 17, kWarpValues = 19;
 // named barriers: + row tile; + 4 * row tile + quadrant, the two warps of the same rows; + row tile
 constexpr uint32_t kBarTile = 1, kBarRows = 3, kBarFirst = 11;
 constexpr uint32_t kWaitLoad = 0x811, kWaitMma = 0x812, kWaitSoftmax = 0x813;
@@ -82,7 +84,7 @@ wide_attention_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_cons
     if (threadIdx.x == 0) {
         for (int i = 0; i < wide::kAhead; ++i) {
             mbar_init(&s.item_full[i], 1);
-            mbar_init(&s.item_empty[i], 2 * wide::kRowThreads + 2);
+            mbar_init(&s.item_empty[i], 2 * wide::kRowThreads + 3);
         }
         for (int i = 0; i < 2; ++i) {
             mbar_init(&s.q_full[i], 1);
@@ -127,8 +129,13 @@ wide_attention_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_cons
     int count = 0, kt = 0, i = 0, used = 0, turn = 0, qt[2] = {0, 0};
     // Pass 0 is all there is, as a rule; passes 1 and 2 take one row tile each.
     for (int pass = 0;; ++pass) {
-        if (warp == kWarpLoad) {
+        if (warp == kWarpLoad || warp == kWarpValues) {
             // ---------------- segments and loads ----------------
+            const bool keys = warp == kWarpLoad;
+            const CUtensorMap* map = keys ? &tmK : &tmV;
+            uint8_t* ring = keys ? s.k[0] : s.v[0];
+            uint64_t* full = keys ? s.k_full : s.v_full;
+            uint64_t* empty = keys ? s.k_empty : s.v_empty;
             const uint64_t keep = l2_policy_evict_last();
             const int page_bits = __ffs(a.page) - 1;
             const int boxes = kTile / a.box_rows * kHalves;
@@ -145,31 +152,42 @@ wide_attention_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_cons
             Walker<true> walk(a);
             Segment<true> g{};
             while (ok) {
-                const bool more = walk.next(g);
                 int n[2];
-                for (int x = 0; x < 2; ++x) {
-                    const int first = g.rt * a.unit_tokens + x * a.tile_tokens;
-                    n[x] = more && first < g.n && (pass == 0 || pass == x + 1) ? g.t1 - g.t0 : 0;
-                    // tiles behind what the row tile's last row sees are for the other alone; one is always there
-                    if (n[x] > 0 && a.causal && (x == 0 || pass == 0))
-                        while (n[x] > 1 && g.place(g.t0 + n[x] - 1) * kTile >= g.kv - g.n + min(g.n, first + a.tile_tokens)) --n[x];
+                if (keys) {
+                    const bool more = walk.next(g);
+                    for (int x = 0; x < 2; ++x) {
+                        const int first = g.rt * a.unit_tokens + x * a.tile_tokens;
+                        n[x] = more && first < g.n && (pass == 0 || pass == x + 1) ? g.t1 - g.t0 : 0;
+                        // tiles behind what the row tile's last row sees are for the other alone; one is always there
+                        if (n[x] > 0 && a.causal)
+                            while (n[x] > 1 && g.place(g.t0 + n[x] - 1) * kTile >= g.kv - g.n + min(g.n, first + a.tile_tokens)) --n[x];
+                    }
+                    if (more && n[0] + n[1] == 0) continue;
+                    ok = all(wait(s.item_empty[count % wide::kAhead], count / wide::kAhead + 1, wide::kWaitLoad));
+                    if (!ok) break;
+                    if (lane == 0) {
+                        Item& it = s.item[count % wide::kAhead];
+                        it.g = g;
+                        it.n[0] = n[0];
+                        it.n[1] = n[1];
+                        mbar_arrive(&s.item_full[count % wide::kAhead]);
+                    }
+                    __syncwarp();
+                } else {
+                    ok = all(wait(s.item_full[count % wide::kAhead], count / wide::kAhead, wide::kWaitLoad));
+                    if (!ok) break;
+                    const Item& it = s.item[count % wide::kAhead];
+                    g = it.g;
+                    n[0] = it.n[0];
+                    n[1] = it.n[1];
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(&s.item_empty[count % wide::kAhead]);
                 }
-                if (more && n[0] + n[1] == 0) continue;
-                const int t1 = g.t0 + max(n[0], n[1]);
-                ok = all(wait(s.item_empty[count % wide::kAhead], count / wide::kAhead + 1, wide::kWaitLoad));
-                if (!ok) break;
-                if (lane == 0) {
-                    Item& it = s.item[count % wide::kAhead];
-                    it.g = g;
-                    if (!more) it.g.t0 = it.g.t1 = 0;
-                    it.n[0] = n[0];
-                    it.n[1] = n[1];
-                    mbar_arrive(&s.item_full[count % wide::kAhead]);
-                }
-                __syncwarp();
                 ++count;
-                if (!more) break;
-                for (int x = 0; ok && x < 2; ++x) {
+                const int t1 = g.t0 + max(n[0], n[1]);
+                if (t1 == g.t0) break;                        // the end of the pass
+                int page = lookup(g, g.t0);
+                for (int x = 0; keys && ok && x < 2; ++x) {
                     if (n[x] == 0) continue;
                     ok = all(wait(s.q_empty[x], qt[x] + 1, wide::kWaitLoad));
                     if (!ok) break;
@@ -182,32 +200,29 @@ wide_attention_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_cons
                     __syncwarp();
                     ++qt[x];
                 }
-                int page = lookup(g, g.t0);
                 for (int t = g.t0; ok && t < t1; ++t, ++kt) {
                     const int next = t + 1 < t1 ? lookup(g, t + 1) : -2;
                     const int slot = kt % kSlots;
+                    ok = all(wait(empty[slot], kt / kSlots + 1, wide::kWaitLoad));
+                    if (!ok) break;
                     const uint32_t bytes = __popc(__ballot_sync(0xFFFFFFFFu, page != -2)) * box_bytes;
-                    const int y = (g.place(t) * kTile + box * a.box_rows) & (a.page - 1);
-                    int z = page * a.Hkv + g.h;
-                    if (page == -3) {
-                        z = a.num_pages * a.Hkv;              // outside the map: reads zeros
-                    } else if (page != -2 && (page < 0 || page >= a.num_pages)) {
-                        flag_input_index(ws);
-                        z = g.h;
-                    }
-                    for (int x = 0; x < 2; ++x) {             // keys, values
-                        uint64_t* full = x == 0 ? s.k_full : s.v_full;
-                        ok = all(wait(x == 0 ? s.k_empty[slot] : s.v_empty[slot], kt / kSlots + 1, wide::kWaitLoad));
-                        if (!ok) break;
-                        if (lane == 0) mbar_arrive_expect_tx(&full[slot], bytes);
-                        __syncwarp();
-                        if (page != -2)
-                            tma_load_3d((x == 0 ? s.k[slot] : s.v[slot]) + box_at, x == 0 ? &tmK : &tmV, half * 64, y, z, &full[slot], keep);
+                    if (lane == 0) mbar_arrive_expect_tx(&full[slot], bytes);
+                    __syncwarp();
+                    if (page != -2) {
+                        const int y = (g.place(t) * kTile + box * a.box_rows) & (a.page - 1);
+                        int z = page * a.Hkv + g.h;
+                        if (page == -3) {
+                            z = a.num_pages * a.Hkv;              // outside the map: reads zeros
+                        } else if (page < 0 || page >= a.num_pages) {
+                            flag_input_index(ws);
+                            z = g.h;
+                        }
+                        tma_load_3d(ring + slot * kTileBytes + box_at, map, half * 64, y, z, &full[slot], keep);
                     }
                     page = next;
                 }
             }
-            grid_dependency_launch();
+            if (keys) grid_dependency_launch();
             if (!ok) {
                 // give copies in flight time to land before the block exits
                 const long long t0 = global_ns();
