@@ -133,6 +133,51 @@ def test_uniforms_at_the_ends_and_equal_logits(cuda_lib):
     case.check(cuda_lib)
 
 
+@pytest.mark.parametrize("bf16", [False, True])
+@pytest.mark.parametrize("V", [997, 30011, 151936])
+def test_draws_at_the_ends_of_entries(cuda_lib, V, bf16):
+    """Uniforms whose share of the mass is an entry's first unit, its last, or next to them: sums in fp32 cannot tell."""
+    import torch
+    case = VerifyCase(24, 1, V, seed=V, bf16=bf16, follow=0.0)
+    case.T[:] = np.tile([0.6, 1.0, 2.5], 8).astype(np.float32)
+    w = _weights(case.target[:, 0].float(), torch.from_numpy(case.T).cuda()).cpu().numpy().astype(np.float64)
+    rng = np.random.default_rng(1)
+    for b in range(24):
+        mass = np.floor(w[b] * MASS).astype(np.uint64)
+        ends = np.cumsum(mass)
+        v = int(np.searchsorted(ends, np.uint64(int(rng.integers(0, int(ends[-1])))), side="right"))
+        # the smallest uniform that is past entry v - 1, and its neighbours
+        u = -(-int(ends[v] - mass[v]) * 2 ** 24 // int(ends[-1])) + b % 3 - 1
+        case.u[b, 0] = min(max(u, 0), 2 ** 24 - 1) * 2.0 ** -24
+    case.check(cuda_lib)
+
+
+@pytest.mark.parametrize("T", [0.01, 0.1, 30.0, 1e4])
+@pytest.mark.parametrize("gain", [0.01, 3.0, 100.0, 1e6])
+def test_scales_of_logits_and_temperatures(cuda_lib, T, gain):
+    import torch
+    case = VerifyCase(8, 3, 20011, seed=21, follow=0.0, gain=gain)
+    case.T[:] = T
+    case.check(cuda_lib)
+    case.target += 1e5                                        # far from 0, where a shift loses bits
+    case.check(cuda_lib)
+    case.target[:, :, :700] = -math.inf                       # nothing to go by among the first entries
+    case.check(cuda_lib)
+
+
+@pytest.mark.parametrize("B", [1, 40, 700])
+def test_odd_values_in_rows_that_are_drawn_from(cuda_lib, B):
+    import torch
+    case = VerifyCase(B, 2, 5003, seed=B, follow=0.0)
+    case.T[:] = 1.0
+    ws = cuda_lib.Workspace(cuda_lib.OP_VERIFY_TREE, B, 2)
+    for at in (0, 1, 2500, 5002):
+        for value in (math.nan, math.inf):
+            case.target[::2, 0, at] = value
+            case.check(cuda_lib, workspace=ws)
+            assert cuda_lib.dspark_read_status(ws)[1] == cuda_lib.STATUS_NUMERIC
+
+
 def test_ties_go_to_the_lowest_id(cuda_lib):
     import torch
     case = VerifyCase(3, 3, 40009, seed=11, greedy=True, follow=0.0)
