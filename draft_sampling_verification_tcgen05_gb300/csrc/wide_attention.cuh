@@ -58,6 +58,13 @@ struct Smem {
     uint32_t tmem_base;
 };
 
+// 32 lanes x 32 bits, 8 consecutive columns from r[0..7].
+__device__ __forceinline__ void tmem_st8(uint32_t taddr, const uint32_t (&r)[8]) {
+    asm volatile("tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};"
+                 :: "r"(taddr), "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7])
+                 : "memory");
+}
+
 // Which of the 64 tokens from j on row `tok` sees.  Out of line, and called where little else is alive: it is needed in few
 // tiles, and the softmax has no registers to spare.
 inline __device__ __noinline__ uint2 row_bits(const PagedArgs& a, const Segment<true>& g, int tok, bool valid, int j) {
@@ -451,15 +458,18 @@ wide_attention_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_cons
                     // 32 weights, to P: one straight piece of code, for which the compiler finds an order that keeps the
                     // exponential's unit (4 cycles a warp) at work.
                     auto weigh = [&](int x) {
-                        uint32_t p[16];
 #pragma unroll
-                        for (int c = 0; c < 32; c += 2) {
-                            const float2 y = __ffma2_rn(make_float2(__uint_as_float(r[x][c]), __uint_as_float(r[x][c + 1])), slope, shift);
-                            const float2 e = make_float2(exp2_approx(y.x), exp2_approx(y.y));
-                            sum[(c >> 1) & 1] = __fadd2_rn(sum[(c >> 1) & 1], e);
-                            p[c >> 1] = pack2(e.x, e.y, T{});
+                        for (int z = 0; z < 2; ++z) {
+                            uint32_t p[8];
+#pragma unroll
+                            for (int c = 16 * z; c < 16 * z + 16; c += 2) {
+                                const float2 y = __ffma2_rn(make_float2(__uint_as_float(r[x][c]), __uint_as_float(r[x][c + 1])), slope, shift);
+                                const float2 e = make_float2(exp2_approx(y.x), exp2_approx(y.y));
+                                sum[(c >> 1) & 1] = __fadd2_rn(sum[(c >> 1) & 1], e);
+                                p[(c >> 1) & 7] = pack2(e.x, e.y, T{});
+                            }
+                            tmem_st8(tP + x * 16 + z * 8, p);
                         }
-                        tmem_st16(tP + x * 16, p);
                         tmem_wait_st();
                     };
                     weigh(0);
