@@ -13,8 +13,18 @@ int wide_cap_of(int N, int heads) { return static_cast<int>(std::min<long long>(
 
 template <typename T, int D>
 dspark_status launch(PagedArgs& a, int grid, cudaStream_t stream) {
-    // More rows than a tile holds: two tiles against one stream of keys and values.
-    if (a.N > a.tile_tokens) return launch_wide<T, D>(a, grid, stream);
+    // More rows than a tile holds: two tiles against one stream of keys and values (wide_attention.cuh), except where
+    // requests bring their own lengths and two tiles hold the longest.  Most of them then fill one tile, and a block that has one
+    // tile has nothing to do while that is in its softmax; two blocks' worth of single tiles it is then.
+    // Measured, wide / one tile at a time, 8 heads of keys, in us:
+    //   lengths given      16 trees of up to 64 nodes, 500 to 8000 keys  71.0 / 57.5     16 of up to 17 of 8 heads each  66.6 / 55.2
+    //                      33 of up to 64, D = 64, a window of 2048      84.0 / 76.5     1 of 64, 1000 keys              23.0 / 19.6
+    //                      4 of up to 64, 20000 to 60000 keys           150.5 / 172.2    64 of up to 64, 100 to 1000     69.0 / 74.2
+    //                      8 of up to 200, 200 to 4000 keys              76.2 / 98.2     (more than two tiles)
+    //   every row used     16 trees of 64 nodes, 500 to 8000 keys        80.7 / 82.9     16 of 17, 8 heads each          72.6 / 80.6
+    //                      4 of 64, 20000 to 60000 keys                 154.0 / 208.3    64 of 64, 100 to 1000           73.7 / 92.1
+    //                      2 chunks of 4096, a window of 1024           206   / 262      1 of 64, 1000 keys              23.1 / 19.6
+    if (a.N > (a.lengths ? 2 : 1) * a.tile_tokens) return launch_wide<T, D>(a, grid, stream);
     return launch_typed<T, D, true>(a, grid, stream);
 }
 
