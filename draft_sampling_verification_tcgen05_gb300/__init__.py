@@ -678,6 +678,11 @@ def dspark_sample(logits, temperature, top_k, top_p, min_p, u, tokens=None, prob
     return tokens
 
 
+def _int(x):
+    """x as the nearest C int: ctypes would cut the upper bits off."""
+    return x if -2147483648 <= x <= 2147483647 else 2147483647 if x > 0 else -2147483648
+
+
 @_on_its_stream
 def dspark_window_attention(q, k_cache, v_cache, block_table, kv_len, window: int, sinks: int, scale: float, lengths=None,
                             causal: bool = True, out=None, lse=None, workspace=None, stream=None):
@@ -688,7 +693,7 @@ def dspark_window_attention(q, k_cache, v_cache, block_table, kv_len, window: in
     num_pages, Hkv, page, _ = k_cache.shape
     ws = workspace if workspace is not None else Workspace(OP_WINDOW_ATTENTION, B, N, Hq, D, q.device)
     _check(lib().dspark_window_attention(_ptr(q), _ptr(k_cache), _ptr(v_cache), dt, _ptr(block_table), block_table.shape[1],
-                                         _ptr(kv_len), _ptr(lengths), window, sinks, scale, int(causal), B, N, Hq, Hkv, D,
+                                         _ptr(kv_len), _ptr(lengths), _int(window), _int(sinks), scale, int(causal), B, N, Hq, Hkv, D,
                                          num_pages, page, _ptr(out), _ptr(lse), ws.address, ws.nbytes, _stream(stream)),
            "dspark_window_attention")
     return out
@@ -712,7 +717,7 @@ def dspark_tree_attention(q, k_cache, v_cache, block_table, kv_len, parents, sca
         raise ValueError("parents must be [B, N]")
     ws = workspace if workspace is not None else Workspace(OP_TREE_ATTENTION, B, N, Hq, D, q.device)
     _check(lib().dspark_tree_attention(_ptr(q), _ptr(k_cache), _ptr(v_cache), dt, _ptr(block_table), block_table.shape[1],
-                                       _ptr(kv_len), _ptr(lengths), _ptr(parents), window, sinks, scale, B, N, Hq, Hkv, D,
+                                       _ptr(kv_len), _ptr(lengths), _ptr(parents), _int(window), _int(sinks), scale, B, N, Hq, Hkv, D,
                                        num_pages, page, _ptr(out), _ptr(lse), ws.address, ws.nbytes, _stream(stream)),
            "dspark_tree_attention")
     return out
