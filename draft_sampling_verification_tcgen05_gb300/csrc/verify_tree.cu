@@ -3,11 +3,20 @@
 //
 // Only the rows on the way are read.  Which row comes next is known when the one before is done, so a request is a
 // chain of row passes, and the requests are independent: a cluster of 1 to 16 blocks takes a request, every warp a
-// part of each row.  A row at temperature 0 is one pass for the largest entry, kept in shared memory as far as it
-// fits.  Otherwise a second pass sums the entries' masses, integers, so that no sum depends on an order, and the warp
-// whose part holds the drawn share looks for the entry.  The warps meet once per pass and once for the token; a
-// value of each goes to all blocks of the cluster.  While a row's masses are summed, the row behind its largest entry,
-// which is the next one most of the time, comes to the L2 cache.
+// part of each row, which comes to shared memory by asynchronous copies kHeld groups ahead.
+//
+// A row is one pass: for the largest entry, the first of equal ones, and at a temperature for fp32 sums of weights
+// 2^((x - ref) / T log2 e) besides, with ref the largest of the row's first pieces.  The warp whose part holds the drawn
+// share of the sum looks for the entry.  Where the sums' error could reach past the entry's ends (its bound stands at
+// `eps`), and where NaN, +infinity or an overflow is in the way, a second pass decides by the exact masses, integers
+// whose sum depends on no order; so the token is the exact one either way.  The blocks meet once per pass and once for
+// the token: each stores a pair into all blocks of the cluster.  While they do, the row behind the largest
+// entry, which is the next one most of the time, comes to the L2 cache.
+//
+// Bound by that chain: a row of 151936 fp32 entries in 16 blocks takes 2.3 us greedily and 4.5 us drawn, of which the
+// memory's rate would explain 0.1; one greedy tree of 25 nodes 13.4 us in all.  64 drawn trees of up to 64 nodes, 230
+// rows (140 MB), take 65 us, 2.1 TB/s, as long as the deepest path needs with 8 blocks.  (Exact masses in every
+// row: 104 us; with the row read again by the second pass and barriers of the cluster: 234.)
 #include "half_common.cuh"
 #include "mass_common.cuh"
 #include "tree_common.cuh"
@@ -44,6 +53,13 @@ struct Shared {
     uint64_t bar[kTurns];
 };
 constexpr uint32_t kWaitPeer = 0xB01;
+// A test build makes a wait run out: limits of 2 ms, and block DSPARK_LATE_RANK of a cluster 20 ms late at its
+// exchange DSPARK_LATE_AT (expressions in the names of the kernel).
+#ifdef DSPARK_LATE_AT
+constexpr long long kPeerLimitNs = 2000000;
+#else
+constexpr long long kPeerLimitNs = kDefaultTimeoutNs;
+#endif
 constexpr long long kUnderWayNs = 100000;  // far more than a store into another block's shared memory takes
 
 __device__ __forceinline__ void copy_async(void* to, const void* from) {
@@ -131,21 +147,30 @@ __global__ void __launch_bounds__(kThreads, kBlocks) verify_tree_kernel(const __
     // there.  Of any three turns at least one is an exchange of all blocks, which a block answers when all its warps
     // have come to it, so what the turn after those overwrites has been read.
     int turn = 0;
-    auto told = [&](uint32_t bytes) {                      // false where the wait gave up
+    auto told = [&](uint32_t bytes) {                      // false where the wait gave up, in all warps of the block alike
         bool ok = true;
         if constexpr (kCluster) {
             uint64_t* bar = &s.bar[turn % kTurns];
             if (tid == 0) mbar_arrive_expect_tx(bar, bytes);
-            ok = mbar_wait_short(bar, static_cast<uint32_t>(turn / kTurns) & 1u, t.ws, kDefaultTimeoutNs, kWaitPeer);
-            ok = __all_sync(0xFFFFFFFFu, ok);
+            ok = __syncthreads_and(mbar_wait_short(bar, static_cast<uint32_t>(turn / kTurns) & 1u, t.ws, kPeerLimitNs, kWaitPeer)) != 0;
         } else {
             __syncthreads();
         }
         ++turn;
         return ok;
     };
+    auto late = [&] {
+#ifdef DSPARK_LATE_AT
+        if (kCluster && turn == DSPARK_LATE_AT && rank == DSPARK_LATE_RANK) {
+            const long long t0 = global_ns();
+            while (global_ns() - t0 < 20000000) {
+            }
+        }
+#endif
+    };
     // A pair of every block: the largest of the warps' `key`s and the sum of their `sum`s (added by `add`).  Lane r then has those of block r, 0 where there is none.
     auto exchange = [&](u64 key, u64 sum, auto add, Pair& all) {
+        late();
         const int now = turn % kTurns;
         if (lane == 0) s.warp_pair[now][warp] = Pair{key, sum};
         __syncthreads();
@@ -165,6 +190,7 @@ __global__ void __launch_bounds__(kThreads, kBlocks) verify_tree_kernel(const __
     };
     // A value that only one warp of the cluster has (`here`).
     auto hear = [&](bool here, u64 mine, u64& value) {
+        late();
         const int now = turn % kTurns;
         if (kCluster && here && lane < C)
             send(remote(&s.pair[now][0].key, static_cast<uint32_t>(lane)), mine, remote(&s.bar[now], static_cast<uint32_t>(lane)));
@@ -636,9 +662,11 @@ dspark_status launch_verify_tree(const void* target, dspark_dtype dtype, const f
     a.target = target;
     a.temperature = temperature;
     a.u = u;
-    // As many blocks per request as the SMs hold, while a block's part of a row stays worth an exchange.
+    // As many blocks per request as the SMs hold at once, while a block's part of a row stays worth an exchange.  64 requests
+    // of 151936 entries: 8 blocks each 65 us; 16, which then wait for room, 71; 4 take nearly twice as long.  One request of 4000
+    // entries: 6.2 us in one block, 7.3 in two and more; of 8000: 7.3 in two and in eight; of 32000 drawn: 14.6 in eight, 14.5 in 16.
     while ((2 << a.cluster_bits) <= kClusterMost && static_cast<long long>(B) * (2 << a.cluster_bits) <= static_cast<long long>(kBlocks) * dev.sm_count &&
-           V / (2 << a.cluster_bits) >= 4 * kThreads)
+           V / (2 << a.cluster_bits) >= 8 * kThreads)
         ++a.cluster_bits;
     const dspark_status st = clear_header(ws, stream);
     if (st != DSPARK_OK) return st;
