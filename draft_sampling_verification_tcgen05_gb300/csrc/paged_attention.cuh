@@ -45,6 +45,12 @@
 // its loads.  200 blocks of 8 tokens over 9 to 2000 (85 MB, D = 64) take 31 us: a unit of three tiles
 // is bound by its way through the products and the softmax.  One token over 4097 takes 14.5 us, most of
 // it the three kernels' starts and the chain from the plan to the join.
+//
+// kMasked adds what dspark_tree_attention and dspark_window_attention need: a request's tiles between its sinks and its
+// window's beginning are not walked, a row's mask is put together where a tile is not seen as a whole, and a tree's plan kernel
+// finds each node's ancestors.  64 tokens over 4001 to 65536 with a window of 1024 (270 MB): 55 us, 4.9 TB/s; 33 trees of
+// up to 31 nodes, D = 64, with a window of 2048 (67 MB): 36 us, a chain of 16 tiles of one row tile each; 16 trees of up to
+// 64 nodes over 500 to 8000 (209 MB): 57.5 us, 3.6 TB/s; one tree of 25 over 1051: 16.4 us.
 #pragma once
 
 #include "attention_common.cuh"

@@ -6,12 +6,18 @@
 //   warps 0-7, 8-15  softmax and results of one row tile each: two threads per row, 64 of a key tile's tokens each
 //   warp 16          walks the run's segments and loads (TMA) queries, and page by page keys
 //   warp 19          loads the values (with pages of 16 a tile is 16 boxes, whose issue takes 1300 cycles: one warp for both
-//                    loads was slower than the products, 77 us for 16 trees of 64 nodes over 500 to 8000 tokens)
+//                    loads was slower than the products, 77 us instead of 72 for 16 trees of up to 64 nodes over 500 to 8000
+//                    tokens)
 //   warps 17, 18     issue S = Q K^T and O += P V of one row tile each on tcgen05 (M = 128, fp32 in tensor memory; P
 //                    replaces half of S)
 //
 // Maxima, rounding and infinities are handled as in paged_attention.cuh; where a result is not finite, the CTA goes
 // through its run again, once for each row tile, as the values' infinities are taken out for its rows.
+//
+// Bound by the chain scores -> softmax -> product of a key tile, of which the two row tiles hide each other's: 1.75 us for
+// both (the products alone are 0.5), and by a unit's ends, 2.4 us for its results.  Two chunks of 4096 tokens with a window of
+// 1024, 32 on 8 heads of 128 (140 GFLOP): 206 us, 0.68 PFLOP/s counted, the tensor pipe at 40 % of its cycles since the tiles at
+// the windows' ends are computed whole; one row tile at a time 262 us.  16 trees of 64 nodes over 500 to 8000 tokens: 80.7 / 82.9.
 #pragma once
 
 #include "paged_attention.cuh"
