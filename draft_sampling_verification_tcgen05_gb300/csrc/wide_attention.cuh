@@ -539,46 +539,61 @@ wide_attention_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_cons
                 const int rows = min(a.tile_tokens, g.n - first) * a.group;
                 const long long row0 = (static_cast<long long>(g.b) * a.N + first) * a.Hq + g.h * a.group;
                 const long long part_base = static_cast<long long>(2 * blockIdx.x + (g.t0 == 0 ? 1 : 0)) * a.rows_cap + w * a.tile_tokens * a.group;
-                // 16 columns at a time through shared memory, so that the lanes write pieces of a row together.  Short code
-                // counts here: it is run once per unit, and its instructions come from the L2 cache each time.
-                const int pieces = whole ? 2 : 4;                         // of 16 bytes, in 16 columns of a row
+                // Through shared memory, 64 bytes of each row at a time, so that a store's lanes write whole pieces of eight rows.
+                const int at0 = static_cast<int>(lane) >> 2, piece = static_cast<int>(lane) & 3;
+                auto put = [&](int x, uint4 v) { stage[lane * 4 + (x ^ ((lane >> 1) & 3))] = v; };
+                auto of = [&](int at) { return stage[at * 4 + (piece ^ ((at >> 1) & 3))]; };
+                if (whole) {
+                    int to[4];                                            // of this lane's rows of a store, from the tile's first
+#pragma unroll
+                    for (int x = 0; x < 4; ++x) {
+                        const int rr = static_cast<int>(quad) * 32 + at0 + 8 * x, rt = s.token_of[rr];
+                        to[x] = rr < rows ? (rt * a.Hq + (rr - rt * a.group)) * D : -1;
+                    }
+                    T* out = static_cast<T*>(a.out) + row0 * D + part * (D / 2) + piece * 8;
 #pragma unroll 1
-                for (int c = 0; c < D / 2; c += 16) {
-                    uint32_t o[16];
-                    tmem_ld16(tO + c, o);
-                    tmem_wait_ld();
-                    if (c + 16 == D / 2) {
-                        tc_fence_before();
-                        mbar_arrive(&s.o_empty[w]);
-                    }
-                    __syncwarp();                                         // the columns before have been read
+                    for (int c = 0; c < D / 2; c += 32) {
+                        uint32_t o[32];
+                        tmem_ld32(tO + c, o);
+                        tmem_wait_ld32(o);
+                        if (c + 32 == D / 2) {
+                            tc_fence_before();
+                            mbar_arrive(&s.o_empty[w]);
+                        }
+                        __syncwarp();                                     // the columns before have been read
 #pragma unroll
-                    for (int x = 0; x < 16; ++x) {
-                        check[x & 3] = fmaf(__uint_as_float(o[x]), 0.0f, check[x & 3]);
-                        o[x] = __float_as_uint(__uint_as_float(o[x]) * f);
-                    }
-                    if (whole) {
+                        for (int x = 0; x < 32; ++x) {
+                            check[x & 3] = fmaf(__uint_as_float(o[x]), 0.0f, check[x & 3]);
+                            o[x] = __float_as_uint(__uint_as_float(o[x]) * f);
+                        }
 #pragma unroll
-                        for (int x = 0; x < 2; ++x)
-                            stage[(lane * 2 + x) ^ ((lane >> 2) & 1)] = pack8(reinterpret_cast<const float*>(o) + 8 * x, T{});
-                    } else {
+                        for (int x = 0; x < 4; ++x) put(x, pack8(reinterpret_cast<const float*>(o) + 8 * x, T{}));
+                        __syncwarp();
 #pragma unroll
                         for (int x = 0; x < 4; ++x)
-                            stage[lane * 4 + (x ^ ((lane >> 1) & 3))] = make_uint4(o[4 * x], o[4 * x + 1], o[4 * x + 2], o[4 * x + 3]);
+                            if (to[x] >= 0) *reinterpret_cast<uint4*>(out + to[x] + c) = of(at0 + 8 * x);
                     }
-                    __syncwarp();
-                    const int col = part * (D / 2) + c;
+                } else {
+                    float* out = a.part_o + (part_base + quad * 32) * D + part * (D / 2) + piece * 4;
 #pragma unroll 1
-                    for (int x = static_cast<int>(lane); x < 32 * pieces; x += 32) {
-                        const int at = x / pieces, piece = x - at * pieces, rr = static_cast<int>(quad) * 32 + at;
-                        if (rr >= rows) break;
-                        if (whole) {
-                            const int rt = s.token_of[rr];
-                            const long long to_row = row0 + static_cast<long long>(rt) * a.Hq + (rr - rt * a.group);
-                            *reinterpret_cast<uint4*>(static_cast<T*>(a.out) + to_row * D + col + piece * 8) = stage[(at * 2 + piece) ^ ((at >> 2) & 1)];
-                        } else {
-                            *reinterpret_cast<uint4*>(a.part_o + (part_base + rr) * D + col + piece * 4) = stage[at * 4 + (piece ^ ((at >> 1) & 3))];
+                    for (int c = 0; c < D / 2; c += 16) {
+                        uint32_t o[16];
+                        tmem_ld16(tO + c, o);
+                        tmem_wait_ld();
+                        if (c + 16 == D / 2) {
+                            tc_fence_before();
+                            mbar_arrive(&s.o_empty[w]);
                         }
+                        __syncwarp();
+#pragma unroll
+                        for (int x = 0; x < 16; ++x) check[x & 3] = fmaf(__uint_as_float(o[x]), 0.0f, check[x & 3]);
+#pragma unroll
+                        for (int x = 0; x < 4; ++x) put(x, make_uint4(o[4 * x], o[4 * x + 1], o[4 * x + 2], o[4 * x + 3]));
+                        __syncwarp();
+#pragma unroll
+                        for (int x = 0; x < 4; ++x)
+                            if (static_cast<int>(quad) * 32 + at0 + 8 * x < rows)
+                                *reinterpret_cast<uint4*>(out + (at0 + 8 * x) * D + c) = of(at0 + 8 * x);
                     }
                 }
                 if (valid && part == 0) {
