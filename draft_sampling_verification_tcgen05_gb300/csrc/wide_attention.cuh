@@ -81,6 +81,91 @@ inline __device__ __noinline__ uint2 row_bits(const PagedArgs& a, const Segment<
 
 }  // namespace wide
 
+// The results of row tile w of a segment, to `out` or as a partial one, with m2 the rows' maxima and their sums in s.half; use:
+// that of pv_done by the last product.  Returns 1 where a row is not finite, -1 where the wait gave up.  Out of line: it is run
+// once per unit, and its registers would be missing in the loop over the key tiles.
+template <typename T, int D>
+__device__ __noinline__ int tile_results(const PagedArgs& a, wide::Smem<D>& s, const Segment<true>& g, int w, float m2, int use) {
+    const uint32_t warp = warp_id(), lane = lane_id(), quad = warp & 3u;
+    const int part = static_cast<int>(warp >> 2) & 1, row = static_cast<int>(quad * 32u + lane), row_tok = row / a.group;
+    const uint32_t tO = s.tmem_base + ((quad * 32u) << 16) + wide::kColO + w * 128u + part * (D / 2u);
+    const int first = g.rt * a.unit_tokens + w * a.tile_tokens;
+    const bool valid = row < a.tile_tokens * a.group && first + row_tok < g.n;
+    // What does not need O comes before the wait for its last product.
+    const float l = s.half[w][0][row] + s.half[w][1][row];
+    const bool whole = g.t0 == 0 && g.t1 == g.tiles;
+    const float f = whole ? (l != 0.0f ? 1.0f / l : 0.0f) : 1.0f;
+    float check[4] = {l * 0.0f, 0.0f, 0.0f, 0.0f};                        // 0, or NaN
+    uint4* stage = s.stage[warp];
+    const int rows = min(a.tile_tokens, g.n - first) * a.group;
+    const long long row0 = (static_cast<long long>(g.b) * a.N + first) * a.Hq + g.h * a.group;
+    const long long part_base = static_cast<long long>(2 * blockIdx.x + (g.t0 == 0 ? 1 : 0)) * a.rows_cap + w * a.tile_tokens * a.group;
+    if (valid && part == 0) {
+        if (!whole) reinterpret_cast<float2*>(a.part_ml)[part_base + row] = make_float2(m2, l);
+        else if (a.lse) a.lse[row0 + static_cast<long long>(row_tok) * a.Hq + (row - row_tok * a.group)] = lse_of(m2, l);
+    }
+    const int at0 = static_cast<int>(lane) >> 2, piece = static_cast<int>(lane) & 3;
+    int to_row[4];                                            // of this lane's rows of a store, from the tile's first
+#pragma unroll
+    for (int x = 0; x < 4; ++x) {
+        const int rr = static_cast<int>(quad) * 32 + at0 + 8 * x, rt = s.token_of[rr];
+        to_row[x] = rr >= rows ? -1 : whole ? (rt * a.Hq + (rr - rt * a.group)) * D : rr * D;
+    }
+    if (!__all_sync(0xFFFFFFFFu, mbar_wait_short(&s.pv_done[w], static_cast<uint32_t>(use) & 1u, &a.plan->header, a.timeout_ns, wide::kWaitSoftmax)))
+        return -1;
+    tc_fence_after();
+    // Through shared memory, 64 bytes of each row at a time, so that a store's lanes write whole pieces of eight rows.
+    auto put = [&](int x, uint4 v) { stage[lane * 4 + (x ^ ((lane >> 1) & 3))] = v; };
+    auto of = [&](int at) { return stage[at * 4 + (piece ^ ((at >> 1) & 3))]; };
+    if (whole) {
+        T* out = static_cast<T*>(a.out) + row0 * D + part * (D / 2) + piece * 8;
+#pragma unroll 1
+        for (int c = 0; c < D / 2; c += 32) {
+            uint32_t o[32];
+            tmem_ld32(tO + c, o);
+            tmem_wait_ld32(o);
+            if (c + 32 == D / 2) {
+                tc_fence_before();
+                mbar_arrive(&s.o_empty[w]);
+            }
+            __syncwarp();                                     // the columns before have been read
+#pragma unroll
+            for (int x = 0; x < 32; ++x) {
+                check[x & 3] = fmaf(__uint_as_float(o[x]), 0.0f, check[x & 3]);
+                o[x] = __float_as_uint(__uint_as_float(o[x]) * f);
+            }
+#pragma unroll
+            for (int x = 0; x < 4; ++x) put(x, pack8(reinterpret_cast<const float*>(o) + 8 * x, T{}));
+            __syncwarp();
+#pragma unroll
+            for (int x = 0; x < 4; ++x)
+                if (to_row[x] >= 0) *reinterpret_cast<uint4*>(out + to_row[x] + c) = of(at0 + 8 * x);
+        }
+    } else {
+        float* out = a.part_o + part_base * D + part * (D / 2) + piece * 4;
+#pragma unroll 1
+        for (int c = 0; c < D / 2; c += 16) {
+            uint32_t o[16];
+            tmem_ld16(tO + c, o);
+            tmem_wait_ld();
+            if (c + 16 == D / 2) {
+                tc_fence_before();
+                mbar_arrive(&s.o_empty[w]);
+            }
+            __syncwarp();
+#pragma unroll
+            for (int x = 0; x < 16; ++x) check[x & 3] = fmaf(__uint_as_float(o[x]), 0.0f, check[x & 3]);
+#pragma unroll
+            for (int x = 0; x < 4; ++x) put(x, make_uint4(o[4 * x], o[4 * x + 1], o[4 * x + 2], o[4 * x + 3]));
+            __syncwarp();
+#pragma unroll
+            for (int x = 0; x < 4; ++x)
+                if (to_row[x] >= 0) *reinterpret_cast<uint4*>(out + to_row[x] + c) = of(at0 + 8 * x);
+        }
+    }
+    return valid && check[0] + check[1] + check[2] + check[3] != 0.0f ? 1 : 0;
+}
+
 template <typename T, int D>
 __global__ void __launch_bounds__(wide::kThreads, 1)
 wide_attention_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmK,
@@ -369,7 +454,7 @@ wide_attention_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_cons
             auto rows_of_pass = [&](auto later) {
             constexpr bool redo = decltype(later)::value;
             while (true) {
-                ok = named_bar_and(bar_tile, wide::kRowThreads, wait(s.item_full[count % wide::kAhead], count / wide::kAhead, wide::kWaitSoftmax));
+                ok = named_bar_and(bar_tile, wide::kRowThreads, ok && wait(s.item_full[count % wide::kAhead], count / wide::kAhead, wide::kWaitSoftmax));
                 if (!ok) break;
                 const Item& it = s.item[count % wide::kAhead];
                 const int n = it.n[w];
@@ -526,81 +611,13 @@ wide_attention_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_cons
                 kt += max(n, it.n[1 - w]);
 
                 // ---------------- the tile's rows ----------------
-                if (ok) ok = all(wait(s.pv_done[w], i - 1, wide::kWaitSoftmax));
                 s.half[w][part][row] = l;
                 ok = named_bar_and(bar_tile, wide::kRowThreads, ok);      // the warps meet again: give up together
                 if (!ok) break;
-                tc_fence_after();
-                l = s.half[w][0][row] + s.half[w][1][row];
-                const bool whole = g.t0 == 0 && g.t1 == g.tiles;
-                const float f = whole ? (l != 0.0f ? 1.0f / l : 0.0f) : 1.0f;
-                float check[4] = {l * 0.0f, 0.0f, 0.0f, 0.0f};            // 0, or NaN
-                uint4* stage = s.stage[warp];
-                const int rows = min(a.tile_tokens, g.n - first) * a.group;
-                const long long row0 = (static_cast<long long>(g.b) * a.N + first) * a.Hq + g.h * a.group;
-                const long long part_base = static_cast<long long>(2 * blockIdx.x + (g.t0 == 0 ? 1 : 0)) * a.rows_cap + w * a.tile_tokens * a.group;
-                // Through shared memory, 64 bytes of each row at a time, so that a store's lanes write whole pieces of eight rows.
-                const int at0 = static_cast<int>(lane) >> 2, piece = static_cast<int>(lane) & 3;
-                auto put = [&](int x, uint4 v) { stage[lane * 4 + (x ^ ((lane >> 1) & 3))] = v; };
-                auto of = [&](int at) { return stage[at * 4 + (piece ^ ((at >> 1) & 3))]; };
-                if (whole) {
-                    int to[4];                                            // of this lane's rows of a store, from the tile's first
-#pragma unroll
-                    for (int x = 0; x < 4; ++x) {
-                        const int rr = static_cast<int>(quad) * 32 + at0 + 8 * x, rt = s.token_of[rr];
-                        to[x] = rr < rows ? (rt * a.Hq + (rr - rt * a.group)) * D : -1;
-                    }
-                    T* out = static_cast<T*>(a.out) + row0 * D + part * (D / 2) + piece * 8;
-#pragma unroll 1
-                    for (int c = 0; c < D / 2; c += 32) {
-                        uint32_t o[32];
-                        tmem_ld32(tO + c, o);
-                        tmem_wait_ld32(o);
-                        if (c + 32 == D / 2) {
-                            tc_fence_before();
-                            mbar_arrive(&s.o_empty[w]);
-                        }
-                        __syncwarp();                                     // the columns before have been read
-#pragma unroll
-                        for (int x = 0; x < 32; ++x) {
-                            check[x & 3] = fmaf(__uint_as_float(o[x]), 0.0f, check[x & 3]);
-                            o[x] = __float_as_uint(__uint_as_float(o[x]) * f);
-                        }
-#pragma unroll
-                        for (int x = 0; x < 4; ++x) put(x, pack8(reinterpret_cast<const float*>(o) + 8 * x, T{}));
-                        __syncwarp();
-#pragma unroll
-                        for (int x = 0; x < 4; ++x)
-                            if (to[x] >= 0) *reinterpret_cast<uint4*>(out + to[x] + c) = of(at0 + 8 * x);
-                    }
-                } else {
-                    float* out = a.part_o + (part_base + quad * 32) * D + part * (D / 2) + piece * 4;
-#pragma unroll 1
-                    for (int c = 0; c < D / 2; c += 16) {
-                        uint32_t o[16];
-                        tmem_ld16(tO + c, o);
-                        tmem_wait_ld();
-                        if (c + 16 == D / 2) {
-                            tc_fence_before();
-                            mbar_arrive(&s.o_empty[w]);
-                        }
-                        __syncwarp();
-#pragma unroll
-                        for (int x = 0; x < 16; ++x) check[x & 3] = fmaf(__uint_as_float(o[x]), 0.0f, check[x & 3]);
-#pragma unroll
-                        for (int x = 0; x < 4; ++x) put(x, make_uint4(o[4 * x], o[4 * x + 1], o[4 * x + 2], o[4 * x + 3]));
-                        __syncwarp();
-#pragma unroll
-                        for (int x = 0; x < 4; ++x)
-                            if (static_cast<int>(quad) * 32 + at0 + 8 * x < rows)
-                                *reinterpret_cast<uint4*>(out + (at0 + 8 * x) * D + c) = of(at0 + 8 * x);
-                    }
-                }
-                if (valid && part == 0) {
-                    if (!whole) reinterpret_cast<float2*>(a.part_ml)[part_base + row] = make_float2(m2, l);
-                    else if (a.lse) a.lse[(static_cast<long long>(g.b) * a.N + tok) * a.Hq + g.h * a.group + (row - row_tok * a.group)] = lse_of(m2, l);
-                }
-                if (!redo && valid && check[0] + check[1] + check[2] + check[3] != 0.0f) s.again = 1u;
+                const int done = tile_results<T, D>(a, s, g, w, m2, i - 1);
+                ok = done >= 0;
+                if (!ok) continue;                                        // to the vote above
+                if (!redo && done > 0) s.again = 1u;
                 __syncwarp();
                 mbar_arrive(&s.item_empty[count++ % wide::kAhead]);
             }
