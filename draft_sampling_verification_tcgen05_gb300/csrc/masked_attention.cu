@@ -17,13 +17,13 @@ dspark_status launch(PagedArgs& a, int grid, cudaStream_t stream) {
     // requests bring their own lengths and two tiles hold the longest.  Most of them then fill one tile, and a block that has one
     // tile has nothing to do while that is in its softmax; two blocks' worth of single tiles it is then.
     // Measured, wide / one tile at a time, 8 heads of keys, in us:
-    //   lengths given      16 trees of up to 64 nodes, 500 to 8000 keys  71.0 / 57.5     16 of up to 17 of 8 heads each  66.6 / 55.2
-    //                      33 of up to 64, D = 64, a window of 2048      84.0 / 76.5     1 of 64, 1000 keys              23.0 / 19.6
-    //                      4 of up to 64, 20000 to 60000 keys           150.5 / 172.2    64 of up to 64, 100 to 1000     69.0 / 74.2
-    //                      8 of up to 200, 200 to 4000 keys              76.2 / 98.2     (more than two tiles)
-    //   every row used     16 trees of 64 nodes, 500 to 8000 keys        80.7 / 82.9     16 of 17, 8 heads each          72.6 / 80.6
-    //                      4 of 64, 20000 to 60000 keys                 154.0 / 208.3    64 of 64, 100 to 1000           73.7 / 92.1
-    //                      2 chunks of 4096, a window of 1024           206   / 262      1 of 64, 1000 keys              23.1 / 19.6
+    //   lengths given      16 trees of up to 64 nodes, 500 to 8000 keys  70.8 / 57.3     16 of up to 17 of 8 heads each  66.1 / 54.4
+    //                      33 of up to 64, D = 64, a window of 2048      85.4 / 75.9     1 of 64, 1000 keys              22.9 / 19.4
+    //                      4 of up to 64, 20000 to 60000 keys           150.2 / 174.1    64 of up to 64, 100 to 1000     68.4 / 74.5
+    //                      8 of up to 200, 200 to 4000 keys              76.7 / 97.4     2 chunks of up to 4096         142.8 / 175.0
+    //   every row used     16 trees of 64 nodes, 500 to 8000 keys        80.5 / 82.2     16 of 17, 8 heads each          71.9 / 80.1
+    //                      4 of 64, 20000 to 60000 keys                 153.7 / 207.4    64 of 64, 100 to 1000           72.8 / 91.7
+    //                      2 chunks of 4096, a window of 1024           209.8 / 273.5    1 of 64, 1000 keys              22.9 / 19.2
     if (a.N > (a.lengths ? 2 : 1) * a.tile_tokens) return launch_wide<T, D>(a, grid, stream);
     return launch_typed<T, D, true>(a, grid, stream);
 }
