@@ -16,7 +16,7 @@
 //
 // Bound by the chain scores -> softmax -> product of a key tile, of which the two row tiles hide each other's: 1.8 us for
 // both (the products alone are 1.0), and by a unit's ends, about 4 us: the last product, the results, the next unit's first scores.
-// Two chunks of 4096 tokens with a window of 1024, 32 on 8 heads of 128 (140 GFLOP): 196 us, 0.71 PFLOP/s counted, the
+// Two chunks of 4096 tokens with a window of 1024, 32 on 8 heads of 128 (140 GFLOP): 194 us, 0.72 PFLOP/s counted, the
 // tensor pipe at 42 % of its cycles since the tiles at the windows' ends are computed whole; one row tile at a time 262 us.
 // 16 trees of 64 nodes over 500 to 8000 tokens: 80.5 / 82.2.
 #pragma once
@@ -57,6 +57,7 @@ struct Smem {
     float half[2][2][kTile];                                      // by row tile and half of the key tiles: a row's largest score, or sum
     uint8_t token_of[kTile];                                      // of a row tile's rows
     uint32_t masks[2][4];
+    PagedArgs args;                                               // for functions out of line: the kernel's own are slower to read through a reference
     uint32_t again, failed;                                       // further passes are needed / a wait gave up
     uint64_t item_full[kAhead], item_empty[kAhead];
     uint64_t q_full[2], q_empty[2];
@@ -208,6 +209,7 @@ wide_attention_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_cons
         prefetch_tensormap(&tmK);
         prefetch_tensormap(&tmV);
     }
+    if (threadIdx.x == 32) s.args = a;
     if (threadIdx.x < kTile) s.token_of[threadIdx.x] = static_cast<uint8_t>(threadIdx.x / a.group);
     if (warp == kWarpMma) {
         tmem_alloc(&s.tmem_base, wide::kTmemCols);
@@ -480,7 +482,7 @@ wide_attention_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_cons
                     const int j = g.place(g.t0 + t) * kTile;
                     const bool masked = j + kTile > to || (j < from && j + kTile > sinks);
                     uint2 sees = make_uint2(0xFFFFFFFFu, 0xFFFFFFFFu);
-                    if (masked) sees = row_bits(a, g, tok, valid, j + part * 64);
+                    if (masked) sees = row_bits(s.args, g, tok, valid, j + part * 64);
                     bool go = wait(s.s_full[w], i, wide::kWaitSoftmax);
                     if (redo) go = named_bar_and(bar_tile, wide::kRowThreads, go);  // these meet in barriers below
                     go = all(go);
@@ -593,7 +595,7 @@ wide_attention_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_cons
                             SeenBits<128> whole;
                             whole.all();
                             if (masked) {
-                                const uint2 other = row_bits(a, g, tok, valid, j + 64);
+                                const uint2 other = row_bits(s.args, g, tok, valid, j + 64);
                                 whole.word[0] = sees.x;
                                 whole.word[1] = sees.y;
                                 whole.word[2] = other.x;
@@ -615,7 +617,7 @@ wide_attention_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_cons
                 s.half[w][part][row] = l;
                 ok = named_bar_and(bar_tile, wide::kRowThreads, ok);      // the warps meet again: give up together
                 if (!ok) break;
-                const int done = tile_results<T, D>(a, s, g, w, m2, i - 1);
+                const int done = tile_results<T, D>(s.args, s, g, w, m2, i - 1);
                 ok = done >= 0;
                 if (!ok) continue;                                        // to the vote above
                 if (!redo && done > 0) s.again = 1u;
