@@ -17,7 +17,7 @@
 // Bound by the chain scores -> softmax -> product of a key tile, of which the two row tiles hide each other's: 1.8 us for
 // both (the products alone are 1.0), and by a unit's ends, about 4 us: the last product, the results, the next unit's first scores.
 // Two chunks of 4096 tokens with a window of 1024, 32 on 8 heads of 128 (140 GFLOP): 194 us, 0.72 PFLOP/s counted, the
-// tensor pipe at 42 % of its cycles since the tiles at the windows' ends are computed whole; one row tile at a time 262 us.
+// tensor pipe at 43 % of its cycles since the tiles at the windows' ends are computed whole; one row tile at a time 262 us.
 // 16 trees of 64 nodes over 500 to 8000 tokens: 80.5 / 82.2.
 #pragma once
 
