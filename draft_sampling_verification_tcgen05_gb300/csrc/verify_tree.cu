@@ -384,24 +384,26 @@ __global__ void __launch_bounds__(kThreads, kBlocks) verify_tree_kernel(const __
                 u = u >= 1.0f ? 0x1.fffffep-1f : 0.0f;
             }
             const uint32_t share = static_cast<uint32_t>(u * 0x1p24f);        // exact: a power of two, then the floor
-            // Which of the lanes' values q, end to end, holds `rest`; leaves in `rest` what is behind its beginning (-1: none).
-            auto locate = [&](auto q, auto& rest) {
+            // Which of the first `count` lanes' values q, end to end, holds `rest`; leaves in `rest` what is behind its beginning
+            // (-1: none).  The lanes behind them hold 0, but fp32 sums of theirs are added in another order and may be larger than
+            // the last value's: they are not asked.
+            auto locate = [&](auto q, int count, auto& rest) {
                 auto in = q;
 #pragma unroll
                 for (int d = 1; d < 32; d <<= 1) {
                     const auto o = __shfl_up_sync(0xFFFFFFFFu, in, d);
                     if (lane >= d) in += o;
                 }
-                const int at = __ffs(__ballot_sync(0xFFFFFFFFu, in > rest)) - 1;
+                const int at = __ffs(__ballot_sync(0xFFFFFFFFu, lane < count && in > rest)) - 1;
                 if (at > 0) rest -= __shfl_sync(0xFFFFFFFFu, in, at - 1);
                 return at;
             };
             // Whether this warp holds `rest`, given the blocks' values and the warps' of this block; exactly one does (where
             // a rounding leaves it behind all, the last).
             auto owns = [&](auto of_blocks, auto of_warps, auto& rest) {
-                const int r = locate(of_blocks, rest);
+                const int r = locate(of_blocks, C, rest);
                 if ((r < 0 ? C - 1 : r) != rank) return false;
-                const int w = locate(of_warps, rest);
+                const int w = locate(of_warps, kWarps, rest);
                 return (w < 0 ? kWarps - 1 : w) == warp;
             };
 
@@ -422,7 +424,7 @@ __global__ void __launch_bounds__(kThreads, kBlocks) verify_tree_kernel(const __
                 const bool here = owns(block_sum, lane < kWarps ? __uint_as_float(static_cast<uint32_t>(s.warp_pair[last][lane].sum)) : 0.0f, rest);
                 if (here) {
                     const float slack = eps * total;
-                    const int l = locate(group_sum, rest);
+                    const int l = locate(group_sum, 32, rest);                // a lane without groups has no rounds either
                     for (int x0 = l * per * kGroup; l >= 0 && x0 < min((l + 1) * per * kGroup, rounds); x0 += kGroup) {
                         float part[kGroup];
 #pragma unroll
@@ -511,13 +513,13 @@ __global__ void __launch_bounds__(kThreads, kBlocks) verify_tree_kernel(const __
                 u64 rest = share_of(warp_sum_u64(all.sum), share);
                 const bool here = owns(all.sum, lane < kWarps ? s.warp_pair[last][lane].sum : 0, rest);
                 if (here) {
-                    for (int x = locate(kept, rest) * per * kGroup; x < rounds; ++x) {
+                    for (int x = locate(kept, 32, rest) * per * kGroup; x < rounds; ++x) {
                         float w[kPer];
                         u64 sum = 0;
                         weights(piece(x), w);
 #pragma unroll
                         for (int e = 0; e < kPer; ++e) sum += mass_of(w[e]);
-                        const int l = locate(sum, rest);
+                        const int l = locate(sum, 32, rest);
                         if (l < 0) {
                             rest -= warp_sum_u64(sum);
                             continue;
