@@ -54,7 +54,7 @@ struct Smem {
     alignas(1024) uint8_t v[kSlots][kTileBytes];
     alignas(1024) uint4 stage[16][128];                           // 32 columns of a warp's rows; a row of values in a later pass
     Item item[kAhead];
-    float half[2][2][kTile];                                      // by row tile and half of the key tiles: a row's largest score, or sum
+    float half[2][2][kTile];                                      // by row tile and half of the key tiles: a row's largest score, at last its sum
     uint8_t token_of[kTile];                                      // of a row tile's rows
     uint32_t masks[2][4];
     PagedArgs args;                                               // for functions out of line: the kernel's own are slower to read through a reference
@@ -523,6 +523,13 @@ wide_attention_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_cons
                         if (t > 0) go = go && all(wait(s.pv_done[w], i - 1, wide::kWaitSoftmax));
                         ok = named_bar_and(bar_rows, 64, go);
                         if (!ok && !redo) break;                          // else at the vote below
+#ifdef DSPARK_LATE_PART                                                   // a test build: this half of the rows' threads reads late
+                        if (part == (DSPARK_LATE_PART)) {
+                            const long long t0 = global_ns();
+                            while (global_ns() - t0 < 50000) {
+                            }
+                        }
+#endif
                         mt = fmaxf(mt, s.half[w][1 - part][row]);
                         if (t == 0) {
                             m2 = mt;
@@ -614,7 +621,9 @@ wide_attention_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_cons
                 kt += max(n, it.n[1 - w]);
 
                 // ---------------- the tile's rows ----------------
-                s.half[w][part][row] = l;
+                // The sum goes where this thread has read the other's maximum (the two sums are added, either way round):
+                // this thread's own maximum may not have been read yet.
+                s.half[w][1 - part][row] = l;
                 ok = named_bar_and(bar_tile, wide::kRowThreads, ok);      // the warps meet again: give up together
                 if (!ok) break;
                 const int done = tile_results<T, D>(s.args, s, g, w, m2, i - 1);
