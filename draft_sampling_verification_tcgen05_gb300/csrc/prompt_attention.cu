@@ -181,7 +181,7 @@ struct PromptSmem {
     alignas(1024) uint8_t v[kSlots][kTileBytes];
     alignas(1024) uint4 stage[16][128];                           // 32 columns of a warp's rows; a row of values where a tile is done again
     Item item[kAhead];
-    float half[2][2][kTile];                                      // by query tile and half of the key tiles: a row's largest score, or sum
+    float half[2][2][kTile];                                      // by query tile and half of the key tiles: a row's largest score, at last its sum
     uint32_t masks[2][4];
     int redo[2][kRedo];                                           // items to be done again, by query tile
     unsigned int redo_count[2];                                   // entries written so far
@@ -518,6 +518,13 @@ prompt_attention_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_co
                     if (t > 0) go = go && all(wait(s.pv_done[w], i - 1, kWaitSoftmax));
                     ok = named_bar_and(bar_rows, 64, go);
                     if (!ok && !redo) break;                              // else at the vote below
+#ifdef DSPARK_LATE_PART                                                   // a test build: this half of the rows' threads reads late
+                    if (part == (DSPARK_LATE_PART)) {
+                        const long long t0 = global_ns();
+                        while (global_ns() - t0 < 50000) {
+                        }
+                    }
+#endif
                     mt = fmaxf(mt, s.half[w][1 - part][row]);
                     if (t == 0) {
                         m2 = mt;
@@ -609,7 +616,9 @@ prompt_attention_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_co
 
             // ---------------- the query tile's rows ----------------
             if (ok) ok = all(wait(s.pv_done[w], i - 1, kWaitSoftmax));
-            s.half[w][part][row] = l;
+            // The sum goes where this thread has read the other's maximum (the two sums are added, either way round): this
+            // thread's own maximum may not have been read yet.
+            s.half[w][1 - part][row] = l;
             ok = named_bar_and(bar_tile, kRowThreads, ok);                // the warps meet again: give up together
             if (!ok) break;
             {

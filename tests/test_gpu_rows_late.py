@@ -35,6 +35,23 @@ def windows(ds):
     return got
 
 
+def prompts(ds):
+    """Prompts of a single key tile, and longer ones whose scores grow to the last."""
+    import torch
+    from tests.test_gpu_prompt_attention import _check, _cu, _inputs
+    got = []
+    for dtype in ("bf16", "f16"):
+        for D in (64, 128):
+            for lens, grow in (([100, 1, 128, 77, 64, 65, 128, 33], False), ([300, 129, 513], True)):
+                q, k, v = _inputs(sum(lens), 16, 4, D, dtype, D)
+                if grow:
+                    ramp = torch.cat([torch.linspace(0.01, 4.0, n, device="cuda") for n in lens])[:, None, None]
+                    k = (ramp * torch.cat([q[a:a + 1, ::4].expand(n, -1, -1) for a, n in zip(_cu(lens), lens)]).float()).to(q.dtype)
+                for causal in (True, False):
+                    got += _check(ds, q, k, v, _cu(lens), dtype, causal, rows=60)
+    return got
+
+
 def _late_library(tmp_path, source):
     from draft_sampling_verification_tcgen05_gb300 import _build
     _build.build()
@@ -49,7 +66,7 @@ def _late_library(tmp_path, source):
     return lib
 
 
-@pytest.mark.parametrize("source,cases", [("masked_attention.cu", "windows")])
+@pytest.mark.parametrize("source,cases", [("masked_attention.cu", "windows"), ("prompt_attention.cu", "prompts")])
 def test_a_half_that_reads_late(cuda_lib, tmp_path, source, cases):
     import torch
     lib, out = _late_library(tmp_path, source), str(tmp_path / "late.pt")
