@@ -612,6 +612,11 @@ static dspark_status check_caches(const char* op, const void* k_cache, const voi
     return DSPARK_OK;
 }
 
+static bool overlap(const void* p, long long p_bytes, const void* q, long long q_bytes) {
+    const uintptr_t a = reinterpret_cast<uintptr_t>(p), b = reinterpret_cast<uintptr_t>(q);
+    return p && q && a < b + static_cast<uintptr_t>(q_bytes) && b < a + static_cast<uintptr_t>(p_bytes);
+}
+
 dspark_status dspark_kv_compact(void* k_cache, void* v_cache, int layers, long long layer_stride, const int32_t* block_table,
                                 int max_pages, const int32_t* kv_len, const int32_t* lengths, const int32_t* path,
                                 const int32_t* num_accepted, int B, int N, int Hkv, int D, int num_pages, int page,
@@ -620,10 +625,16 @@ dspark_status dspark_kv_compact(void* k_cache, void* v_cache, int layers, long l
     const dspark_status st = check_caches("kv_compact", k_cache, v_cache, layers, layer_stride, Hkv, D, num_pages, page);
     if (st != DSPARK_OK) return st;
     DSPARK_REQUIRE(block_table && kv_len && path && num_accepted && kv_len_out, "kv_compact: null pointer");
-    DSPARK_REQUIRE(kv_len_out != kv_len, "kv_compact: kv_len_out must not be kv_len");
     DSPARK_REQUIRE(B >= 1 && N >= 1 && N <= kTreeMost, "kv_compact: bad sizes (B=%d N=%d)", B, N);
     DSPARK_REQUIRE(max_pages >= 1 && static_cast<long long>(max_pages) * page <= (1ll << 30), "kv_compact: bad table (%d pages of %d)",
                    max_pages, page);
+    // several blocks read a request's values, and one of them writes its new length, in no order
+    const long long per_request = 4ll * B;
+    DSPARK_REQUIRE(!overlap(kv_len_out, per_request, kv_len, per_request) && !overlap(kv_len_out, per_request, lengths, per_request) &&
+                       !overlap(kv_len_out, per_request, num_accepted, per_request) &&
+                       !overlap(kv_len_out, per_request, path, per_request * N) &&
+                       !overlap(kv_len_out, per_request, block_table, per_request * max_pages),
+                   "kv_compact: kv_len_out must not overlap an input");
     if (bad_ws(workspace, ws_bytes, sizeof(WsHeader))) return DSPARK_ERR_INVALID_ARG;
     DeviceInfo dev;
     if (!current_device(&dev)) return DSPARK_ERR_UNSUPPORTED;

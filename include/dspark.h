@@ -799,7 +799,7 @@ DSPARK_API dspark_status dspark_verify_tree_tokens(const int32_t* target_tokens,
  *                pages that hold their trees
  *   kv_len       [B] int32, device;   lengths [B] int32 in [0, N], device, or NULL (= N)
  *   path         [B, N] int32, device;  num_accepted [B] int32 in [0, n), device (0 where n is 0)
- *   kv_len_out   [B] int32 output; not kv_len itself
+ *   kv_len_out   [B] int32 output; overlaps none of the int32 inputs
  * Requirements: B >= 1, 1 <= N <= 256, layers, Hkv, num_pages, max_pages, page >= 1, D a multiple of 8
  * up to 512, num_pages * page < 2^31, max_pages * page <= 2^30, layers * Hkv * D < 2^29, layer_stride a
  * multiple of 8 and (with more than one layer) at least num_pages * Hkv * page * D; the caches 16-byte aligned.
