@@ -10,7 +10,8 @@ namespace dspark {
 
 struct TreeArgs {
     const int32_t *parents, *draft_tokens, *lengths;
-    int B, N, V;                           // V: tokens are below it
+    int B, N, V;                           // V: entries of a row (0: there are none)
+    int last;                              // the largest token
     int32_t *out_tokens, *num_accepted, *path;
     WsHeader* ws;
 };
@@ -31,7 +32,7 @@ __device__ __forceinline__ void tree_node(const TreeArgs& a, int b, int i, int& 
         bad = true;
         parent = -1;
     }
-    if (i > 0 && (token < 0 || token >= a.V)) {
+    if (i > 0 && (token < 0 || token > a.last)) {
         bad = true;
         parent = -1;
     }

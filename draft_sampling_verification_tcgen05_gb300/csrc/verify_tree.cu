@@ -660,7 +660,7 @@ dspark_status launch_verify_tree(const void* target, dspark_dtype dtype, const f
                                  int V, int32_t* out_tokens, int32_t* num_accepted, int32_t* path, void* ws,
                                  cudaStream_t stream, const DeviceInfo& dev) {
     VerifyArgs a{};
-    a.tree = TreeArgs{parents, draft_tokens, lengths, B, N, V, out_tokens, num_accepted, path, static_cast<WsHeader*>(ws)};
+    a.tree = TreeArgs{parents, draft_tokens, lengths, B, N, V, V - 1, out_tokens, num_accepted, path, static_cast<WsHeader*>(ws)};
     a.target = target;
     a.temperature = temperature;
     a.u = u;
@@ -678,7 +678,7 @@ dspark_status launch_verify_tree(const void* target, dspark_dtype dtype, const f
 dspark_status launch_verify_tree_tokens(const int32_t* target_tokens, const int32_t* parents, const int32_t* draft_tokens,
                                         const int32_t* lengths, int B, int N, int32_t* out_tokens, int32_t* num_accepted,
                                         int32_t* path, void* ws, cudaStream_t stream) {
-    const TreeArgs t{parents, draft_tokens, lengths, B, N, INT32_MAX, out_tokens, num_accepted, path, static_cast<WsHeader*>(ws)};
+    const TreeArgs t{parents, draft_tokens, lengths, B, N, 0, INT32_MAX, out_tokens, num_accepted, path, static_cast<WsHeader*>(ws)};
     const dspark_status st = clear_header(ws, stream);
     if (st != DSPARK_OK) return st;
     const cudaError_t e = launch_dependent(walk_tree_kernel, dim3((B + kWalkWarps - 1) / kWalkWarps), dim3(32 * kWalkWarps), 0,
