@@ -14,8 +14,8 @@
 // entry, which is the next one most of the time, comes to the L2 cache.
 //
 // Bound by that chain: a row of 151936 fp32 entries in 16 blocks takes 2.3 us greedily and 4.5 us drawn, of which the
-// memory's rate would explain 0.1; one greedy tree of 25 nodes 13.4 us in all.  64 drawn trees of up to 64 nodes, 230
-// rows (140 MB), take 65 us, 2.1 TB/s, as long as the deepest path needs with 8 blocks.  (Exact masses in every
+// memory's rate would explain 0.1; one greedy tree of 25 nodes 13.5 us in all.  64 drawn trees of up to 64 nodes, 230
+// rows (140 MB), take 66 us, 2.1 TB/s, as long as the deepest path needs with 8 blocks.  (Exact masses in every
 // row: 104 us; with the row read again by the second pass and barriers of the cluster: 234.)
 #include "half_common.cuh"
 #include "mass_common.cuh"
@@ -386,7 +386,7 @@ __global__ void __launch_bounds__(kThreads, kBlocks) verify_tree_kernel(const __
             const uint32_t share = static_cast<uint32_t>(u * 0x1p24f);        // exact: a power of two, then the floor
             // Which of the first `count` lanes' values q, end to end, holds `rest`; leaves in `rest` what is behind its beginning
             // (-1: none).  The lanes behind them hold 0, but fp32 sums of theirs are added in another order and may be larger than
-            // the last value's: they are not asked.
+            // the last value's: their votes do not count.
             auto locate = [&](auto q, int count, auto& rest) {
                 auto in = q;
 #pragma unroll
@@ -394,7 +394,7 @@ __global__ void __launch_bounds__(kThreads, kBlocks) verify_tree_kernel(const __
                     const auto o = __shfl_up_sync(0xFFFFFFFFu, in, d);
                     if (lane >= d) in += o;
                 }
-                const int at = __ffs(__ballot_sync(0xFFFFFFFFu, lane < count && in > rest)) - 1;
+                const int at = __ffs(__ballot_sync(0xFFFFFFFFu, in > rest) & (0xFFFFFFFFu >> (32 - count))) - 1;
                 if (at > 0) rest -= __shfl_sync(0xFFFFFFFFu, in, at - 1);
                 return at;
             };
@@ -665,8 +665,9 @@ dspark_status launch_verify_tree(const void* target, dspark_dtype dtype, const f
     a.temperature = temperature;
     a.u = u;
     // As many blocks per request as the SMs hold at once, while a block's part of a row stays worth an exchange.  64 requests
-    // of 151936 entries: 8 blocks each 65 us; 16, which then wait for room, 71; 4 take nearly twice as long.  One request of 4000
-    // entries: 6.2 us in one block, 7.3 in two and more; of 8000: 7.3 in two and in eight; of 32000 drawn: 14.6 in eight, 14.5 in 16.
+    // of 151936 entries: 8 blocks each 66 us; 16, which then wait for room, 70; 4 take 82.  One request with one row to draw from:
+    // of 4000 entries 5.8 us in one block, 6.7 in two; of 8000, where two are taken, 6.5 and 7.3; of 32000 9.4, 8.7 in two,
+    // 7.5 in four, 7.2 in eight (which are taken), 7.1 in 16.
     while ((2 << a.cluster_bits) <= kClusterMost && static_cast<long long>(B) * (2 << a.cluster_bits) <= static_cast<long long>(kBlocks) * dev.sm_count &&
            V / (2 << a.cluster_bits) >= 8 * kThreads)
         ++a.cluster_bits;
