@@ -826,7 +826,7 @@ def dspark_kv_compact(k_cache, v_cache, block_table, kv_len, path, num_accepted,
                       stream=None):
     """Moves the keys and values of each tree's accepted path (dspark_verify_tree's path and num_accepted) behind the
     tokens before the tree, in place, in all layers of the caches ([num_pages, Hkv, page_size, D] or [layers, ...]);
-    returns kv_len_out [B] int32, the cached tokens afterwards."""
+    returns kv_len_out [B] int32, the cached tokens afterwards; it may share no memory with the int32 inputs."""
     torch = _torch()
     i32 = (torch.int32,)
     layers, stride, num_pages, Hkv, page, D = _caches(k_cache, v_cache)

@@ -15,15 +15,19 @@ template <typename T, int D>
 dspark_status launch(PagedArgs& a, int grid, cudaStream_t stream) {
     // More rows than a tile holds: two tiles against one stream of keys and values (wide_attention.cuh), except where
     // requests bring their own lengths and two tiles hold the longest.  Most of them then fill one tile, and a block that has one
-    // tile has nothing to do while that is in its softmax; two blocks' worth of single tiles it is then.
-    // Measured, wide / one tile at a time, 8 heads of keys, in us:
-    //   lengths given      16 trees of up to 64 nodes, 500 to 8000 keys  70.8 / 57.3     16 of up to 17 of 8 heads each  66.1 / 54.4
-    //                      33 of up to 64, D = 64, a window of 2048      85.4 / 75.9     1 of 64, 1000 keys              22.9 / 19.4
-    //                      4 of up to 64, 20000 to 60000 keys           150.2 / 174.1    64 of up to 64, 100 to 1000     68.4 / 74.5
-    //                      8 of up to 200, 200 to 4000 keys              76.7 / 97.4     2 chunks of up to 4096         142.8 / 175.0
-    //   every row used     16 trees of 64 nodes, 500 to 8000 keys        80.5 / 82.2     16 of 17, 8 heads each          71.9 / 80.1
-    //                      4 of 64, 20000 to 60000 keys                 153.7 / 207.4    64 of 64, 100 to 1000           72.8 / 91.7
-    //                      2 chunks of 4096, a window of 1024           209.8 / 273.5    1 of 64, 1000 keys              22.9 / 19.2
+    // tile has nothing to do while that is in its softmax; two blocks' worth of single tiles it is then.  The host knows neither
+    // how many rows the requests use nor how long their contexts are, so this is a guess from the call's shape; where the other
+    // side was the faster one (marked), it costs 3 us, 5 % and 17 %.
+    // Measured, the kernels of a call, wide / one tile at a time, 8 heads of keys, four (or eight) of queries to each, bf16, in us:
+    //   lengths given      16 trees of up to 64 nodes, 500 to 8000 keys   65.7 / 57.0     16 of up to 17 of 8 heads each  55.8 / 45.7
+    //                      33 of up to 64, D = 64, a window of 2048       79.5 / 74.9     1 of 64, 1000 keys              22.2 / 19.3
+    //                      4 of up to 64, 20000 to 60000 keys (marked)   138.4 / 146.0    64 of up to 64, 100 to 1000
+    //                                                                                     keys (marked)                   64.8 / 75.6
+    //                      8 of up to 200, 200 to 4000 keys               45.8 / 45.1     2 chunks of up to 4096,
+    //                                                                                     a window of 1024               140.2 / 185.9
+    //   every row used     16 trees of 64 nodes, 500 to 8000 keys         72.0 / 75.8     16 of 17, 8 heads each          64.4 / 72.5
+    //                      4 of 64, 20000 to 60000 keys                  147.0 / 184.0    64 of 64, 100 to 1000           69.4 / 92.9
+    //                      2 chunks of 4096, a window of 1024            185.9 / 256.1    1 of 64, 1000 keys (marked)     22.5 / 19.6
     if (a.N > (a.lengths ? 2 : 1) * a.tile_tokens) return launch_wide<T, D>(a, grid, stream);
     return launch_typed<T, D, true>(a, grid, stream);
 }

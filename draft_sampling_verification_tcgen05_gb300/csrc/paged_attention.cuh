@@ -50,7 +50,7 @@
 // window's beginning are not walked, a row's mask is put together where a tile is not seen as a whole, and a tree's plan kernel
 // finds each node's ancestors.  64 tokens over 4001 to 65536 with a window of 1024 (270 MB): 55 us, 4.9 TB/s; 33 trees of
 // up to 31 nodes, D = 64, with a window of 2048 (67 MB): 36 us, a chain of 16 tiles of one row tile each; 16 trees of up to
-// 64 nodes over 500 to 8000 (209 MB): 57.5 us, 3.6 TB/s; one tree of 25 over 1051: 16.4 us.
+// 64 nodes over 500 to 8000 (209 MB): 57 us, 3.7 TB/s; one tree of 25 over 1051: 16.4 us.
 #pragma once
 
 #include "attention_common.cuh"

@@ -6,8 +6,7 @@
 //   warps 0-7, 8-15  softmax and results of one row tile each: two threads per row, 64 of a key tile's tokens each
 //   warp 16          walks the run's segments and loads (TMA) queries, and page by page keys
 //   warp 19          loads the values (with pages of 16 a tile is 16 boxes, whose issue takes 1300 cycles: one warp for both
-//                    loads was slower than the products, 77 us instead of 72 for 16 trees of up to 64 nodes over 500 to 8000
-//                    tokens)
+//                    loads was slower than the products, by 7 % for 16 trees of up to 64 nodes over 500 to 8000 tokens)
 //   warps 17, 18     issue S = Q K^T and O += P V of one row tile each on tcgen05 (M = 128, fp32 in tensor memory; P
 //                    replaces half of S)
 //
@@ -16,9 +15,10 @@
 //
 // Bound by the chain scores -> softmax -> product of a key tile, of which the two row tiles hide each other's: 1.8 us for
 // both (the products alone are 1.0), and by a unit's ends, about 4 us: the last product, the results, the next unit's first scores.
-// Two chunks of 4096 tokens with a window of 1024, 32 on 8 heads of 128 (140 GFLOP): 194 us, 0.72 PFLOP/s counted, the
-// tensor pipe at 43 % of its cycles since the tiles at the windows' ends are computed whole; one row tile at a time 262 us.
-// 16 trees of 64 nodes over 500 to 8000 tokens: 80.5 / 82.2.
+// Two chunks of 4096 tokens with a window of 1024, 32 on 8 heads of 128 (140 GFLOP): 193 us, 0.72 PFLOP/s counted, the
+// tensor pipe at 43 % of its cycles since the tiles at the windows' ends are computed whole; 186 where the output's memory
+// is one that the call before has written too, and then 256 with one row tile at a time.  16 trees of 64 nodes over 500 to 8000
+// tokens: 72, and 76 with one row tile at a time.  More sizes of both are in masked_attention.cu.
 #pragma once
 
 #include "paged_attention.cuh"

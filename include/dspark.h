@@ -691,7 +691,9 @@ DSPARK_API dspark_status dspark_sample(const void* logits, dspark_dtype dtype, c
  * values that a row does not see are dspark_paged_attention's, as are all arguments but
  *   window       >= 1
  *   sinks        >= 0
- * and as are the requirements and the device-side checks.  Entries of block_table for tiles of
+ * and as are the requirements and the device-side checks.  Which kernel runs depends on the sizes and
+ * on whether lengths is NULL: lengths that are all N give the same rows as NULL but may round them
+ * otherwise, within the same bound.  Entries of block_table for tiles of
  * min(page, 128) tokens that no row of a request sees are not used and may be anything.
  * workspace: >= dspark_workspace_size(DSPARK_OP_WINDOW_ATTENTION, B, N, Hq, D).
  */
@@ -722,7 +724,7 @@ DSPARK_API dspark_status dspark_window_attention(const void* q, const void* k_ca
  * Requirements: dspark_paged_attention's, and N <= 256.
  * Device-side: kv_len[b] below n sets INPUT_RANGE and the request's rows are as rows that see nothing;
  * a parent out of its range sets INPUT_RANGE and is read as -1.  With a window, entries of block_table
- * as for dspark_window_attention.
+ * as for dspark_window_attention; lengths and rounding as there.
  * workspace: >= dspark_workspace_size(DSPARK_OP_TREE_ATTENTION, B, N, Hq, D).
  */
 DSPARK_API dspark_status dspark_tree_attention(const void* q, const void* k_cache, const void* v_cache,
